@@ -79,6 +79,7 @@ extern "C" {
 #define MBT_DTYPE_BF16   0u
 #define MBT_DTYPE_E4M3   1u
 #define MBT_DTYPE_F32    2u
+#define MBT_DTYPE_E2M1   3u   /* KV caches of the 4-bit entry points (mbt_ops.h) only */
 
 enum mbt_tensor_kind {
   MBT_T_EMBED = 0, MBT_T_G_ATTN = 1, MBT_T_W_QKV = 2, MBT_T_S_QKV = 3,

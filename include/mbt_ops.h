@@ -177,6 +177,90 @@ int op_paged_attention_noalloc(int B, const float* q, int nq, int nkv, int d, co
 /* op_paged_attention_noalloc_limit: MBT_NOALLOC_SCRATCH_BYTES, as built. */
 size_t op_paged_attention_noalloc_limit(void);
 
+/* ---- 4-bit paged KV cache and prompt attention --------------------------- *
+ * A third cache format beside BF16 and e4m3 (MBT_DTYPE_E2M1), for 0.28 of the
+ * BF16 bytes: value = e2m1(code) * e4m3(scale) * g, one 4-bit e2m1 code per
+ * value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), one e4m3 scale per 16
+ * neighbouring channels of a token's head, and the fp32 scale g of the K or V
+ * tensor (k_scale, v_scale). A pool is [num_blocks + 1][nkv][unit]; the unit
+ * of a (block, KV head) is 9 d bytes: the codes of its 16 tokens [16][d / 2]
+ * (channel 2j in the low half of byte j), then their scales [16][d / 16]. K and
+ * V have a pool each. ("Kernel Fusion for Large-Scale LLM Inference", section
+ * 11, "FP8 weights and KV cache": a narrow paged cache; the pages stop at 8
+ * bits.)
+ * Of these entry points, all take any 16-byte aligned pools, head sizes 64 and
+ * 128; the attention ones up to 16 query heads per KV head. Scales are positive
+ * and finite. They keep nothing between calls, so calls on several streams and
+ * captured graphs that run at the same time do not disturb one another as long
+ * as their outputs differ. */
+
+/* op_kv_unit_bytes: bytes of one (block, KV head) of a K or V pool for a head
+ * size and cache format (MBT_DTYPE_BF16, _E4M3 or _E2M1); 0 for any other. */
+size_t op_kv_unit_bytes(int d, int kv_dtype);
+
+/* op_rope_table: the table op_rope_kv_write_fp4 reads: [max_pos][d / 2] pairs
+ * (cos, sin) of the angle p * theta^(-2i/d), evaluated in double precision and
+ * rounded to fp32 (device memory). Set-up: computes on the host and
+ * synchronises `stream`; keep the table for all calls. */
+int op_rope_table(int max_pos, int d, float theta, float* table, void* stream);
+
+/* op_rope_kv_write_fp4: op_rope_kv_write for the 4-bit cache, n rows of any
+ * sequences: rotate the q and k heads of row i of qkv [n][ld_qkv] (fp32; q
+ * heads, then k heads, then v heads; ld_qkv a multiple of 4) at positions[i],
+ * write the rotated q to q_out [n][nq][d] fp32, and store k and v at block
+ * bt[row_seq[i]][p / 16], slot p % 16. row_seq NULL: row i is sequence i (nseq
+ * >= n). bt [nseq][bt_stride]. Over each 16 channels
+ *   scale = e4m3(max |x| / (6 g)),  code = e2m1(x / (scale g)),
+ * to nearest (ties to even) and saturating, decided for the exact x (the
+ * rotation of the fp32 inputs by the fp32 table). A group with a NaN reads as
+ * NaN; an infinity saturates its group (its finite values are then small
+ * beside the scale). A row whose position is outside [0, max_pos) sets
+ * MBT_DEV_POS_RANGE, one whose sequence or block id is out of range
+ * MBT_DEV_BLOCK_RANGE; neither is stored (its q_out row is rotated at position
+ * 0 in the first case). Padding rows name block num_blocks, the null block.
+ * Rows of one call that name the same slot leave its contents unspecified (the
+ * null block's among them); every other byte of the pools stays as it was. */
+int op_rope_kv_write_fp4(int n, const float* qkv, int ld_qkv, int nq, int nkv, int d, const int32_t* positions,
+                         const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride, const float* rope,
+                         int max_pos, void* kpool, void* vpool, int num_blocks, float k_scale, float v_scale,
+                         float* q_out, uint32_t* err, void* stream);
+
+/* op_kv_read_fp4: the values the cache holds for n (sequence, position) rows:
+ * k_out, v_out [n][nkv][d] fp32. row_seq, nseq and bt as above. A row whose
+ * position or sequence is outside the table (MBT_DEV_POS_RANGE) or whose block
+ * id is out of range (MBT_DEV_BLOCK_RANGE) reads as zeros. */
+int op_kv_read_fp4(int n, const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
+                   int nkv, int d, const void* kpool, const void* vpool, int num_blocks, float k_scale, float v_scale,
+                   float* k_out, float* v_out, uint32_t* err, void* stream);
+
+/* op_paged_attention_fp4: op_paged_attention over the 4-bit cache. q [B][nq][d]
+ * fp32, out [B][nq * d] fp32, seq_lens[b] tokens of bt [B][bt_stride]. A row
+ * with seq_len < 1 or beyond its table sets MBT_DEV_SEQLEN_RANGE and is 0; an
+ * out-of-range block id sets MBT_DEV_BLOCK_RANGE and reads the null block.
+ * Cache contents past seq_len never reach the output, NaN scales included. */
+int op_paged_attention_fp4(int B, const float* q, int nq, int nkv, int d, const void* kpool, const void* vpool,
+                           float k_scale, float v_scale, const int32_t* bt, int bt_stride, const int32_t* seq_lens,
+                           int num_blocks, float* out, uint32_t* err, void* stream);
+
+/* op_prompt_attention: causal attention of packed prompts over the paged cache
+ * (kv_dtype MBT_DTYPE_BF16, _E4M3 or _E2M1) that already holds their K and V
+ * ("GPU Inference Internals", "Roofline: Why Decode Is Memory-Bound": prefill
+ * works on the whole prompt at once). Rows cu_seqlens[s] .. cu_seqlens[s + 1]
+ * - 1 of q [n][nq][d] (fp32, rotated) are the last tokens of sequence s, whose
+ * ctx_lens[s] tokens (those before the prompt included) are in the blocks
+ * bt[s][0 ..]; the row at position p attends over tokens 0 .. p. out [n][nq * d]
+ * fp32. cu_seqlens has nseq + 1 device ints, non-decreasing from 0 to at most
+ * n; a sequence may have no rows. Rows past the last sequence are left as they
+ * are. A row whose position is negative (ctx_lens[s] smaller than its prompt)
+ * attends over nothing and is 0; ctx_lens[s] < 0 or beyond the table sets
+ * MBT_DEV_SEQLEN_RANGE and the sequence's rows are 0; an out-of-range block id
+ * sets MBT_DEV_BLOCK_RANGE and reads the null block. Tokens after a row's own
+ * never reach it, NaN and infinities included. */
+int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq, const int32_t* cu_seqlens,
+                        const int32_t* ctx_lens, const void* kpool, const void* vpool, int kv_dtype, float k_scale,
+                        float v_scale, const int32_t* bt, int bt_stride, int num_blocks, float* out, uint32_t* err,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

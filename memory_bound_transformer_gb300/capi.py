@@ -22,7 +22,7 @@ STATUS = {0: "MBT_OK", -1: "MBT_ERR_BAD_ARG", -2: "MBT_ERR_BATCH", -3: "MBT_ERR_
           -8: "MBT_ERR_SCRATCH"}
 DEV_TOKEN_RANGE, DEV_BLOCK_RANGE, DEV_POS_RANGE, DEV_SEQLEN_RANGE, DEV_NONFINITE = 1, 2, 4, 8, 16
 EPI_PARTIAL, EPI_SWIGLU, EPI_ARGMAX = 0, 1, 2
-DTYPE_BF16, DTYPE_E4M3, DTYPE_F32 = 0, 1, 2
+DTYPE_BF16, DTYPE_E4M3, DTYPE_F32, DTYPE_E2M1 = 0, 1, 2, 3
 
 # every symbol the headers declare, with (restype, argtypes)
 _P, _I, _Z, _F, _U = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint32
@@ -59,6 +59,12 @@ SIGNATURES = {
     "op_paged_attention": (_I, [_I, _P, _I, _I, _I, _P, _P, _I, _F, _F, _P, _I, _P, _I, _P, _P, _P]),
     "op_paged_attention_noalloc": (_I, [_I, _P, _I, _I, _I, _P, _P, _I, _F, _F, _P, _I, _P, _I, _P, _P, _P]),
     "op_paged_attention_noalloc_limit": (_Z, []),
+    "op_kv_unit_bytes": (_Z, [_I, _I]),
+    "op_rope_table": (_I, [_I, _I, _F, _P, _P]),
+    "op_rope_kv_write_fp4": (_I, [_I, _P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _I, _F, _F, _P, _P, _P]),
+    "op_kv_read_fp4": (_I, [_I, _P, _P, _I, _P, _I, _I, _I, _P, _P, _I, _F, _F, _P, _P, _P, _P]),
+    "op_paged_attention_fp4": (_I, [_I, _P, _I, _I, _I, _P, _P, _F, _F, _P, _I, _P, _I, _P, _P, _P]),
+    "op_prompt_attention": (_I, [_I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _F, _F, _P, _I, _I, _P, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -355,3 +361,120 @@ def op_paged_attention_noalloc(q, nkv, kpool, vpool, kv_dtype, k_scale, v_scale,
 
 def op_paged_attention_noalloc_limit() -> int:
     return load().op_paged_attention_noalloc_limit()
+
+
+def _tensor(fn: str, name: str, t, dtype, *shape):
+    """A dense tensor of this type on the current device whose sizes are `shape` (None: any)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on another device than the current one")
+    if t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if shape and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _pool(fn: str, name: str, t, nkv: int, d: int, num_blocks: int, kv_dtype: int):
+    """A pool of at least num_blocks + 1 blocks in the cache format (any tensor shape and element type)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on another device than the current one")
+    if t.numel() * t.element_size() < (num_blocks + 1) * nkv * op_kv_unit_bytes(d, kv_dtype):
+        raise ValueError(f"{fn}: {name} is smaller than num_blocks + 1 blocks")
+
+
+def _rows_of(fn: str, n: int, row_seq, bt):
+    if row_seq is not None:
+        _tensor(fn, "row_seq", row_seq, torch.int32, n)
+    elif bt.shape[0] < n:
+        raise ValueError(f"{fn}: bt has fewer rows than positions (give row_seq)")
+
+
+def op_kv_unit_bytes(d: int, kv_dtype: int) -> int:
+    """Bytes of one (block, KV head) of a K or V pool; 0 for a head size or format the kernels do not take."""
+    return load().op_kv_unit_bytes(d, kv_dtype)
+
+
+def op_rope_table(max_pos: int, d: int, theta: float, table, stream=None) -> None:
+    """table [max_pos][d / 2][2] fp32 (cos, sin): set-up, synchronises the stream."""
+    _tensor("op_rope_table", "table", table, torch.float32, max_pos, d // 2, 2)
+    _check("op_rope_table", load().op_rope_table(max_pos, d, theta, _ptr(table), _stream(stream)))
+
+
+def op_rope_kv_write_fp4(qkv, nq, nkv, d, positions, bt, rope, kpool, vpool, num_blocks, k_scale, v_scale, q_out,
+                         row_seq=None, err=None, stream=None) -> None:
+    """RoPE and the 4-bit paged KV write of n rows: qkv [n][>= (nq + 2 nkv) d] fp32 (rows may be strided), positions
+    [n], bt [sequences][width], row_seq [n] or None (row i is sequence i), rope [max_pos][d / 2][2], q_out [n][nq][d]."""
+    fn = "op_rope_kv_write_fp4"
+    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2 or qkv.dtype != torch.float32 or not qkv.is_cuda:
+        raise ValueError(f"{fn}: qkv must be a two-dimensional fp32 device tensor")
+    n = qkv.shape[0]
+    if qkv.device.index != torch.cuda.current_device() or qkv.shape[1] < (nq + 2 * nkv) * d or qkv.stride(1) != 1:
+        raise ValueError(f"{fn}: qkv must hold (nq + 2 nkv) d neighbouring columns on the current device")
+    ld = qkv.stride(0) if n > 1 else max(qkv.stride(0), qkv.shape[1])
+    _tensor(fn, "positions", positions, torch.int32, n)
+    _tensor(fn, "bt", bt, torch.int32, None, None)
+    _rows_of(fn, n, row_seq, bt)
+    _tensor(fn, "rope", rope, torch.float32, None, d // 2, 2)
+    _tensor(fn, "q_out", q_out, torch.float32, n, nq, d)
+    _pool(fn, "kpool", kpool, nkv, d, num_blocks, DTYPE_E2M1)
+    _pool(fn, "vpool", vpool, nkv, d, num_blocks, DTYPE_E2M1)
+    _check(fn, load().op_rope_kv_write_fp4(n, _ptr(qkv), ld, nq, nkv, d, _ptr(positions), _ptr(row_seq), bt.shape[0],
+                                           _ptr(bt), bt.shape[1], _ptr(rope), rope.shape[0], _ptr(kpool), _ptr(vpool),
+                                           num_blocks, k_scale, v_scale, _ptr(q_out), _ptr(err), _stream(stream)))
+
+
+def op_kv_read_fp4(positions, bt, kpool, vpool, nkv, d, num_blocks, k_scale, v_scale, k_out, v_out, row_seq=None,
+                   err=None, stream=None) -> None:
+    """Cached rows as fp32 values: k_out, v_out [n][nkv][d]."""
+    fn = "op_kv_read_fp4"
+    _tensor(fn, "positions", positions, torch.int32, None)
+    n = positions.shape[0]
+    _tensor(fn, "bt", bt, torch.int32, None, None)
+    _rows_of(fn, n, row_seq, bt)
+    _tensor(fn, "k_out", k_out, torch.float32, n, nkv, d)
+    _tensor(fn, "v_out", v_out, torch.float32, n, nkv, d)
+    _pool(fn, "kpool", kpool, nkv, d, num_blocks, DTYPE_E2M1)
+    _pool(fn, "vpool", vpool, nkv, d, num_blocks, DTYPE_E2M1)
+    _check(fn, load().op_kv_read_fp4(n, _ptr(positions), _ptr(row_seq), bt.shape[0], _ptr(bt), bt.shape[1], nkv, d,
+                                     _ptr(kpool), _ptr(vpool), num_blocks, k_scale, v_scale, _ptr(k_out), _ptr(v_out),
+                                     _ptr(err), _stream(stream)))
+
+
+def op_paged_attention_fp4(q, nkv, kpool, vpool, k_scale, v_scale, bt, seq_lens, num_blocks, out, err=None,
+                           stream=None) -> None:
+    """Single-token attention over the 4-bit cache: q [B][nq][d] fp32, out [B][nq * d] fp32."""
+    fn = "op_paged_attention_fp4"
+    _tensor(fn, "q", q, torch.float32, None, None, None)
+    B, nq, d = q.shape
+    _tensor(fn, "bt", bt, torch.int32, B, None)
+    _tensor(fn, "seq_lens", seq_lens, torch.int32, B)
+    _tensor(fn, "out", out, torch.float32, B, nq * d)
+    _pool(fn, "kpool", kpool, nkv, d, num_blocks, DTYPE_E2M1)
+    _pool(fn, "vpool", vpool, nkv, d, num_blocks, DTYPE_E2M1)
+    _check(fn, load().op_paged_attention_fp4(B, _ptr(q), nq, nkv, d, _ptr(kpool), _ptr(vpool), k_scale, v_scale, _ptr(bt),
+                                             bt.shape[1], _ptr(seq_lens), num_blocks, _ptr(out), _ptr(err),
+                                             _stream(stream)))
+
+
+def op_prompt_attention(q, nkv, cu_seqlens, ctx_lens, kpool, vpool, kv_dtype, k_scale, v_scale, bt, num_blocks, out,
+                        err=None, stream=None) -> None:
+    """Causal attention of packed prompts over a paged cache: q [n][nq][d] fp32, cu_seqlens [sequences + 1], ctx_lens
+    [sequences], bt [sequences][width], out [n][nq * d] fp32; kv_dtype DTYPE_BF16, DTYPE_E4M3 or DTYPE_E2M1."""
+    fn = "op_prompt_attention"
+    _tensor(fn, "q", q, torch.float32, None, None, None)
+    n, nq, d = q.shape
+    _tensor(fn, "ctx_lens", ctx_lens, torch.int32, None)
+    nseq = ctx_lens.shape[0]
+    _tensor(fn, "cu_seqlens", cu_seqlens, torch.int32, nseq + 1)
+    _tensor(fn, "bt", bt, torch.int32, nseq, None)
+    _tensor(fn, "out", out, torch.float32, n, nq * d)
+    _pool(fn, "kpool", kpool, nkv, d, num_blocks, kv_dtype)
+    _pool(fn, "vpool", vpool, nkv, d, num_blocks, kv_dtype)
+    _check(fn, load().op_prompt_attention(n, _ptr(q), nq, nkv, d, nseq, _ptr(cu_seqlens), _ptr(ctx_lens), _ptr(kpool),
+                                          _ptr(vpool), kv_dtype, k_scale, v_scale, _ptr(bt), bt.shape[1], num_blocks,
+                                          _ptr(out), _ptr(err), _stream(stream)))

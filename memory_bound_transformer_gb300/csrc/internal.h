@@ -254,4 +254,41 @@ struct PrefillStageArgs {
 };
 cudaError_t launch_stage_prefill(const PrefillStageArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// 4-bit paged KV cache (format in fp4.cuh) and prompt attention
+
+enum KvType { KV_BF16 = 0, KV_E4M3 = 1, KV_FP4 = 2 };
+
+// RoPE on the q and k heads of n rows, q to q_out (fp32), k and v quantised
+// into the 4-bit paged cache. Row i belongs to sequence row_seq[i] (null: i).
+struct RopeKvFp4Args {
+  int n; const float* qkv; int ld_qkv; int nq, nkv, d;
+  const int* positions; const int* row_seq; int nseq; const int* bt; int bt_stride;
+  const float* rope; int max_pos;       // [max_pos][d / 2] (cos, sin) pairs
+  void* kpool; void* vpool; int num_blocks;
+  float k_scale, v_scale, inv6_k, inv6_v;   // inv6 = 1 / (6 scale)
+  float* q_out; uint32_t* err;
+};
+cudaError_t launch_rope_kv_write_fp4(const RopeKvFp4Args& a, cudaStream_t s);
+
+// Cached tokens read back as fp32 values [n][nkv][d].
+struct KvReadFp4Args {
+  int n; const int* positions; const int* row_seq; int nseq; const int* bt; int bt_stride; int nkv, d;
+  const void* kpool; const void* vpool; int num_blocks; float k_scale, v_scale;
+  float* k_out; float* v_out; uint32_t* err;
+};
+cudaError_t launch_kv_read_fp4(const KvReadFp4Args& a, cudaStream_t s);
+
+// Attention of n query rows over a paged cache. cu null: row i is sequence i
+// and attends over lens[i] tokens. Otherwise rows cu[s] .. cu[s + 1] - 1 are
+// the last of the lens[s] tokens of sequence s and each attends over the
+// tokens up to its own.
+struct RowsAttnArgs {
+  int n; const float* q; int nq, nkv, d; int kv;
+  const void* kpool; const void* vpool; float k_scale, v_scale;
+  int nseq; const int* cu; const int* lens; const int* bt; int bt_stride; int num_blocks;
+  float* out; uint32_t* err;
+};
+cudaError_t launch_attention_rows(const RowsAttnArgs& a, cudaStream_t s);
+
 }  // namespace mbt
