@@ -363,35 +363,71 @@ def op_paged_attention_noalloc_limit() -> int:
     return load().op_paged_attention_noalloc_limit()
 
 
-def _tensor(fn: str, name: str, t, dtype, *shape):
-    """A dense tensor of this type on the current device whose sizes are `shape` (None: any)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _tensor(fn: str, name: str, t, dev: int, dtype, shape) -> int:
+    """Address of a dense tensor of this type and shape on device `dev`, the current one."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{fn}: {name} must be a device tensor") from None
+    if not t.is_cuda:
         raise ValueError(f"{fn}: {name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} is on another device than the current one")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
-    if shape and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{fn}: {name} must be contiguous")
 
 
-def _pool(fn: str, name: str, t, nkv: int, d: int, num_blocks: int, kv_dtype: int):
-    """A pool of at least num_blocks + 1 blocks in the cache format (any tensor shape and element type)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be a contiguous device tensor")
-    if t.device.index != torch.cuda.current_device():
+def _device(fn: str, name: str, t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{fn}: {name} must be a device tensor")
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{fn}: {name} is on another device than the current one")
-    if t.numel() * t.element_size() < (num_blocks + 1) * nkv * op_kv_unit_bytes(d, kv_dtype):
-        raise ValueError(f"{fn}: {name} is smaller than num_blocks + 1 blocks")
+    return dev
 
 
-def _rows_of(fn: str, n: int, row_seq, bt):
+def _shape(fn: str, name: str, t, dims: int):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{fn}: {name} must be a tensor of {dims} dimensions")
+    return t.shape
+
+
+# op_kv_unit_bytes of the head sizes and cache formats the kernels take
+_UNIT = {(d, k): b for d in (64, 128) for k, b in ((DTYPE_BF16, 32 * d), (DTYPE_E4M3, 16 * d), (DTYPE_E2M1, 9 * d))}
+
+
+def _pools(fn: str, k, v, dev: int, nkv: int, d: int, num_blocks: int, kv_dtype: int):
+    """Addresses of two pools of at least num_blocks + 1 blocks in the cache format (any shape and element type)."""
+    need = (num_blocks + 1) * nkv * _UNIT.get((d, kv_dtype), 0)
+    for name, t in (("kpool", k), ("vpool", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be a contiguous device tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on another device than the current one")
+        if t.nbytes < need:
+            raise ValueError(f"{fn}: {name} is smaller than num_blocks + 1 blocks")
+    return k.data_ptr(), v.data_ptr()
+
+
+def _err(fn: str, err, dev: int):
+    return None if err is None else _tensor(fn, "err", err, dev, torch.int32, (1,))
+
+
+def _rows_of(fn: str, n: int, row_seq, nseq: int, dev: int):
     if row_seq is not None:
-        _tensor(fn, "row_seq", row_seq, torch.int32, n)
-    elif bt.shape[0] < n:
+        return _tensor(fn, "row_seq", row_seq, dev, torch.int32, (n,))
+    if nseq < n:
         raise ValueError(f"{fn}: bt has fewer rows than positions (give row_seq)")
+    return None
+
+
+def _stream_of(stream, dev: int) -> Optional[int]:
+    """_stream, with the current stream of `dev` read without a Stream object (these calls are a few us long)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def op_kv_unit_bytes(d: int, kv_dtype: int) -> int:
@@ -401,8 +437,10 @@ def op_kv_unit_bytes(d: int, kv_dtype: int) -> int:
 
 def op_rope_table(max_pos: int, d: int, theta: float, table, stream=None) -> None:
     """table [max_pos][d / 2][2] fp32 (cos, sin): set-up, synchronises the stream."""
-    _tensor("op_rope_table", "table", table, torch.float32, max_pos, d // 2, 2)
-    _check("op_rope_table", load().op_rope_table(max_pos, d, theta, _ptr(table), _stream(stream)))
+    fn = "op_rope_table"
+    dev = torch.cuda.current_device()
+    _check(fn, load().op_rope_table(max_pos, d, theta, _tensor(fn, "table", table, dev, torch.float32, (max_pos, d // 2, 2)),
+                                    _stream_of(stream, dev)))
 
 
 def op_rope_kv_write_fp4(qkv, nq, nkv, d, positions, bt, rope, kpool, vpool, num_blocks, k_scale, v_scale, q_out,
@@ -410,55 +448,49 @@ def op_rope_kv_write_fp4(qkv, nq, nkv, d, positions, bt, rope, kpool, vpool, num
     """RoPE and the 4-bit paged KV write of n rows: qkv [n][>= (nq + 2 nkv) d] fp32 (rows may be strided), positions
     [n], bt [sequences][width], row_seq [n] or None (row i is sequence i), rope [max_pos][d / 2][2], q_out [n][nq][d]."""
     fn = "op_rope_kv_write_fp4"
-    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2 or qkv.dtype != torch.float32 or not qkv.is_cuda:
-        raise ValueError(f"{fn}: qkv must be a two-dimensional fp32 device tensor")
-    n = qkv.shape[0]
-    if qkv.device.index != torch.cuda.current_device() or qkv.shape[1] < (nq + 2 * nkv) * d or qkv.stride(1) != 1:
-        raise ValueError(f"{fn}: qkv must hold (nq + 2 nkv) d neighbouring columns on the current device")
-    ld = qkv.stride(0) if n > 1 else max(qkv.stride(0), qkv.shape[1])
-    _tensor(fn, "positions", positions, torch.int32, n)
-    _tensor(fn, "bt", bt, torch.int32, None, None)
-    _rows_of(fn, n, row_seq, bt)
-    _tensor(fn, "rope", rope, torch.float32, None, d // 2, 2)
-    _tensor(fn, "q_out", q_out, torch.float32, n, nq, d)
-    _pool(fn, "kpool", kpool, nkv, d, num_blocks, DTYPE_E2M1)
-    _pool(fn, "vpool", vpool, nkv, d, num_blocks, DTYPE_E2M1)
-    _check(fn, load().op_rope_kv_write_fp4(n, _ptr(qkv), ld, nq, nkv, d, _ptr(positions), _ptr(row_seq), bt.shape[0],
-                                           _ptr(bt), bt.shape[1], _ptr(rope), rope.shape[0], _ptr(kpool), _ptr(vpool),
-                                           num_blocks, k_scale, v_scale, _ptr(q_out), _ptr(err), _stream(stream)))
+    n, cols = _shape(fn, "qkv", qkv, 2)
+    dev = _device(fn, "qkv", qkv)
+    if qkv.dtype is not torch.float32 or cols < (nq + 2 * nkv) * d or qkv.stride(1) != 1:
+        raise ValueError(f"{fn}: qkv must be fp32 with (nq + 2 nkv) d neighbouring columns")
+    ld = max(qkv.stride(0), cols) if n < 2 else qkv.stride(0)
+    nseq, width = _shape(fn, "bt", bt, 2)
+    max_pos = _shape(fn, "rope", rope, 3)[0]
+    pk, pv = _pools(fn, kpool, vpool, dev, nkv, d, num_blocks, DTYPE_E2M1)
+    _check(fn, load().op_rope_kv_write_fp4(
+        n, qkv.data_ptr(), ld, nq, nkv, d, _tensor(fn, "positions", positions, dev, torch.int32, (n,)),
+        _rows_of(fn, n, row_seq, nseq, dev), nseq, _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width,
+        _tensor(fn, "rope", rope, dev, torch.float32, (max_pos, d // 2, 2)), max_pos, pk, pv, num_blocks, k_scale, v_scale,
+        _tensor(fn, "q_out", q_out, dev, torch.float32, (n, nq, d)), _err(fn, err, dev), _stream_of(stream, dev)))
 
 
 def op_kv_read_fp4(positions, bt, kpool, vpool, nkv, d, num_blocks, k_scale, v_scale, k_out, v_out, row_seq=None,
                    err=None, stream=None) -> None:
     """Cached rows as fp32 values: k_out, v_out [n][nkv][d]."""
     fn = "op_kv_read_fp4"
-    _tensor(fn, "positions", positions, torch.int32, None)
-    n = positions.shape[0]
-    _tensor(fn, "bt", bt, torch.int32, None, None)
-    _rows_of(fn, n, row_seq, bt)
-    _tensor(fn, "k_out", k_out, torch.float32, n, nkv, d)
-    _tensor(fn, "v_out", v_out, torch.float32, n, nkv, d)
-    _pool(fn, "kpool", kpool, nkv, d, num_blocks, DTYPE_E2M1)
-    _pool(fn, "vpool", vpool, nkv, d, num_blocks, DTYPE_E2M1)
-    _check(fn, load().op_kv_read_fp4(n, _ptr(positions), _ptr(row_seq), bt.shape[0], _ptr(bt), bt.shape[1], nkv, d,
-                                     _ptr(kpool), _ptr(vpool), num_blocks, k_scale, v_scale, _ptr(k_out), _ptr(v_out),
-                                     _ptr(err), _stream(stream)))
+    n, = _shape(fn, "positions", positions, 1)
+    dev = _device(fn, "positions", positions)
+    nseq, width = _shape(fn, "bt", bt, 2)
+    pk, pv = _pools(fn, kpool, vpool, dev, nkv, d, num_blocks, DTYPE_E2M1)
+    _check(fn, load().op_kv_read_fp4(
+        n, _tensor(fn, "positions", positions, dev, torch.int32, (n,)), _rows_of(fn, n, row_seq, nseq, dev), nseq,
+        _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, nkv, d, pk, pv, num_blocks, k_scale, v_scale,
+        _tensor(fn, "k_out", k_out, dev, torch.float32, (n, nkv, d)),
+        _tensor(fn, "v_out", v_out, dev, torch.float32, (n, nkv, d)), _err(fn, err, dev), _stream_of(stream, dev)))
 
 
 def op_paged_attention_fp4(q, nkv, kpool, vpool, k_scale, v_scale, bt, seq_lens, num_blocks, out, err=None,
                            stream=None) -> None:
     """Single-token attention over the 4-bit cache: q [B][nq][d] fp32, out [B][nq * d] fp32."""
     fn = "op_paged_attention_fp4"
-    _tensor(fn, "q", q, torch.float32, None, None, None)
-    B, nq, d = q.shape
-    _tensor(fn, "bt", bt, torch.int32, B, None)
-    _tensor(fn, "seq_lens", seq_lens, torch.int32, B)
-    _tensor(fn, "out", out, torch.float32, B, nq * d)
-    _pool(fn, "kpool", kpool, nkv, d, num_blocks, DTYPE_E2M1)
-    _pool(fn, "vpool", vpool, nkv, d, num_blocks, DTYPE_E2M1)
-    _check(fn, load().op_paged_attention_fp4(B, _ptr(q), nq, nkv, d, _ptr(kpool), _ptr(vpool), k_scale, v_scale, _ptr(bt),
-                                             bt.shape[1], _ptr(seq_lens), num_blocks, _ptr(out), _ptr(err),
-                                             _stream(stream)))
+    B, nq, d = _shape(fn, "q", q, 3)
+    dev = _device(fn, "q", q)
+    width = _shape(fn, "bt", bt, 2)[1]
+    pk, pv = _pools(fn, kpool, vpool, dev, nkv, d, num_blocks, DTYPE_E2M1)
+    _check(fn, load().op_paged_attention_fp4(
+        B, _tensor(fn, "q", q, dev, torch.float32, (B, nq, d)), nq, nkv, d, pk, pv, k_scale, v_scale,
+        _tensor(fn, "bt", bt, dev, torch.int32, (B, width)), width,
+        _tensor(fn, "seq_lens", seq_lens, dev, torch.int32, (B,)), num_blocks,
+        _tensor(fn, "out", out, dev, torch.float32, (B, nq * d)), _err(fn, err, dev), _stream_of(stream, dev)))
 
 
 def op_prompt_attention(q, nkv, cu_seqlens, ctx_lens, kpool, vpool, kv_dtype, k_scale, v_scale, bt, num_blocks, out,
@@ -466,15 +498,13 @@ def op_prompt_attention(q, nkv, cu_seqlens, ctx_lens, kpool, vpool, kv_dtype, k_
     """Causal attention of packed prompts over a paged cache: q [n][nq][d] fp32, cu_seqlens [sequences + 1], ctx_lens
     [sequences], bt [sequences][width], out [n][nq * d] fp32; kv_dtype DTYPE_BF16, DTYPE_E4M3 or DTYPE_E2M1."""
     fn = "op_prompt_attention"
-    _tensor(fn, "q", q, torch.float32, None, None, None)
-    n, nq, d = q.shape
-    _tensor(fn, "ctx_lens", ctx_lens, torch.int32, None)
-    nseq = ctx_lens.shape[0]
-    _tensor(fn, "cu_seqlens", cu_seqlens, torch.int32, nseq + 1)
-    _tensor(fn, "bt", bt, torch.int32, nseq, None)
-    _tensor(fn, "out", out, torch.float32, n, nq * d)
-    _pool(fn, "kpool", kpool, nkv, d, num_blocks, kv_dtype)
-    _pool(fn, "vpool", vpool, nkv, d, num_blocks, kv_dtype)
-    _check(fn, load().op_prompt_attention(n, _ptr(q), nq, nkv, d, nseq, _ptr(cu_seqlens), _ptr(ctx_lens), _ptr(kpool),
-                                          _ptr(vpool), kv_dtype, k_scale, v_scale, _ptr(bt), bt.shape[1], num_blocks,
-                                          _ptr(out), _ptr(err), _stream(stream)))
+    n, nq, d = _shape(fn, "q", q, 3)
+    dev = _device(fn, "q", q)
+    nseq, width = _shape(fn, "bt", bt, 2)
+    pk, pv = _pools(fn, kpool, vpool, dev, nkv, d, num_blocks, kv_dtype)
+    _check(fn, load().op_prompt_attention(
+        n, _tensor(fn, "q", q, dev, torch.float32, (n, nq, d)), nq, nkv, d, nseq,
+        _tensor(fn, "cu_seqlens", cu_seqlens, dev, torch.int32, (nseq + 1,)),
+        _tensor(fn, "ctx_lens", ctx_lens, dev, torch.int32, (nseq,)), pk, pv, kv_dtype, k_scale, v_scale,
+        _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, num_blocks,
+        _tensor(fn, "out", out, dev, torch.float32, (n, nq * d)), _err(fn, err, dev), _stream_of(stream, dev)))

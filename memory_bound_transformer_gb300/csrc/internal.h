@@ -291,4 +291,17 @@ struct RowsAttnArgs {
 };
 cudaError_t launch_attention_rows(const RowsAttnArgs& a, cudaStream_t s);
 
+// Single-token attention over the 4-bit cache: a cluster of `cluster` CTAs per
+// (row, KV head, group of eight query heads; hblocks of those per KV head).
+struct AttnFp4Args {
+  int B; const float* q; int nq, nkv, d;
+  const void* kpool; const void* vpool; float k_scale, v_scale;
+  const int* bt; int bt_stride; const int* seq_lens; int num_blocks;
+  float* out; uint32_t* err;
+  int hblocks, cluster;
+};
+cudaError_t attn_fp4_plan(AttnFp4Args* a, int num_sms);     // sets hblocks and cluster
+cudaError_t launch_attention_fp4(const AttnFp4Args& a, cudaStream_t s);
+cudaError_t attn_fp4_init();
+
 }  // namespace mbt

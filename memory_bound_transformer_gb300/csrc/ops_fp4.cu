@@ -2,6 +2,7 @@
 // attention (include/mbt_ops.h).
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -18,6 +19,24 @@ bool scale_ok(float s) { return s > 0.f && std::isfinite(s); }
 // Heads and head size that the cache's kernels take.
 bool heads_ok(int nq, int nkv, int d) {
   return nq >= 1 && nkv >= 1 && nq % nkv == 0 && nq / nkv <= 16 && (d == 64 || d == 128);
+}
+// SM count of the current device; the kernels' shared-memory limits are raised
+// once per device.
+int device_setup(int* sms) {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static int known[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MBT_ERR_NO_DEVICE;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!known[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MBT_ERR_NO_DEVICE;
+    if (attn_fp4_init() != cudaSuccess) return MBT_ERR_CUDA;
+    known[dev] = n;
+  }
+  *sms = known[dev];
+  return MBT_OK;
 }
 int status(cudaError_t e) {
   if (e == cudaSuccess) return MBT_OK;
@@ -97,11 +116,15 @@ int op_paged_attention_fp4(int B, const float* q, int nq, int nkv, int d, const 
       bt_stride < 1 || !seq_lens || num_blocks < 1 || !out)
     return MBT_ERR_BAD_ARG;
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out)) return MBT_ERR_BAD_ARG;
-  RowsAttnArgs a = {};
-  a.n = B; a.q = q; a.nq = nq; a.nkv = nkv; a.d = d; a.kv = KV_FP4; a.kpool = kpool; a.vpool = vpool;
-  a.k_scale = k_scale; a.v_scale = v_scale; a.nseq = B; a.lens = seq_lens; a.bt = bt; a.bt_stride = bt_stride;
+  int sms = 0;
+  const int rc = device_setup(&sms);
+  if (rc != MBT_OK) return rc;
+  AttnFp4Args a = {};
+  a.B = B; a.q = q; a.nq = nq; a.nkv = nkv; a.d = d; a.kpool = kpool; a.vpool = vpool;
+  a.k_scale = k_scale; a.v_scale = v_scale; a.bt = bt; a.bt_stride = bt_stride; a.seq_lens = seq_lens;
   a.num_blocks = num_blocks; a.out = out; a.err = err;
-  return status(launch_attention_rows(a, (cudaStream_t)stream));
+  if (attn_fp4_plan(&a, sms) != cudaSuccess) return MBT_ERR_BAD_ARG;
+  return status(launch_attention_fp4(a, (cudaStream_t)stream));
 }
 
 int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq, const int32_t* cu_seqlens,
