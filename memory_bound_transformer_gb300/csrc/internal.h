@@ -279,17 +279,16 @@ struct KvReadFp4Args {
 };
 cudaError_t launch_kv_read_fp4(const KvReadFp4Args& a, cudaStream_t s);
 
-// Attention of n query rows over a paged cache. cu null: row i is sequence i
-// and attends over lens[i] tokens. Otherwise rows cu[s] .. cu[s + 1] - 1 are
-// the last of the lens[s] tokens of sequence s and each attends over the
-// tokens up to its own.
-struct RowsAttnArgs {
+// Causal attention of n packed query rows over a paged cache: rows cu[s] ..
+// cu[s + 1] - 1 are the last of the lens[s] tokens of sequence s.
+struct PromptArgs {
   int n; const float* q; int nq, nkv, d; int kv;
   const void* kpool; const void* vpool; float k_scale, v_scale;
   int nseq; const int* cu; const int* lens; const int* bt; int bt_stride; int num_blocks;
   float* out; uint32_t* err;
 };
-cudaError_t launch_attention_rows(const RowsAttnArgs& a, cudaStream_t s);
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s);
+cudaError_t prompt_attention_init();
 
 // Single-token attention over the 4-bit cache: a cluster of `cluster` CTAs per
 // (row, KV head, group of eight query heads; hblocks of those per KV head).

@@ -32,7 +32,7 @@ int device_setup(int* sms) {
   if (!known[dev]) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MBT_ERR_NO_DEVICE;
-    if (attn_fp4_init() != cudaSuccess) return MBT_ERR_CUDA;
+    if (attn_fp4_init() != cudaSuccess || prompt_attention_init() != cudaSuccess) return MBT_ERR_CUDA;
     known[dev] = n;
   }
   *sms = known[dev];
@@ -136,12 +136,15 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
     return MBT_ERR_BAD_ARG;
   if (kv_dtype != MBT_DTYPE_BF16 && kv_dtype != MBT_DTYPE_E4M3 && kv_dtype != MBT_DTYPE_E2M1) return MBT_ERR_BAD_ARG;
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out)) return MBT_ERR_BAD_ARG;
-  RowsAttnArgs a = {};
+  int sms = 0;
+  const int rc = device_setup(&sms);
+  if (rc != MBT_OK) return rc;
+  PromptArgs a = {};
   a.n = n; a.q = q; a.nq = nq; a.nkv = nkv; a.d = d; a.kpool = kpool; a.vpool = vpool;
   a.kv = kv_dtype == MBT_DTYPE_BF16 ? KV_BF16 : kv_dtype == MBT_DTYPE_E4M3 ? KV_E4M3 : KV_FP4;
   a.k_scale = k_scale; a.v_scale = v_scale; a.nseq = nseq; a.cu = cu_seqlens; a.lens = ctx_lens; a.bt = bt;
   a.bt_stride = bt_stride; a.num_blocks = num_blocks; a.out = out; a.err = err;
-  return status(launch_attention_rows(a, (cudaStream_t)stream));
+  return status(launch_prompt_attention(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,745 @@
+// Causal attention of packed prompts over the paged KV cache (BF16, e4m3 or
+// 4-bit), on the tcgen05 tensor cores:
+//   o = sum_{t <= p} softmax_t(q . K_t / sqrt(d)) V_t   for the row at position p,
+// one pass with the running maximum and sum of the softmax ("GPU Inference
+// Internals", "Kernels: FlashAttention and the Memory Hierarchy": K and V tiles
+// in on-chip memory, no score matrix in HBM).
+//
+// A CTA takes 128 query rows: T = 128 / G neighbouring tokens x the G query heads
+// of one KV head, so grouped heads share every K and V tile and a short prompt
+// fills the MMA's rows. Keys come in tiles of 128 tokens, in two streams (even
+// and odd tiles) with a softmax warpgroup each, so that one stream's products
+// run while the other's softmax does; the streams' states merge at the end.
+//   warps 0-3, 4-7   softmax and output of stream 0 and 1, one row per thread
+//   warps 8-11       loader: raw cache blocks to 16-bit tiles in shared memory
+//   warps 12, 13     MMA issue of stream 0 and 1 (one issuing thread reaches an
+//                    M = 128 MMA per ~100 cycles, two reach the pipe's 64)
+// Accuracy is that of single-token attention: queries and probabilities enter
+// as FP16 high and low parts (2^-22), two MMAs per product, low part first. So
+// the floor is twice the formula's operations at the tensor rate. e4m3 and 4-bit
+// values widen to FP16 exactly. BF16 values get one exponent per 16 tokens (a
+// cache block of a head) that puts the largest just below 2^16: exact down to
+// 2^-29 of it, 2^-30 of it off below; scores take the exponent with the query
+// scale, probabilities with the softmax's offset, both for free.
+// Queries and probabilities are the A operand in tensor memory (the tile of K
+// or V is then the only operand read from shared memory: an M = N = 128 MMA with
+// both there needs all of its bandwidth); probabilities take the place of the
+// scores they came from. P V of each tile goes to a fresh accumulator that the
+// softmax threads add to fp32 registers (IEEE adds; the tensor core's own
+// accumulation truncates), which also makes the rescaling a fused multiply-add.
+//
+// Tensor memory (512 columns): scores / probabilities of stream 0 and 1 (128
+// each: for 16 keys 8 columns of high and 8 of low parts), P V (128, the streams
+// take turns), queries (D / 2 high, D / 2 low).
+//
+// A value of V that is not finite at a token some rows of the tile do not attend
+// to would reach them as 0 x inf: the loader stores 0 for it and raises a flag,
+// and the rows that do attend to it add it at the end.
+#include <algorithm>
+
+#include "fp4.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace mbt {
+
+namespace {
+
+constexpr int kPaRows = 128;                // query rows and keys per tile
+constexpr int kPaThreads = 512;
+constexpr uint32_t kPaO = 256, kPaQ = 384;  // TMEM columns (stream s's scores at 128 s)
+// registers: 2 x 128 x 192 + 128 x 96 + 128 x 32 = 512 x 128
+constexpr int kPaSoftmaxRegs = 192, kPaLoadRegs = 96, kPaIssueRegs = 32;
+
+template <int D, int KV>
+struct PaShape {
+  static constexpr bool BF = KV == KV_BF16;           // tiles carry an exponent per block
+  static constexpr int UNIT = KV == KV_FP4 ? fp4_unit_bytes(D) : kBlockTokens * D * (KV == KV_E4M3 ? 1 : 2);
+  static constexpr int CPC = KV == KV_FP4 ? 32 : KV == KV_E4M3 ? 16 : 8;   // channels of a 16-byte raw chunk
+  static constexpr int ROWB = D / CPC * 16;           // raw bytes of a token's codes
+  static constexpr int PP = 64 / CPC;                 // chunks of a row in a 64-channel panel
+  static constexpr int NCH = kBlockTokens * (D / CPC) / 32;   // chunks of a block per lane
+  static constexpr int PANEL = kPaRows * 128;         // 128 tokens x 64 channels, 128-byte swizzle
+  static constexpr int TILE = D / 64 * PANEL;
+  static constexpr int LDO = D + 4;                   // output staging row, floats
+  static constexpr int SMEM = 4 * TILE + 1024;
+  static_assert(kPaRows * LDO * 4 <= 4 * TILE, "the output fits in the drained tiles");
+};
+
+struct PaBars {
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], done[2], ofree, qfull;
+};
+
+// Bounded wait; once any wait of the CTA has run out, the others give up too.
+__device__ __forceinline__ bool pa_wait(uint64_t* b, uint32_t parity, volatile int* stop) {
+  if (mbar_try(b, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try(b, parity)) {
+    if (*stop) return false;
+    if (clock64() - t0 > kTcWaitCycles) { *stop = 1; return false; }
+  }
+  return true;
+}
+
+__device__ __forceinline__ float pa_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// x = hi + lo as FP16 pairs (first value in the low half).
+__device__ __forceinline__ void pa_split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
+  const float2 h = h2_to_float2(hi);
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(x1 - h.y), "f"(x0 - h.x));
+}
+__device__ __forceinline__ uint32_t pa_hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// tensor memory: 32 or 16 columns of this thread's lane to registers, 8 from them
+__device__ __forceinline__ void pa_ld32(uint32_t t, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                 "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                 "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(t));
+}
+// Wait for the loads into r (threaded through, so no use moves before it).
+__device__ __forceinline__ void pa_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :: "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void pa_st8(uint32_t t, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"r"(t), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
+__device__ __forceinline__ void pa_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D += A B with A from tensor memory (rows in lanes, two 16-bit K elements per column).
+__device__ __forceinline__ void pa_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// Shared-memory descriptor of a tile whose rows are K (tokens) and whose
+// 64-channel panels are N: 8-row groups 1024 bytes apart, panels `panel` bytes.
+__device__ __forceinline__ uint64_t pa_mn_desc(uint32_t saddr, uint32_t panel) {
+  return (sw128_desc(saddr) & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(panel >> 4) << 16);
+}
+
+// One query tile: where its rows are and how far they see.
+struct PaTile { int seq, row0, tokens, pos0, ctx; };   // pos0: position of the first token's row
+
+// The tile of index `idx` among all sequences' tiles of T tokens, in order of
+// the sequences; false past the last. One warp; every lane gets the result.
+__device__ __forceinline__ bool pa_find(const PromptArgs& a, int T, long long idx, int lane, PaTile* t) {
+  long long before = 0;
+  for (int s0 = 0; s0 < a.nseq; s0 += 32) {
+    const int s = s0 + lane;
+    int lo = 0, hi = 0;
+    if (s < a.nseq) {
+      lo = min(max(a.cu[s], 0), a.n);
+      hi = min(max(a.cu[s + 1], lo), a.n);
+    }
+    const int mine = (hi - lo + T - 1) / T;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > idx);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int first = (int)(idx - before) - __shfl_sync(0xffffffffu, inc - mine, src);
+      const int count = __shfl_sync(0xffffffffu, mine, src);
+      lo = __shfl_sync(0xffffffffu, lo, src);
+      hi = __shfl_sync(0xffffffffu, hi, src);
+      const int at = (count - 1 - first) * T;                        // a sequence's last tiles (the longest) first
+      t->seq = s0 + src;
+      t->row0 = lo + at;
+      t->tokens = min(T, hi - lo - at);
+      t->ctx = a.lens[t->seq];
+      t->pos0 = t->ctx - (hi - lo) + at;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return false;
+}
+
+// ---------------------------------------------------------------------------
+// loader
+
+template <int D, int KV>
+struct PaRaw { uint4 c[PaShape<D, KV>::NCH]; uint16_t sc[PaShape<D, KV>::NCH]; };
+
+// A lane's chunk q of a block: panel, token and part of the token's panel row.
+template <int D, int KV>
+__device__ __forceinline__ void pa_chunk(int q, int lane, int& panel, int& row, int& part) {
+  using S = PaShape<D, KV>;
+  const int id = q * 32 + lane;
+  panel = id / (kBlockTokens * S::PP);
+  row = id / S::PP % kBlockTokens;
+  part = id % S::PP;
+}
+
+template <int D, int KV>
+__device__ __forceinline__ void pa_fetch(const void* pool, size_t unit, bool live, int lane, PaRaw<D, KV>& r) {
+  using S = PaShape<D, KV>;
+  const unsigned char* u = reinterpret_cast<const unsigned char*>(pool) + unit * S::UNIT;
+#pragma unroll
+  for (int q = 0; q < S::NCH; ++q) {
+    int panel, row, part;
+    pa_chunk<D, KV>(q, lane, panel, row, part);
+    r.c[q] = live ? __ldg(reinterpret_cast<const uint4*>(u + row * S::ROWB + (panel * S::PP + part) * 16))
+                  : make_uint4(0u, 0u, 0u, 0u);
+    if (KV == KV_FP4)
+      r.sc[q] = live ? __ldg(reinterpret_cast<const uint16_t*>(u + kBlockTokens * (D / 2) + row * (D / 16) + panel * 4 + part * 2))
+                     : (uint16_t)0;
+  }
+}
+
+// Exponent base of a BF16 block: FP16 exponent field = BF16 field - base, the
+// largest finite value's at 30. `high` (uniform): some value is not finite.
+template <int NCH>
+__device__ __forceinline__ int pa_block_base(const uint4 (&c)[NCH], bool& high) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < NCH; ++q) {
+    m = __vmaxu2(m, c[q].x & 0x7fff7fffu); m = __vmaxu2(m, c[q].y & 0x7fff7fffu);
+    m = __vmaxu2(m, c[q].z & 0x7fff7fffu); m = __vmaxu2(m, c[q].w & 0x7fff7fffu);
+  }
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
+  high = top >= 0x7f80u;
+  if (high) {                                                        // rare: the largest of the finite values
+    uint32_t f = 0;
+#pragma unroll
+    for (int q = 0; q < NCH; ++q) {
+      const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = w[e] & 0x7fffu, hi = w[e] >> 16 & 0x7fffu;
+        f = max(f, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, f);
+  }
+  return max(0, (int)(top >> 7) - 30);
+}
+
+// Raw chunks to FP16 values in the tile (rows R0 .. R0 + 15). Tokens from `keep`
+// on are stored as zeros; where `guard`, values that are not finite are too, and
+// the return value says whether there were any. BF16: *base receives the
+// block's exponent base.
+template <int D, int KV>
+__device__ __forceinline__ bool pa_store(PaRaw<D, KV>& r, unsigned char* tile, int R0, int keep, bool guard, int lane, int* base) {
+  using S = PaShape<D, KV>;
+  bool found = false, high = false;
+  uint32_t low = 0, shift = 0;
+  if (S::BF) {
+#pragma unroll
+    for (int q = 0; q < S::NCH; ++q) {
+      int panel, row, part;
+      pa_chunk<D, KV>(q, lane, panel, row, part);
+      if (row >= keep) r.c[q] = make_uint4(0u, 0u, 0u, 0u);          // nothing past the context sets the exponent
+    }
+    const int b = pa_block_base(r.c, high);
+    *base = b;
+    low = (uint32_t)((b + 1) << 7) * 0x10001u;                       // smallest magnitude kept: FP16 exponent field 1
+    shift = 0u - (uint32_t)(b << 10) * 0x10001u;
+  }
+#pragma unroll
+  for (int q = 0; q < S::NCH; ++q) {
+    int panel, row, part;
+    pa_chunk<D, KV>(q, lane, panel, row, part);
+    const uint32_t w[4] = {r.c[q].x, r.c[q].y, r.c[q].z, r.c[q].w};
+    const int R = R0 + row;
+    unsigned char* dst = tile + panel * S::PANEL + R * 128;
+    uint32_t sc[2];
+    if (KV == KV_FP4) {
+      uint32_t s2;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(r.sc[q]));
+      sc[0] = __byte_perm(s2, s2, 0x1010);
+      sc[1] = __byte_perm(s2, s2, 0x3232);
+    }
+#pragma unroll
+    for (int k = 0; k < S::CPC / 8; ++k) {                           // 8 channels = 16 bytes of the tile
+      uint32_t v[4];
+      if (KV == KV_FP4) {
+        e2m1x8_to_h2(w[k], v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = pa_hmul2(v[e], sc[k >> 1]);
+      } else if (KV == KV_E4M3) {
+        v[0] = e4m3x2_to_h2bits(w[2 * k]); v[1] = e4m3x2_to_h2bits(w[2 * k] >> 16);
+        v[2] = e4m3x2_to_h2bits(w[(2 * k + 1) & 3]); v[3] = e4m3x2_to_h2bits(w[(2 * k + 1) & 3] >> 16);
+      } else {
+        // (magnitude - (base << 7)) << 3 in both halves at once, sign kept
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = (__vmaxu2(w[e] & 0x7fff7fffu, low) * 8u + shift) | (w[e] & 0x80008000u);
+        if (high) {                                                  // non-finite values: FP16 infinity or NaN
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t out = 0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t x = w[e] >> (16 * half) & 0xffffu, f = v[e] >> (16 * half) & 0xffffu;
+              out |= ((x & 0x7f80u) == 0x7f80u ? (x & 0x8000u) | 0x7c00u | ((x & 0x7fu) ? 0x200u : 0u) : f) << (16 * half);
+            }
+            v[e] = out;
+          }
+        }
+      }
+      if (guard) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t bad = __vcmpeq2(v[e] & 0x7c007c00u, 0x7c007c00u);
+          found |= bad != 0;
+          v[e] &= ~bad;
+        }
+      }
+      if (row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;
+      *reinterpret_cast<uint4*>(dst + (((part * (S::CPC / 8) + k) ^ (R & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  return found;
+}
+
+// One cached value as fp32 (the slow path's).
+template <int D, int KV>
+__device__ float pa_value(const unsigned char* unit, int slot, int ch) {
+  if (KV == KV_FP4) {
+    uint32_t h[4];
+    e2m1x8_to_h2(unit[slot * (D / 2) + ch / 2], h);
+    const float2 f = h2_to_float2(h[0]);
+    return (ch & 1 ? f.y : f.x) * e4m3_to_f32(unit[kBlockTokens * (D / 2) + slot * (D / 16) + ch / 16]);
+  }
+  if (KV == KV_E4M3) return e4m3_to_f32(unit[slot * D + ch]);
+  return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(unit)[slot * D + ch] << 16);
+}
+
+// ---------------------------------------------------------------------------
+
+template <int D, int KV>
+__global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const PromptArgs a) {
+  using S = PaShape<D, KV>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  __shared__ __align__(8) PaBars bars;
+  __shared__ uint32_t tmem_slot, sm_big[2][kPaRows];
+  __shared__ float sm_m[2][kPaRows], sm_l[2][kPaRows];
+  __shared__ PaTile sm_tile;
+  // BF16 exponent bases of the tiles' blocks; a K tile's outlive its buffer
+  __shared__ int sm_ok, sm_poison, sm_kbase[4][8], sm_vbase[2][8];
+  __shared__ volatile int sm_stop;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.nq / a.nkv, T = kPaRows / G, h = (int)(blockIdx.x % (unsigned)a.nkv);
+
+  if (warp == 0) {
+    PaTile t;
+    const bool ok = pa_find(a, T, blockIdx.x / (unsigned)a.nkv, lane, &t);
+    if (lane == 0) {
+      sm_ok = ok;
+      if (ok) sm_tile = t;
+      sm_stop = 0;
+      sm_poison = 0;
+    }
+  }
+  if (warp == 1 && lane == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.kfull[s], 4); mbar_init(&bars.vfull[s], 4); mbar_init(&bars.pfull[s], 4);
+      mbar_init(&bars.kempty[s], 1); mbar_init(&bars.vempty[s], 1); mbar_init(&bars.sfull[s], 1);
+      mbar_init(&bars.ofull[s], 1); mbar_init(&bars.done[s], 1);
+    }
+    mbar_init(&bars.ofree, 4);
+    mbar_init(&bars.qfull, 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  if (!sm_ok) return;                                                // past the last tile
+  const PaTile t = sm_tile;
+  const bool bad_len = t.ctx < 0 || t.ctx > (long long)a.bt_stride * kBlockTokens;
+  if (bad_len && tid == 0) set_err(a.err, MBT_DEV_SEQLEN_RANGE);
+  const int last = bad_len ? -1 : t.pos0 + t.tokens - 1;             // the tile's last position
+  const int ntiles = last < 0 ? 0 : last / kPaRows + 1;
+  const size_t qrow0 = (size_t)t.row0 * a.nq + (size_t)h * G;        // row r: qrow0 + (r / G) nq + r % G
+  if (!ntiles) {                                                     // nothing to attend to
+    for (int i = tid; i < t.tokens * G * D; i += kPaThreads)
+      a.out[(qrow0 + (size_t)(i / D / G) * a.nq + i / D % G) * D + i % D] = 0.f;
+    return;
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  unsigned char* kbuf = smem;
+  unsigned char* vbuf = smem + 2 * S::TILE;
+
+  if (warp < 8) {
+    // ---- softmax and output of stream s: row r of the tile per thread ------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaSoftmaxRegs));
+    const int s = warp >> 2, r = 32 * (warp & 3) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const bool live = r < t.tokens * G;
+    const int pos = live ? t.pos0 + r / G : -1;
+    float fac;
+    {
+      // this warpgroup's half of the row's channels: scaled by a power of two
+      // that puts the row's largest in [2^13, 2^14), high and low parts to
+      // tensor memory; fac takes scores back to the log2 domain
+      float x[D / 2];
+      const float4* src = reinterpret_cast<const float4*>(a.q + (qrow0 + (size_t)(r / G) * a.nq + r % G) * D + s * (D / 2));
+      uint32_t big = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float4 v = live ? __ldg(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
+      sm_big[s][r] = big;
+      named_bar(1, 256);
+      big = max(big, sm_big[s ^ 1][r]);
+      const int e = min(120, 140 - (int)(big >> 23));
+      const float up = __int_as_float((e + 127) << 23);
+      fac = 1.4426950408889634f / sqrtf((float)D) * a.k_scale * __int_as_float((127 - e) << 23);
+      fac = fmaxf(fac, 1.2e-38f);                                    // masked scores (-inf) stay -inf
+      if (big >= 0x7f800000u) fac = __int_as_float(0x7fc00000);      // a non-finite query: its row is NaN
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 16) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pa_split(x[c + 2 * i] * up, x[c + 2 * i + 1] * up, hi[i], lo[i]);
+        const uint32_t col = tmem + lanes + kPaQ + (uint32_t)(s * (D / 2) + c) / 2;
+        pa_st8(col, hi);
+        pa_st8(col + D / 2, lo);
+      }
+      pa_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.qfull);
+    }
+    float m = -INFINITY, l = 0.f;
+    int vbase = -1000;                                               // BF16: o is in units of 2^(vbase - 112)
+    float o[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) o[i] = 0.f;
+    const uint32_t sc = tmem + lanes + 128u * s;
+    // 16 columns (one cache block) at a time, the next ones' load in flight
+    auto each_block = [&](auto&& f) {
+      uint32_t va[16], vb[16];
+      tmem_ld16_async(sc, va);
+#pragma unroll 1
+      for (int c = 0; c < kPaRows / 16; c += 2) {
+        tmem_ld_wait16(va);
+        tmem_ld16_async(sc + 16 * c + 16, vb);
+        f(c, va);
+        tmem_ld_wait16(vb);
+        if (c + 2 < kPaRows / 16) tmem_ld16_async(sc + 16 * c + 32, va);
+        f(c + 1, vb);
+      }
+    };
+    auto exponent = [](int e) { return __int_as_float((e + 15) << 23); };   // 2^(e - 112)
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0, j = s; j < ntiles; ++i, j += 2) {
+      ok = __all_sync(0xffffffffu, pa_wait(&bars.sfull[s], i & 1, &sm_stop));
+      if (!ok) break;
+      tc_fence_after();
+      const int lim = pos - j * kPaRows;                             // columns 0..lim are seen
+      const bool masked = __any_sync(0xffffffffu, lim < kPaRows - 1);
+      float mx = -INFINITY;
+      auto block_max = [&](int c, const uint32_t (&v)[16], bool mask) {
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float y = mask && 16 * c + k > lim ? -INFINITY : __uint_as_float(v[k]);
+          x[k & 3] = fmaxf(x[k & 3], y);
+        }
+        const float b = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        mx = fmaxf(mx, S::BF ? b * exponent(sm_kbase[j & 3][c]) : b);
+      };
+      if (masked) each_block([&](int c, const uint32_t (&v)[16]) { block_max(c, v, true); });
+      else each_block([&](int c, const uint32_t (&v)[16]) { block_max(c, v, false); });
+      const float mn = fmaxf(m, mx * fac), mu = mn == -INFINITY ? 0.f : mn;
+      float al = pa_ex2(m - mu);
+      m = mn;
+      l *= al;
+      if (S::BF) {                                                   // V's largest exponent so far
+        ok = __all_sync(0xffffffffu, pa_wait(&bars.vfull[s], i & 1, &sm_stop));
+        if (!ok) break;
+        int top = vbase;
+#pragma unroll
+        for (int c = 0; c < kPaRows / 16; ++c) top = max(top, sm_vbase[s][c]);
+        al *= pa_ex2((float)(vbase - top));
+        vbase = top;
+      }
+      // P = 2^(score - maximum), for BF16 times 2^(block's base - vbase)
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      auto block_exp = [&](int c, const uint32_t (&v)[16], bool mask) {
+        const float fc = S::BF ? fac * exponent(sm_kbase[j & 3][c]) : fac;
+        const float off = S::BF ? (float)max(sm_vbase[s][c] - vbase, -80) : 0.f;   // below: nothing beside the largest
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          float p0 = pa_ex2(fmaf(__uint_as_float(v[k]), fc, off - mu)), p1 = pa_ex2(fmaf(__uint_as_float(v[k + 1]), fc, off - mu));
+          if (mask) {
+            if (16 * c + k > lim) p0 = 0.f;
+            if (16 * c + k + 1 > lim) p1 = 0.f;
+          }
+          part[k & 2] += p0;
+          part[(k & 2) + 1] += p1;
+          pa_split(p0, p1, hi[k / 2], lo[k / 2]);
+        }
+        if (S::BF) {
+          const float back = pa_ex2(-off);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ls[e] = fmaf(part[e], back, ls[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ls[e] += part[e];
+        }
+        pa_st8(sc + 16 * c, hi);                                     // 16 keys: 8 columns high parts, 8 low parts
+        pa_st8(sc + 16 * c + 8, lo);
+      };
+      if (masked) each_block([&](int c, const uint32_t (&v)[16]) { block_exp(c, v, true); });
+      else each_block([&](int c, const uint32_t (&v)[16]) { block_exp(c, v, false); });
+      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      pa_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.pfull[s]);
+      // the tile's P V into the registers
+      ok = __all_sync(0xffffffffu, pa_wait(&bars.ofull[s], i & 1, &sm_stop));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        pa_ld32(tmem + lanes + kPaO + c, v);
+        pa_ld_wait32(v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[c + k] = fmaf(o[c + k], al, __uint_as_float(v[k]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.ofree);
+    }
+    if (!ok && tid == 0) set_err(a.err, MBT_DEV_WAIT_LIMIT);
+
+    // merge the two streams (all products and copies are done): weights from
+    // both states, stream 1's output through shared memory, rows stored whole
+    sm_m[s][r] = m;
+    sm_l[s][r] = l;
+    named_bar(1, 256);
+    const float M = fmaxf(m, sm_m[s ^ 1][r]), mu = M == -INFINITY ? 0.f : M;
+    const float mine = pa_ex2(m - mu);
+    const float L = fmaf(l, mine, sm_l[s ^ 1][r] * pa_ex2(sm_m[s ^ 1][r] - mu));
+    const float wgt = pos < 0 ? 0.f : mine * (a.v_scale / L) * (S::BF ? exponent(max(vbase, 0)) : 1.f);
+    float* stage = reinterpret_cast<float*>(smem) + r * S::LDO;
+    if (s) {
+#pragma unroll
+      for (int i = 0; i < D; i += 4)
+        *reinterpret_cast<float4*>(stage + i) = make_float4(o[i] * wgt, o[i + 1] * wgt, o[i + 2] * wgt, o[i + 3] * wgt);
+    }
+    named_bar(1, 256);
+    if (!s) {
+#pragma unroll
+      for (int i = 0; i < D; i += 4) {
+        float4 v = *reinterpret_cast<const float4*>(stage + i);
+        v.x = fmaf(o[i], wgt, v.x); v.y = fmaf(o[i + 1], wgt, v.y);
+        v.z = fmaf(o[i + 2], wgt, v.z); v.w = fmaf(o[i + 3], wgt, v.w);
+        *reinterpret_cast<float4*>(stage + i) = v;
+      }
+      if (sm_poison) {                                               // rare: non-finite V among the tile's own tokens
+        // from the first block whose values the loader guarded
+        for (int tok = max(0, t.pos0 + 1) / kBlockTokens * kBlockTokens; tok <= pos; ++tok) {
+          int id = a.bt[(size_t)t.seq * a.bt_stride + tok / kBlockTokens];
+          if ((uint32_t)id > (uint32_t)a.num_blocks) id = a.num_blocks;
+          const unsigned char* u = reinterpret_cast<const unsigned char*>(a.vpool) + ((size_t)id * a.nkv + h) * S::UNIT;
+          for (int ch = 0; ch < D; ++ch) {
+            const float v = pa_value<D, KV>(u, tok % kBlockTokens, ch);
+            if (!(fabsf(v) <= 3.0e38f)) stage[ch] += v;
+          }
+        }
+      }
+    }
+    named_bar(1, 256);
+    const float* all = reinterpret_cast<const float*>(smem);
+    for (int i = tid; i < t.tokens * G * (D / 4); i += 256) {
+      const int rr = i / (D / 4), c = 4 * (i % (D / 4));
+      *reinterpret_cast<float4*>(a.out + (qrow0 + (size_t)(rr / G) * a.nq + rr % G) * D + c) =
+          *reinterpret_cast<const float4*>(all + rr * S::LDO + c);
+    }
+  } else if (warp < 12) {
+    // ---- loader: K(0), K(1), V(0), K(2), V(1), ..., 64 tokens (a piece) at a
+    // time, one block per warp; raw data is fetched one piece ahead into the
+    // other register set, block ids (lanes 0..7 hold a tile's) a tile ahead
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaLoadRegs));
+    const int lw = warp - 8, nblk = (t.ctx + kBlockTokens - 1) / kBlockTokens;
+    const int* bt = a.bt + (size_t)t.seq * a.bt_stride;
+    auto ids_of = [&](int j) {
+      const int jb = j * (kPaRows / kBlockTokens) + lane;
+      return lane < kPaRows / kBlockTokens && jb < nblk ? __ldg(bt + jb) : 0;
+    };
+    int idk = ids_of(0), idv = idk, idn = ids_of(1);                 // of the next K tile, the next V tile, the K tile after
+    // the next piece to fetch: half `fh` of K tile fk or V tile fv
+    int fk = 0, fv = 0, fh = 0;
+    bool f_is_k = true;
+    struct Piece { int j, half; bool k; };
+    auto fetch = [&](PaRaw<D, KV>& r) {
+      Piece p{-1, 0, false};
+      if (fv >= ntiles) return p;
+      p.j = f_is_k ? fk : fv; p.half = fh; p.k = f_is_k;
+      const int at = fh * 4 + lw;
+      const bool in = p.j * (kPaRows / kBlockTokens) + at < nblk;
+      int id = __shfl_sync(0xffffffffu, f_is_k ? idk : idv, at);
+      if (in && (uint32_t)id > (uint32_t)a.num_blocks) {             // out of range: the null block
+        if (lane == 0) set_err(a.err, MBT_DEV_BLOCK_RANGE);
+        id = a.num_blocks;
+      }
+      pa_fetch<D, KV>(f_is_k ? a.kpool : a.vpool, (size_t)id * a.nkv + h, in, lane, r);
+      if (fh) {                                                      // on to the next tile of the order
+        if (f_is_k) {
+          ++fk;
+          if (fk > 1) f_is_k = false;                                // K(0), K(1), then V and K in turn
+          if (fk == ntiles) f_is_k = false;
+          idk = idn;
+          idn = ids_of(fk + 1);
+        } else {
+          ++fv;
+          if (fv + 1 < ntiles) { f_is_k = fk < ntiles && fk < fv + 2; }
+          idv = ids_of(fv);
+        }
+      }
+      fh ^= 1;
+      return p;
+    };
+    auto convert = [&](PaRaw<D, KV>& r, const Piece& p) {
+      const int buf = p.j & 1, i = p.j >> 1;
+      if (!p.half && i > 0 &&
+          !__all_sync(0xffffffffu, pa_wait(p.k ? &bars.kempty[buf] : &bars.vempty[buf], (i - 1) & 1, &sm_stop)))
+        return false;
+      const int tok0 = p.j * kPaRows + (p.half * 4 + lw) * kBlockTokens;
+      const bool guard = !p.k && tok0 + kBlockTokens - 1 > t.pos0;
+      int base = 0;
+      const bool found = pa_store<D, KV>(r, (p.k ? kbuf : vbuf) + buf * S::TILE, p.half * 64 + lw * kBlockTokens,
+                                         t.ctx - tok0, guard, lane, &base);
+      if (found) sm_poison = 1;
+      if (S::BF && lane == 0) (p.k ? sm_kbase[p.j & 3] : sm_vbase[buf])[p.half * 4 + lw] = base;
+      if (p.half) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p.k ? &bars.kfull[buf] : &bars.vfull[buf]);
+      }
+      return true;
+    };
+    PaRaw<D, KV> ra, rb;
+    Piece pa = fetch(ra);
+#pragma unroll 1
+    while (pa.j >= 0) {
+      const Piece pb = fetch(rb);
+      if (!convert(ra, pa)) break;
+      if (pb.j < 0) break;
+      pa = fetch(ra);
+      if (!convert(rb, pb)) break;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaIssueRegs));
+    if (warp < 14 && lane == 0) {
+      // ---- MMA issue of stream s ---------------------------------------------
+      const int s = warp - 12;
+      const uint32_t sacc = tmem + 128u * s;
+      constexpr uint32_t id_s = idesc_16(128, kPaRows, 1), id_o = idesc_16(128, D, 1) | (1u << 16);
+      const uint32_t kt = smem_u32(kbuf + s * S::TILE), vt = smem_u32(vbuf + s * S::TILE);
+      bool ok = pa_wait(&bars.qfull, 0, &sm_stop);
+      tc_fence_after();
+      for (int i = 0, j = s; ok && j < ntiles; ++i, j += 2) {
+        if (!(ok = pa_wait(&bars.kfull[s], i & 1, &sm_stop))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 1; part >= 0; --part)                        // low parts, then high
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            pa_mma(sacc, tmem + kPaQ + part * (D / 2) + 8 * k, sw128_desc(kt + (k >> 2) * S::PANEL + (k & 3) * 32), id_s,
+                   part == 0 || k > 0);
+        umma_commit(&bars.sfull[s]);
+        umma_commit(&bars.kempty[s]);
+        if (!(ok = pa_wait(&bars.pfull[s], i & 1, &sm_stop))) break;
+        if (!(ok = pa_wait(&bars.vfull[s], i & 1, &sm_stop))) break;
+        if (j && !(ok = pa_wait(&bars.ofree, (j - 1) & 1, &sm_stop))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 1; part >= 0; --part)
+#pragma unroll
+          for (int k = 0; k < kPaRows / 16; ++k)
+            pa_mma(tmem + kPaO, sacc + 16 * k + 8 * part, pa_mn_desc(vt + k * 2048, S::PANEL), id_o, part == 0 || k > 0);
+        umma_commit(&bars.ofull[s]);
+        umma_commit(&bars.vempty[s]);
+      }
+      umma_commit(&bars.done[s]);
+      mbar_wait(&bars.done[s], 0);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+template <int D, int KV>
+cudaError_t pa_launch(const PromptArgs& a, unsigned grid, cudaStream_t s) {
+  PromptArgs args = a;
+  void* p[] = {&args};
+  return launch_ex((const void*)prompt_attention_kernel<D, KV>, dim3(grid), dim3(kPaThreads), PaShape<D, KV>::SMEM, s, p, false, -1);
+}
+template <int D>
+cudaError_t pa_launch_d(const PromptArgs& a, unsigned grid, cudaStream_t s) {
+  if (a.kv == KV_FP4) return pa_launch<D, KV_FP4>(a, grid, s);
+  return a.kv == KV_E4M3 ? pa_launch<D, KV_E4M3>(a, grid, s) : pa_launch<D, KV_BF16>(a, grid, s);
+}
+template <int D, int KV>
+cudaError_t pa_init() {
+  return cudaFuncSetAttribute((const void*)prompt_attention_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              PaShape<D, KV>::SMEM);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s) {
+  // as many CTAs as there can be tiles: a sequence's last may be short
+  const int T = kPaRows / (a.nq / a.nkv);
+  const long long grid = ((long long)a.n / T + std::min(a.nseq, a.n)) * a.nkv;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return a.d == 64 ? pa_launch_d<64>(a, (unsigned)grid, s) : pa_launch_d<128>(a, (unsigned)grid, s);
+}
+
+cudaError_t prompt_attention_init() {
+  cudaError_t e = pa_init<64, KV_BF16>();
+  if (e == cudaSuccess) e = pa_init<64, KV_E4M3>();
+  if (e == cudaSuccess) e = pa_init<64, KV_FP4>();
+  if (e == cudaSuccess) e = pa_init<128, KV_BF16>();
+  if (e == cudaSuccess) e = pa_init<128, KV_E4M3>();
+  if (e == cudaSuccess) e = pa_init<128, KV_FP4>();
+  return e;
+}
+
+}  // namespace mbt
