@@ -7,13 +7,15 @@
 //
 // A CTA takes 128 query rows: T = 128 / G neighbouring tokens x the G query heads
 // of one KV head, so grouped heads share every K and V tile and a short prompt
-// fills the MMA's rows. Keys come in tiles of 128 tokens, in two streams (even
-// and odd tiles) with a softmax warpgroup each, so that one stream's products
-// run while the other's softmax does; the streams' states merge at the end.
-//   warps 0-3, 4-7   softmax and output of stream 0 and 1, one row per thread
-//   warps 8-11       loader: raw cache blocks to 16-bit tiles in shared memory
-//   warps 12, 13     MMA issue of stream 0 and 1 (one issuing thread reaches an
-//                    M = 128 MMA per ~100 cycles, two reach the pipe's 64)
+// fills the MMA's rows. Keys come in tiles of 128 tokens with two score buffers:
+// while the softmax of tile j runs, the tensor cores do P V of tile j - 1 and the
+// scores of tile j + 1.
+//   warps 0-7        softmax and output: two threads per row, half of a tile's
+//                    columns and half of the output channels each
+//   warps 8-11       K loader: raw cache blocks to FP16 tiles in shared memory
+//   warps 12-15      V loader
+//   warps 16, 17     MMA issue of even and odd tiles (one issuing thread reaches
+//                    an M = 128 MMA per ~100 cycles, two reach the pipe's 64)
 // Accuracy is that of single-token attention: queries and probabilities enter
 // as FP16 high and low parts (2^-22), two MMAs per product, low part first. So
 // the floor is twice the formula's operations at the tensor rate. e4m3 and 4-bit
@@ -28,9 +30,9 @@
 // softmax threads add to fp32 registers (IEEE adds; the tensor core's own
 // accumulation truncates), which also makes the rescaling a fused multiply-add.
 //
-// Tensor memory (512 columns): scores / probabilities of stream 0 and 1 (128
-// each: for 16 keys 8 columns of high and 8 of low parts), P V (128, the streams
-// take turns), queries (D / 2 high, D / 2 low).
+// Tensor memory (512 columns): scores / probabilities of even and odd tiles (128
+// each: for 16 keys 8 columns of high and 8 of low parts), P V (128), queries
+// (D / 2 high, D / 2 low).
 //
 // A value of V that is not finite at a token some rows of the tile do not attend
 // to would reach them as 0 x inf: the loader stores 0 for it and raises a flag,
@@ -46,10 +48,10 @@ namespace mbt {
 namespace {
 
 constexpr int kPaRows = 128;                // query rows and keys per tile
-constexpr int kPaThreads = 512;
-constexpr uint32_t kPaO = 256, kPaQ = 384;  // TMEM columns (stream s's scores at 128 s)
-// registers: 2 x 128 x 192 + 128 x 96 + 128 x 32 = 512 x 128
-constexpr int kPaSoftmaxRegs = 192, kPaLoadRegs = 96, kPaIssueRegs = 32;
+constexpr int kPaThreads = 640;
+constexpr uint32_t kPaO = 256, kPaQ = 384;  // TMEM columns (scores at 0 and 128)
+// registers: 256 x 168 + 256 x 56 + 128 x 32 = 640 x 96, what the block is launched with
+constexpr int kPaSoftmaxRegs = 168, kPaLoadRegs = 56, kPaIssueRegs = 32;
 
 template <int D, int KV>
 struct PaShape {
@@ -62,7 +64,8 @@ struct PaShape {
   static constexpr int PANEL = kPaRows * 128;         // 128 tokens x 64 channels, 128-byte swizzle
   static constexpr int TILE = D / 64 * PANEL;
   static constexpr int LDO = D + 4;                   // output staging row, floats
-  static constexpr int SMEM = 4 * TILE + 1024;
+  static constexpr int STAGES = BF ? 1 : 2;           // raw pairs of blocks of a loader warp
+  static constexpr int SMEM = 4 * TILE + 8 * STAGES * 2 * UNIT + 1024;
   static_assert(kPaRows * LDO * 4 <= 4 * TILE, "the output fits in the drained tiles");
 };
 
@@ -70,11 +73,19 @@ struct PaBars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], done[2], ofree, qfull;
 };
 
+// One try that may sleep in hardware for up to about a millisecond.
+__device__ __forceinline__ bool pa_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(smem_u32(b)), "r"(parity), "r"(1000000u) : "memory");
+  return ok != 0;
+}
 // Bounded wait; once any wait of the CTA has run out, the others give up too.
 __device__ __forceinline__ bool pa_wait(uint64_t* b, uint32_t parity, volatile int* stop) {
-  if (mbar_try(b, parity)) return true;
+  if (pa_try(b, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try(b, parity)) {
+  while (!pa_try(b, parity)) {
     if (*stop) return false;
     if (clock64() - t0 > kTcWaitCycles) { *stop = 1; return false; }
   }
@@ -124,6 +135,12 @@ __device__ __forceinline__ void pa_st8(uint32_t t, const uint32_t (&v)[8]) {
 }
 __device__ __forceinline__ void pa_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One thread of the (converged) warp.
+__device__ __forceinline__ bool pa_elect() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
+}
 // D += A B with A from tensor memory (rows in lanes, two 16-bit K elements per column).
 __device__ __forceinline__ void pa_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -180,9 +197,6 @@ __device__ __forceinline__ bool pa_find(const PromptArgs& a, int T, long long id
 // ---------------------------------------------------------------------------
 // loader
 
-template <int D, int KV>
-struct PaRaw { uint4 c[PaShape<D, KV>::NCH]; uint16_t sc[PaShape<D, KV>::NCH]; };
-
 // A lane's chunk q of a block: panel, token and part of the token's panel row.
 template <int D, int KV>
 __device__ __forceinline__ void pa_chunk(int q, int lane, int& panel, int& row, int& part) {
@@ -193,67 +207,66 @@ __device__ __forceinline__ void pa_chunk(int q, int lane, int& panel, int& row, 
   part = id % S::PP;
 }
 
-template <int D, int KV>
-__device__ __forceinline__ void pa_fetch(const void* pool, size_t unit, bool live, int lane, PaRaw<D, KV>& r) {
-  using S = PaShape<D, KV>;
-  const unsigned char* u = reinterpret_cast<const unsigned char*>(pool) + unit * S::UNIT;
+// Requests one raw block.
+template <int UNIT>
+__device__ __forceinline__ void pa_request(uint32_t dst, const unsigned char* src, int lane) {
 #pragma unroll
-  for (int q = 0; q < S::NCH; ++q) {
-    int panel, row, part;
-    pa_chunk<D, KV>(q, lane, panel, row, part);
-    r.c[q] = live ? __ldg(reinterpret_cast<const uint4*>(u + row * S::ROWB + (panel * S::PP + part) * 16))
-                  : make_uint4(0u, 0u, 0u, 0u);
-    if (KV == KV_FP4)
-      r.sc[q] = live ? __ldg(reinterpret_cast<const uint16_t*>(u + kBlockTokens * (D / 2) + row * (D / 16) + panel * 4 + part * 2))
-                     : (uint16_t)0;
-  }
+  for (int c = 0; c < UNIT; c += 512)
+    if (c + 512 <= UNIT || c + lane * 16 < UNIT)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + c + lane * 16), "l"(src + c + lane * 16) : "memory");
 }
 
-// Exponent base of a BF16 block: FP16 exponent field = BF16 field - base, the
-// largest finite value's at 30. `high` (uniform): some value is not finite.
-template <int NCH>
-__device__ __forceinline__ int pa_block_base(const uint4 (&c)[NCH], bool& high) {
+// A lane's chunk q of a raw block in shared memory.
+template <int D, int KV>
+__device__ __forceinline__ uint4 pa_read(const unsigned char* u, int q, int lane) {
+  using S = PaShape<D, KV>;
+  int panel, row, part;
+  pa_chunk<D, KV>(q, lane, panel, row, part);
+  return *reinterpret_cast<const uint4*>(u + row * S::ROWB + (panel * S::PP + part) * 16);
+}
+
+// Exponent base of a BF16 block's first `keep` tokens: FP16 exponent field =
+// BF16 field - base, the largest finite value's at 30. `high` (uniform): some
+// value is not finite.
+template <int D>
+__device__ __forceinline__ int pa_block_base(const unsigned char* raw, int keep, int lane, bool& high) {
+  using S = PaShape<D, KV_BF16>;
   uint32_t m = 0;
+  for (int pass = 0; pass < 2; ++pass) {                             // the second, rare: finite values only
+    m = 0;
 #pragma unroll
-  for (int q = 0; q < NCH; ++q) {
-    m = __vmaxu2(m, c[q].x & 0x7fff7fffu); m = __vmaxu2(m, c[q].y & 0x7fff7fffu);
-    m = __vmaxu2(m, c[q].z & 0x7fff7fffu); m = __vmaxu2(m, c[q].w & 0x7fff7fffu);
-  }
-  uint32_t top = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
-  high = top >= 0x7f80u;
-  if (high) {                                                        // rare: the largest of the finite values
-    uint32_t f = 0;
+    for (int q = 0; q < S::NCH; ++q) {
+      int panel, row, part;
+      pa_chunk<D, KV_BF16>(q, lane, panel, row, part);
+      const uint4 c = pa_read<D, KV_BF16>(raw, q, lane);
+      uint32_t x[4] = {c.x & 0x7fff7fffu, c.y & 0x7fff7fffu, c.z & 0x7fff7fffu, c.w & 0x7fff7fffu};
+      if (pass) {
 #pragma unroll
-    for (int q = 0; q < NCH; ++q) {
-      const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = w[e] & 0x7fffu, hi = w[e] >> 16 & 0x7fffu;
-        f = max(f, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        for (int e = 0; e < 4; ++e) x[e] &= ~__vcmpgeu2(x[e], 0x7f807f80u);
       }
+      const uint32_t y = __vmaxu2(__vmaxu2(x[0], x[1]), __vmaxu2(x[2], x[3]));
+      m = __vmaxu2(m, row < keep ? y : 0u);
     }
-    top = __reduce_max_sync(0xffffffffu, f);
+    m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
+    if (!pass) high = m >= 0x7f80u;
+    if (!high) break;
   }
-  return max(0, (int)(top >> 7) - 30);
+  return max(0, (int)(m >> 7) - 30);
 }
 
 // Raw chunks to FP16 values in the tile (rows R0 .. R0 + 15). Tokens from `keep`
 // on are stored as zeros; where `guard`, values that are not finite are too, and
 // the return value says whether there were any. BF16: *base receives the
 // block's exponent base.
-template <int D, int KV>
-__device__ __forceinline__ bool pa_store(PaRaw<D, KV>& r, unsigned char* tile, int R0, int keep, bool guard, int lane, int* base) {
+// EDGE: the checks of `keep` and `guard` are compiled in (a branch inside would
+// keep the loop's chains from interleaving).
+template <int D, int KV, bool EDGE>
+__device__ __forceinline__ bool pa_store(const unsigned char* raw, unsigned char* tile, int R0, int keep, bool guard, int lane, int* base) {
   using S = PaShape<D, KV>;
   bool found = false, high = false;
   uint32_t low = 0, shift = 0;
   if (S::BF) {
-#pragma unroll
-    for (int q = 0; q < S::NCH; ++q) {
-      int panel, row, part;
-      pa_chunk<D, KV>(q, lane, panel, row, part);
-      if (row >= keep) r.c[q] = make_uint4(0u, 0u, 0u, 0u);          // nothing past the context sets the exponent
-    }
-    const int b = pa_block_base(r.c, high);
+    const int b = pa_block_base<D>(raw, keep, lane, high);           // nothing past the context sets the exponent
     *base = b;
     low = (uint32_t)((b + 1) << 7) * 0x10001u;                       // smallest magnitude kept: FP16 exponent field 1
     shift = 0u - (uint32_t)(b << 10) * 0x10001u;
@@ -262,13 +275,15 @@ __device__ __forceinline__ bool pa_store(PaRaw<D, KV>& r, unsigned char* tile, i
   for (int q = 0; q < S::NCH; ++q) {
     int panel, row, part;
     pa_chunk<D, KV>(q, lane, panel, row, part);
-    const uint32_t w[4] = {r.c[q].x, r.c[q].y, r.c[q].z, r.c[q].w};
+    const uint4 in = pa_read<D, KV>(raw, q, lane);
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
     const int R = R0 + row;
     unsigned char* dst = tile + panel * S::PANEL + R * 128;
     uint32_t sc[2];
     if (KV == KV_FP4) {
       uint32_t s2;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(r.sc[q]));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(*reinterpret_cast<const uint16_t*>(
+          raw + kBlockTokens * (D / 2) + row * (D / 16) + panel * 4 + part * 2)));
       sc[0] = __byte_perm(s2, s2, 0x1010);
       sc[1] = __byte_perm(s2, s2, 0x3232);
     }
@@ -300,7 +315,7 @@ __device__ __forceinline__ bool pa_store(PaRaw<D, KV>& r, unsigned char* tile, i
           }
         }
       }
-      if (guard) {
+      if (EDGE && guard) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t bad = __vcmpeq2(v[e] & 0x7c007c00u, 0x7c007c00u);
@@ -308,7 +323,7 @@ __device__ __forceinline__ bool pa_store(PaRaw<D, KV>& r, unsigned char* tile, i
           v[e] &= ~bad;
         }
       }
-      if (row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;
+      if (EDGE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;
       *reinterpret_cast<uint4*>(dst + (((part * (S::CPC / 8) + k) ^ (R & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
@@ -337,12 +352,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   unsigned char* smem = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ __align__(8) PaBars bars;
   __shared__ uint32_t tmem_slot, sm_big[2][kPaRows];
-  __shared__ float sm_m[2][kPaRows], sm_l[2][kPaRows];
+  __shared__ float sm_mx[2][2][kPaRows];                             // halves' maxima: even and odd tiles
   __shared__ PaTile sm_tile;
   // BF16 exponent bases of the tiles' blocks; a K tile's outlive its buffer
   __shared__ int sm_ok, sm_poison, sm_kbase[4][8], sm_vbase[2][8];
   __shared__ volatile int sm_stop;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int G = a.nq / a.nkv, T = kPaRows / G, h = (int)(blockIdx.x % (unsigned)a.nkv);
 
   if (warp == 0) {
@@ -357,11 +372,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   }
   if (warp == 1 && lane == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.kfull[s], 4); mbar_init(&bars.vfull[s], 4); mbar_init(&bars.pfull[s], 4);
+      mbar_init(&bars.kfull[s], 4); mbar_init(&bars.vfull[s], 4); mbar_init(&bars.pfull[s], 8);
       mbar_init(&bars.kempty[s], 1); mbar_init(&bars.vempty[s], 1); mbar_init(&bars.sfull[s], 1);
       mbar_init(&bars.ofull[s], 1); mbar_init(&bars.done[s], 1);
     }
-    mbar_init(&bars.ofree, 4);
+    mbar_init(&bars.ofree, 8);
     mbar_init(&bars.qfull, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -378,7 +393,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       a.out[(qrow0 + (size_t)(i / D / G) * a.nq + i / D % G) * D + i % D] = 0.f;
     return;
   }
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -390,7 +405,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   unsigned char* vbuf = smem + 2 * S::TILE;
 
   if (warp < 8) {
-    // ---- softmax and output of stream s: row r of the tile per thread ------
+    // ---- softmax and output: row r of the tile, half `s` of the columns of
+    // every tile and of the output channels ------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaSoftmaxRegs));
     const int s = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -398,7 +414,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     const int pos = live ? t.pos0 + r / G : -1;
     float fac;
     {
-      // this warpgroup's half of the row's channels: scaled by a power of two
+      // this half of the row's channels: scaled by a power of two
       // that puts the row's largest in [2^13, 2^14), high and low parts to
       // tensor memory; fac takes scores back to the log2 domain
       float x[D / 2];
@@ -433,105 +449,21 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.qfull);
     }
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, al_prev = 0.f;
     int vbase = -1000;                                               // BF16: o is in units of 2^(vbase - 112)
-    float o[D];
+    constexpr int C = kPaRows / 2, E = D / 2;                        // columns and channels of this thread
+    float o[E];
 #pragma unroll
-    for (int i = 0; i < D; ++i) o[i] = 0.f;
-    const uint32_t sc = tmem + lanes + 128u * s;
-    // 16 columns (one cache block) at a time, the next ones' load in flight
-    auto each_block = [&](auto&& f) {
-      uint32_t va[16], vb[16];
-      tmem_ld16_async(sc, va);
-#pragma unroll 1
-      for (int c = 0; c < kPaRows / 16; c += 2) {
-        tmem_ld_wait16(va);
-        tmem_ld16_async(sc + 16 * c + 16, vb);
-        f(c, va);
-        tmem_ld_wait16(vb);
-        if (c + 2 < kPaRows / 16) tmem_ld16_async(sc + 16 * c + 32, va);
-        f(c + 1, vb);
-      }
-    };
+    for (int i = 0; i < E; ++i) o[i] = 0.f;
     auto exponent = [](int e) { return __int_as_float((e + 15) << 23); };   // 2^(e - 112)
-    bool ok = true;
-#pragma unroll 1
-    for (int i = 0, j = s; j < ntiles; ++i, j += 2) {
-      ok = __all_sync(0xffffffffu, pa_wait(&bars.sfull[s], i & 1, &sm_stop));
-      if (!ok) break;
-      tc_fence_after();
-      const int lim = pos - j * kPaRows;                             // columns 0..lim are seen
-      const bool masked = __any_sync(0xffffffffu, lim < kPaRows - 1);
-      float mx = -INFINITY;
-      auto block_max = [&](int c, const uint32_t (&v)[16], bool mask) {
-        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float y = mask && 16 * c + k > lim ? -INFINITY : __uint_as_float(v[k]);
-          x[k & 3] = fmaxf(x[k & 3], y);
-        }
-        const float b = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        mx = fmaxf(mx, S::BF ? b * exponent(sm_kbase[j & 3][c]) : b);
-      };
-      if (masked) each_block([&](int c, const uint32_t (&v)[16]) { block_max(c, v, true); });
-      else each_block([&](int c, const uint32_t (&v)[16]) { block_max(c, v, false); });
-      const float mn = fmaxf(m, mx * fac), mu = mn == -INFINITY ? 0.f : mn;
-      float al = pa_ex2(m - mu);
-      m = mn;
-      l *= al;
-      if (S::BF) {                                                   // V's largest exponent so far
-        ok = __all_sync(0xffffffffu, pa_wait(&bars.vfull[s], i & 1, &sm_stop));
-        if (!ok) break;
-        int top = vbase;
-#pragma unroll
-        for (int c = 0; c < kPaRows / 16; ++c) top = max(top, sm_vbase[s][c]);
-        al *= pa_ex2((float)(vbase - top));
-        vbase = top;
-      }
-      // P = 2^(score - maximum), for BF16 times 2^(block's base - vbase)
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
-      auto block_exp = [&](int c, const uint32_t (&v)[16], bool mask) {
-        const float fc = S::BF ? fac * exponent(sm_kbase[j & 3][c]) : fac;
-        const float off = S::BF ? (float)max(sm_vbase[s][c] - vbase, -80) : 0.f;   // below: nothing beside the largest
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          float p0 = pa_ex2(fmaf(__uint_as_float(v[k]), fc, off - mu)), p1 = pa_ex2(fmaf(__uint_as_float(v[k + 1]), fc, off - mu));
-          if (mask) {
-            if (16 * c + k > lim) p0 = 0.f;
-            if (16 * c + k + 1 > lim) p1 = 0.f;
-          }
-          part[k & 2] += p0;
-          part[(k & 2) + 1] += p1;
-          pa_split(p0, p1, hi[k / 2], lo[k / 2]);
-        }
-        if (S::BF) {
-          const float back = pa_ex2(-off);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ls[e] = fmaf(part[e], back, ls[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ls[e] += part[e];
-        }
-        pa_st8(sc + 16 * c, hi);                                     // 16 keys: 8 columns high parts, 8 low parts
-        pa_st8(sc + 16 * c + 8, lo);
-      };
-      if (masked) each_block([&](int c, const uint32_t (&v)[16]) { block_exp(c, v, true); });
-      else each_block([&](int c, const uint32_t (&v)[16]) { block_exp(c, v, false); });
-      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      pa_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.pfull[s]);
-      // the tile's P V into the registers
-      ok = __all_sync(0xffffffffu, pa_wait(&bars.ofull[s], i & 1, &sm_stop));
-      if (!ok) break;
+    // adds tile j's P V, rescaling what is there by `al`
+    auto drain = [&](int j, float al) {
+      if (!__all_sync(0xffffffffu, pa_wait(&bars.ofull[j & 1], (j >> 1) & 1, &sm_stop))) return false;
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < E; c += 32) {
         uint32_t v[32];
-        pa_ld32(tmem + lanes + kPaO + c, v);
+        pa_ld32(tmem + lanes + kPaO + s * E + c, v);
         pa_ld_wait32(v);
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[c + k] = fmaf(o[c + k], al, __uint_as_float(v[k]));
@@ -539,43 +471,104 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.ofree);
+      return true;
+    };
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; j < ntiles; ++j) {
+      ok = __all_sync(0xffffffffu, pa_wait(&bars.sfull[j & 1], (j >> 1) & 1, &sm_stop));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sc = tmem + lanes + 128u * (j & 1) + s * C;
+      const int lim = pos - j * kPaRows - s * C;                     // columns 0..lim are seen
+      const bool masked = __any_sync(0xffffffffu, lim < C - 1);
+      uint32_t v[2][32];
+      pa_ld32(sc, v[0]);
+      pa_ld32(sc + 32, v[1]);
+      pa_ld_wait32(v[0]);
+      pa_ld_wait32(v[1]);
+      if (masked) {
+#pragma unroll
+        for (int k = 0; k < C; ++k) if (k > lim) v[k / 32][k % 32] = 0xff800000u;
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < C; c += 16) {                              // 16 columns: a cache block
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = c; k < c + 16; ++k) x[k & 3] = fmaxf(x[k & 3], __uint_as_float(v[k / 32][k % 32]));
+        const float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        mx = fmaxf(mx, S::BF ? y * exponent(sm_kbase[j & 3][(s * C + c) / 16]) : y);
+      }
+      sm_mx[j & 1][s][r] = mx;
+      named_bar(1, 256);
+      mx = fmaxf(mx, sm_mx[j & 1][s ^ 1][r]);
+      const float mn = fmaxf(m, mx * fac), mu = mn == -INFINITY ? 0.f : mn;
+      float al = pa_ex2(m - mu);
+      m = mn;
+      l *= al;
+      if (S::BF) {                                                   // V's largest exponent so far
+        ok = __all_sync(0xffffffffu, pa_wait(&bars.vfull[j & 1], (j >> 1) & 1, &sm_stop));
+        if (!ok) break;
+        int top = vbase;
+#pragma unroll
+        for (int c = 0; c < kPaRows / 16; ++c) top = max(top, sm_vbase[j & 1][c]);
+        al *= pa_ex2((float)(vbase - top));
+        vbase = top;
+      }
+      // P = 2^(score - maximum), for BF16 times 2^(block's base - vbase)
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < C; c += 16) {
+        const int blk = (s * C + c) / 16;
+        const float fc = S::BF ? fac * exponent(sm_kbase[j & 3][blk]) : fac;
+        const float off = S::BF ? (float)max(sm_vbase[j & 1][blk] - vbase, -80) : 0.f;   // below: nothing beside the largest
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const float p0 = pa_ex2(fmaf(__uint_as_float(v[c / 32][(c + k) % 32]), fc, off - mu));
+          const float p1 = pa_ex2(fmaf(__uint_as_float(v[c / 32][(c + k + 1) % 32]), fc, off - mu));
+          part[k & 2] += p0;
+          part[(k & 2) + 1] += p1;
+          pa_split(p0, p1, hi[k / 2], lo[k / 2]);
+        }
+        const float back = S::BF ? pa_ex2(-off) : 1.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ls[e] = S::BF ? fmaf(part[e], back, ls[e]) : ls[e] + part[e];
+        pa_st8(sc + c, hi);                                          // 16 keys: 8 columns high parts, 8 low parts
+        pa_st8(sc + c + 8, lo);
+      }
+      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      pa_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.pfull[j & 1]);
+      // the previous tile's P V, done meanwhile
+      if (j && !(ok = drain(j - 1, al_prev))) break;
+      al_prev = al;
     }
+    if (ok) ok = drain(ntiles - 1, al_prev);
     if (!ok && tid == 0) set_err(a.err, MBT_DEV_WAIT_LIMIT);
 
-    // merge the two streams (all products and copies are done): weights from
-    // both states, stream 1's output through shared memory, rows stored whole
-    sm_m[s][r] = m;
-    sm_l[s][r] = l;
+    // all products and copies are done: rows through the drained tiles, stored whole
+    sm_mx[0][s][r] = l;
     named_bar(1, 256);
-    const float M = fmaxf(m, sm_m[s ^ 1][r]), mu = M == -INFINITY ? 0.f : M;
-    const float mine = pa_ex2(m - mu);
-    const float L = fmaf(l, mine, sm_l[s ^ 1][r] * pa_ex2(sm_m[s ^ 1][r] - mu));
-    const float wgt = pos < 0 ? 0.f : mine * (a.v_scale / L) * (S::BF ? exponent(max(vbase, 0)) : 1.f);
-    float* stage = reinterpret_cast<float*>(smem) + r * S::LDO;
-    if (s) {
+    const float L = l + sm_mx[0][s ^ 1][r];
+    const float wgt = pos < 0 ? 0.f : a.v_scale / L * (S::BF ? exponent(max(vbase, 0)) : 1.f);
+    float* stage = reinterpret_cast<float*>(smem) + r * S::LDO + s * E;
 #pragma unroll
-      for (int i = 0; i < D; i += 4)
-        *reinterpret_cast<float4*>(stage + i) = make_float4(o[i] * wgt, o[i + 1] * wgt, o[i + 2] * wgt, o[i + 3] * wgt);
-    }
-    named_bar(1, 256);
-    if (!s) {
-#pragma unroll
-      for (int i = 0; i < D; i += 4) {
-        float4 v = *reinterpret_cast<const float4*>(stage + i);
-        v.x = fmaf(o[i], wgt, v.x); v.y = fmaf(o[i + 1], wgt, v.y);
-        v.z = fmaf(o[i + 2], wgt, v.z); v.w = fmaf(o[i + 3], wgt, v.w);
-        *reinterpret_cast<float4*>(stage + i) = v;
-      }
-      if (sm_poison) {                                               // rare: non-finite V among the tile's own tokens
-        // from the first block whose values the loader guarded
-        for (int tok = max(0, t.pos0 + 1) / kBlockTokens * kBlockTokens; tok <= pos; ++tok) {
-          int id = a.bt[(size_t)t.seq * a.bt_stride + tok / kBlockTokens];
-          if ((uint32_t)id > (uint32_t)a.num_blocks) id = a.num_blocks;
-          const unsigned char* u = reinterpret_cast<const unsigned char*>(a.vpool) + ((size_t)id * a.nkv + h) * S::UNIT;
-          for (int ch = 0; ch < D; ++ch) {
-            const float v = pa_value<D, KV>(u, tok % kBlockTokens, ch);
-            if (!(fabsf(v) <= 3.0e38f)) stage[ch] += v;
-          }
+    for (int i = 0; i < E; i += 4)
+      *reinterpret_cast<float4*>(stage + i) = make_float4(o[i] * wgt, o[i + 1] * wgt, o[i + 2] * wgt, o[i + 3] * wgt);
+    if (sm_poison) {                                                 // rare: non-finite V among the tile's own tokens
+      // from the first block whose values the loader guarded
+      for (int tok = max(0, t.pos0 + 1) / kBlockTokens * kBlockTokens; tok <= pos; ++tok) {
+        int id = a.bt[(size_t)t.seq * a.bt_stride + tok / kBlockTokens];
+        if ((uint32_t)id > (uint32_t)a.num_blocks) id = a.num_blocks;
+        const unsigned char* u = reinterpret_cast<const unsigned char*>(a.vpool) + ((size_t)id * a.nkv + h) * S::UNIT;
+        for (int ch = 0; ch < E; ++ch) {
+          const float x = pa_value<D, KV>(u, tok % kBlockTokens, s * E + ch);
+          if (!(fabsf(x) <= 3.0e38f)) stage[ch] += x;
         }
       }
     }
@@ -586,120 +579,116 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       *reinterpret_cast<float4*>(a.out + (qrow0 + (size_t)(rr / G) * a.nq + rr % G) * D + c) =
           *reinterpret_cast<const float4*>(all + rr * S::LDO + c);
     }
-  } else if (warp < 12) {
-    // ---- loader: K(0), K(1), V(0), K(2), V(1), ..., 64 tokens (a piece) at a
-    // time, one block per warp; raw data is fetched one piece ahead into the
-    // other register set, block ids (lanes 0..7 hold a tile's) a tile ahead
+  } else if (warp < 16) {
+    // ---- loaders: two blocks of every K (or V) tile per warp; raw blocks are
+    // requested as their stage of the ring falls free, block ids (lanes 0..7
+    // hold a tile's) a tile before that
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaLoadRegs));
-    const int lw = warp - 8, nblk = (t.ctx + kBlockTokens - 1) / kBlockTokens;
+    const bool is_k = warp < 12;
+    const int lw = warp & 3, nblk = (t.ctx + kBlockTokens - 1) / kBlockTokens;
+    constexpr int BT = kPaRows / kBlockTokens;
     const int* bt = a.bt + (size_t)t.seq * a.bt_stride;
-    auto ids_of = [&](int j) {
-      const int jb = j * (kPaRows / kBlockTokens) + lane;
-      return lane < kPaRows / kBlockTokens && jb < nblk ? __ldg(bt + jb) : 0;
-    };
-    int idk = ids_of(0), idv = idk, idn = ids_of(1);                 // of the next K tile, the next V tile, the K tile after
-    // the next piece to fetch: half `fh` of K tile fk or V tile fv
-    int fk = 0, fv = 0, fh = 0;
-    bool f_is_k = true;
-    struct Piece { int j, half; bool k; };
-    auto fetch = [&](PaRaw<D, KV>& r) {
-      Piece p{-1, 0, false};
-      if (fv >= ntiles) return p;
-      p.j = f_is_k ? fk : fv; p.half = fh; p.k = f_is_k;
-      const int at = fh * 4 + lw;
-      const bool in = p.j * (kPaRows / kBlockTokens) + at < nblk;
-      int id = __shfl_sync(0xffffffffu, f_is_k ? idk : idv, at);
-      if (in && (uint32_t)id > (uint32_t)a.num_blocks) {             // out of range: the null block
-        if (lane == 0) set_err(a.err, MBT_DEV_BLOCK_RANGE);
-        id = a.num_blocks;
-      }
-      pa_fetch<D, KV>(f_is_k ? a.kpool : a.vpool, (size_t)id * a.nkv + h, in, lane, r);
-      if (fh) {                                                      // on to the next tile of the order
-        if (f_is_k) {
-          ++fk;
-          if (fk > 1) f_is_k = false;                                // K(0), K(1), then V and K in turn
-          if (fk == ntiles) f_is_k = false;
-          idk = idn;
-          idn = ids_of(fk + 1);
-        } else {
-          ++fv;
-          if (fv + 1 < ntiles) { f_is_k = fk < ntiles && fk < fv + 2; }
-          idv = ids_of(fv);
+    const unsigned char* pool = reinterpret_cast<const unsigned char*>(is_k ? a.kpool : a.vpool) + (size_t)h * S::UNIT;
+    unsigned char* ring = smem + 4 * S::TILE + (warp - 8) * S::STAGES * 2 * S::UNIT;
+    uint64_t* full = is_k ? bars.kfull : bars.vfull;
+    uint64_t* empty = is_k ? bars.kempty : bars.vempty;
+    auto ids_of = [&](int j) { return lane < BT && j * BT + lane < nblk ? __ldg(bt + j * BT + lane) : 0; };
+    int ids = ids_of(0);
+    auto request = [&](int j) {
+      if (j < ntiles) {
+        if (lane < BT && j * BT + lane < nblk && (uint32_t)ids > (uint32_t)a.num_blocks) {   // out of range: the null block
+          set_err(a.err, MBT_DEV_BLOCK_RANGE);
+          ids = a.num_blocks;
         }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int at = half * 4 + lw;
+          const unsigned char* src = pool + (size_t)__shfl_sync(0xffffffffu, ids, at) * a.nkv * S::UNIT;
+          if (j * BT + at < nblk) pa_request<S::UNIT>(smem_u32(ring) + ((j % S::STAGES) * 2 + half) * S::UNIT, src, lane);
+        }
+        ids = ids_of(j + 1);
       }
-      fh ^= 1;
-      return p;
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto convert = [&](PaRaw<D, KV>& r, const Piece& p) {
-      const int buf = p.j & 1, i = p.j >> 1;
-      if (!p.half && i > 0 &&
-          !__all_sync(0xffffffffu, pa_wait(p.k ? &bars.kempty[buf] : &bars.vempty[buf], (i - 1) & 1, &sm_stop)))
-        return false;
-      const int tok0 = p.j * kPaRows + (p.half * 4 + lw) * kBlockTokens;
-      const bool guard = !p.k && tok0 + kBlockTokens - 1 > t.pos0;
-      int base = 0;
-      const bool found = pa_store<D, KV>(r, (p.k ? kbuf : vbuf) + buf * S::TILE, p.half * 64 + lw * kBlockTokens,
-                                         t.ctx - tok0, guard, lane, &base);
-      if (found) sm_poison = 1;
-      if (S::BF && lane == 0) (p.k ? sm_kbase[p.j & 3] : sm_vbase[buf])[p.half * 4 + lw] = base;
-      if (p.half) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p.k ? &bars.kfull[buf] : &bars.vfull[buf]);
-      }
-      return true;
-    };
-    PaRaw<D, KV> ra, rb;
-    Piece pa = fetch(ra);
+#pragma unroll
+    for (int j = 0; j < S::STAGES; ++j) request(j);
 #pragma unroll 1
-    while (pa.j >= 0) {
-      const Piece pb = fetch(rb);
-      if (!convert(ra, pa)) break;
-      if (pb.j < 0) break;
-      pa = fetch(ra);
-      if (!convert(rb, pb)) break;
+    for (int j = 0; j < ntiles; ++j) {
+      const int buf = j & 1, i = j >> 1;
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
+      __syncwarp();
+      if (i > 0 && !__all_sync(0xffffffffu, pa_wait(&empty[buf], (i - 1) & 1, &sm_stop))) break;
+      unsigned char* tile = (is_k ? kbuf : vbuf) + buf * S::TILE;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int at = half * 4 + lw, tok0 = j * kPaRows + at * kBlockTokens;
+        const bool guard = !is_k && tok0 + kBlockTokens - 1 > t.pos0;
+        const unsigned char* raw = ring + ((j % S::STAGES) * 2 + half) * S::UNIT;
+        int base = 0;
+        if (guard || t.ctx - tok0 < kBlockTokens) {
+          if (pa_store<D, KV, true>(raw, tile, at * kBlockTokens, t.ctx - tok0, guard, lane, &base)) sm_poison = 1;
+        } else {
+          pa_store<D, KV, false>(raw, tile, at * kBlockTokens, kBlockTokens, false, lane, &base);
+        }
+        if (S::BF && lane == 0) (is_k ? sm_kbase[j & 3] : sm_vbase[buf])[at] = base;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();                                                  // every lane has read the raw blocks
+      if (lane == 0) mbar_arrive(&full[buf]);
+      request(j + S::STAGES);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaIssueRegs));
-    if (warp < 14 && lane == 0) {
-      // ---- MMA issue of stream s ---------------------------------------------
-      const int s = warp - 12;
+    if (warp < 18) {
+      // ---- MMA issue of tiles s, s + 2, ...: the whole warp follows, one elected
+      // thread issues (with uniform control flow the descriptors stay in uniform
+      // registers) ----------------------------------------------------------------
+      const int s = warp - 16;
       const uint32_t sacc = tmem + 128u * s;
       constexpr uint32_t id_s = idesc_16(128, kPaRows, 1), id_o = idesc_16(128, D, 1) | (1u << 16);
-      const uint32_t kt = smem_u32(kbuf + s * S::TILE), vt = smem_u32(vbuf + s * S::TILE);
-      bool ok = pa_wait(&bars.qfull, 0, &sm_stop);
+      const uint64_t kt = sw128_desc(smem_u32(kbuf) + s * S::TILE), vt = pa_mn_desc(smem_u32(vbuf) + s * S::TILE, S::PANEL);
+      bool ok = __all_sync(0xffffffffu, pa_wait(&bars.qfull, 0, &sm_stop));
       tc_fence_after();
+#pragma unroll 1
       for (int i = 0, j = s; ok && j < ntiles; ++i, j += 2) {
-        if (!(ok = pa_wait(&bars.kfull[s], i & 1, &sm_stop))) break;
+        if (!(ok = __all_sync(0xffffffffu, pa_wait(&bars.kfull[s], i & 1, &sm_stop)))) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int part = 1; part >= 0; --part)                        // low parts, then high
+        if (pa_elect()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            pa_mma(sacc, tmem + kPaQ + part * (D / 2) + 8 * k, sw128_desc(kt + (k >> 2) * S::PANEL + (k & 3) * 32), id_s,
-                   part == 0 || k > 0);
-        umma_commit(&bars.sfull[s]);
-        umma_commit(&bars.kempty[s]);
-        if (!(ok = pa_wait(&bars.pfull[s], i & 1, &sm_stop))) break;
-        if (!(ok = pa_wait(&bars.vfull[s], i & 1, &sm_stop))) break;
-        if (j && !(ok = pa_wait(&bars.ofree, (j - 1) & 1, &sm_stop))) break;
+          for (int part = 1; part >= 0; --part)                      // low parts, then high
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              pa_mma(sacc, tmem + kPaQ + part * (D / 2) + 8 * k, kt + (((k >> 2) * S::PANEL + (k & 3) * 32) >> 4), id_s,
+                     part == 0 || k > 0);
+          umma_commit(&bars.sfull[s]);
+          umma_commit(&bars.kempty[s]);
+        }
+        __syncwarp();
+        ok = pa_wait(&bars.pfull[s], i & 1, &sm_stop) && pa_wait(&bars.vfull[s], i & 1, &sm_stop) &&
+             (!j || pa_wait(&bars.ofree, (j - 1) & 1, &sm_stop));
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int part = 1; part >= 0; --part)
+        if (pa_elect()) {
 #pragma unroll
-          for (int k = 0; k < kPaRows / 16; ++k)
-            pa_mma(tmem + kPaO, sacc + 16 * k + 8 * part, pa_mn_desc(vt + k * 2048, S::PANEL), id_o, part == 0 || k > 0);
-        umma_commit(&bars.ofull[s]);
-        umma_commit(&bars.vempty[s]);
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int k = 0; k < kPaRows / 16; ++k)
+              pa_mma(tmem + kPaO, sacc + 16 * k + 8 * part, vt + ((k * 2048) >> 4), id_o, part == 0 || k > 0);
+          umma_commit(&bars.ofull[s]);
+          umma_commit(&bars.vempty[s]);
+        }
+        __syncwarp();
       }
-      umma_commit(&bars.done[s]);
+      if (pa_elect()) umma_commit(&bars.done[s]);
+      __syncwarp();
       mbar_wait(&bars.done[s], 0);
     }
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
