@@ -369,31 +369,18 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       sm_stop = 0;
       sm_poison = 0;
     }
-  }
-  if (warp == 1 && lane == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.kfull[s], 4); mbar_init(&bars.vfull[s], 4); mbar_init(&bars.pfull[s], 8);
-      mbar_init(&bars.kempty[s], 1); mbar_init(&bars.vempty[s], 1); mbar_init(&bars.sfull[s], 1);
-      mbar_init(&bars.ofull[s], 1); mbar_init(&bars.done[s], 1);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&bars.kfull[s], 4); mbar_init(&bars.vfull[s], 4); mbar_init(&bars.pfull[s], 8);
+        mbar_init(&bars.kempty[s], 1); mbar_init(&bars.vempty[s], 1); mbar_init(&bars.sfull[s], 1);
+        mbar_init(&bars.ofull[s], 1); mbar_init(&bars.done[s], 1);
+      }
+      mbar_init(&bars.ofree, 8);
+      mbar_init(&bars.qfull, 8);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    mbar_init(&bars.ofree, 8);
-    mbar_init(&bars.qfull, 8);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
-  if (!sm_ok) return;                                                // past the last tile
-  const PaTile t = sm_tile;
-  const bool bad_len = t.ctx < 0 || t.ctx > (long long)a.bt_stride * kBlockTokens;
-  if (bad_len && tid == 0) set_err(a.err, MBT_DEV_SEQLEN_RANGE);
-  const int last = bad_len ? -1 : t.pos0 + t.tokens - 1;             // the tile's last position
-  const int ntiles = last < 0 ? 0 : last / kPaRows + 1;
-  const size_t qrow0 = (size_t)t.row0 * a.nq + (size_t)h * G;        // row r: qrow0 + (r / G) nq + r % G
-  if (!ntiles) {                                                     // nothing to attend to
-    for (int i = tid; i < t.tokens * G * D; i += kPaThreads)
-      a.out[(qrow0 + (size_t)(i / D / G) * a.nq + i / D % G) * D + i % D] = 0.f;
-    return;
-  }
-  if (warp == 16) {
+  } else if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -401,6 +388,23 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  auto release = [&]() {
+    if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  };
+  if (!sm_ok) { release(); return; }                                 // past the last tile
+  const PaTile t = sm_tile;
+  const bool bad_len = t.ctx < 0 || t.ctx > (long long)a.bt_stride * kBlockTokens;
+  if (bad_len && tid == 0) set_err(a.err, MBT_DEV_SEQLEN_RANGE);
+  const int last = bad_len ? -1 : t.pos0 + t.tokens - 1;             // the tile's last position
+  const int ntiles = last < 0 ? 0 : last / kPaRows + 1;
+  // row r of the tile is row r / G nq + r % G from here: a token's G heads are neighbours
+  const size_t qrow0 = (size_t)t.row0 * a.nq + (size_t)h * G;
+  if (!ntiles) {                                                     // nothing to attend to
+    for (int i = tid; i < t.tokens * G * D; i += kPaThreads)
+      a.out[(qrow0 + (size_t)(i / D / G) * a.nq + i / D % G) * D + i % D] = 0.f;
+    release();
+    return;
+  }
   unsigned char* kbuf = smem;
   unsigned char* vbuf = smem + 2 * S::TILE;
 
@@ -410,19 +414,35 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaSoftmaxRegs));
     const int s = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const bool live = r < t.tokens * G;
-    const int pos = live ? t.pos0 + r / G : -1;
+    // r / G for r < 128 and G <= 16 by a multiplication (exact: 128 * 16 < 2^16)
+    const uint32_t inv = (0x10000u + G - 1) / G;
+    auto row_of = [&](int rr) { return qrow0 + rr + (size_t)((rr * inv) >> 16) * (a.nq - G); };
+    const int rows = t.tokens * G;
+    const int pos = r < rows ? t.pos0 + (int)((r * inv) >> 16) : -1;
+    constexpr int RL = D / 4, RW = 32 / RL;                          // lanes of a row's 16-byte chunks, rows per warp and access
     float fac;
     {
-      // this half of the row's channels: scaled by a power of two
-      // that puts the row's largest in [2^13, 2^14), high and low parts to
-      // tensor memory; fac takes scores back to the log2 domain
+      // the query rows, whole rows at a time, into the V tiles' place (the V
+      // loader waits), chunks swizzled by row
+#pragma unroll 4
+      for (int i = 0; i < kPaRows / 8; i += RW) {
+        const int rr = warp * (kPaRows / 8) + i + lane / RL, ch = lane % RL;
+        if (rr < rows)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                       ::"r"(smem_u32(vbuf) + rr * D * 4 + ((ch ^ (rr & 7)) << 4)),
+                       "l"(a.q + row_of(rr) * D + ch * 4) : "memory");
+      }
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+      named_bar(1, 256);
+      // this half of the row's channels: scaled by a power of two that puts the
+      // row's largest in [2^13, 2^14), high and low parts to tensor memory; fac
+      // takes scores back to the log2 domain
       float x[D / 2];
-      const float4* src = reinterpret_cast<const float4*>(a.q + (qrow0 + (size_t)(r / G) * a.nq + r % G) * D + s * (D / 2));
       uint32_t big = 0;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        const float4 v = live ? __ldg(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 v = r >= rows ? make_float4(0.f, 0.f, 0.f, 0.f)
+            : *reinterpret_cast<const float4*>(vbuf + r * D * 4 + (((s * (D / 8) + i) ^ (r & 7)) << 4));
         x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
       }
 #pragma unroll
@@ -573,11 +593,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       }
     }
     named_bar(1, 256);
-    const float* all = reinterpret_cast<const float*>(smem);
-    for (int i = tid; i < t.tokens * G * (D / 4); i += 256) {
-      const int rr = i / (D / 4), c = 4 * (i % (D / 4));
-      *reinterpret_cast<float4*>(a.out + (qrow0 + (size_t)(rr / G) * a.nq + rr % G) * D + c) =
-          *reinterpret_cast<const float4*>(all + rr * S::LDO + c);
+#pragma unroll 4
+    for (int i = 0; i < kPaRows / 8; i += RW) {
+      const int rr = warp * (kPaRows / 8) + i + lane / RL, ch = lane % RL;
+      if (rr < rows)
+        *reinterpret_cast<float4*>(a.out + row_of(rr) * D + ch * 4) =
+            *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + rr * S::LDO + ch * 4);
     }
   } else if (warp < 16) {
     // ---- loaders: two blocks of every K (or V) tile per warp; raw blocks are
@@ -612,8 +633,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     };
 #pragma unroll
     for (int j = 0; j < S::STAGES; ++j) request(j);
+    const bool go = is_k || __all_sync(0xffffffffu, pa_wait(&bars.qfull, 0, &sm_stop));   // the queries sit in V's place
 #pragma unroll 1
-    for (int j = 0; j < ntiles; ++j) {
+    for (int j = 0; go && j < ntiles; ++j) {
       const int buf = j & 1, i = j >> 1;
       asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
       __syncwarp();
@@ -688,10 +710,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-  }
+  tc_fence_after();
+  release();
 }
 
 template <int D, int KV>
