@@ -50,8 +50,7 @@ namespace {
 constexpr int kPaRows = 128;                // query rows and keys per tile
 constexpr int kPaThreads = 640;
 constexpr uint32_t kPaO = 256, kPaQ = 384;  // TMEM columns (scores at 0 and 128)
-// registers: 256 x 168 + 256 x 56 + 128 x 32 = 640 x 96, what the block is launched with
-constexpr int kPaSoftmaxRegs = 168, kPaLoadRegs = 56, kPaIssueRegs = 32;
+constexpr int kPaIssueRegs = 32;
 
 template <int D, int KV>
 struct PaShape {
@@ -63,6 +62,9 @@ struct PaShape {
   static constexpr int NCH = kBlockTokens * (D / CPC) / 32;   // chunks of a block per lane
   static constexpr int PANEL = kPaRows * 128;         // 128 tokens x 64 channels, 128-byte swizzle
   static constexpr int TILE = D / 64 * PANEL;
+  // registers: 256 x 168 + 256 x 56 + 128 x 32 (BF16: 160 and 64, its loader holds
+  // a raw block) = 640 x 96, what the block is launched with
+  static constexpr int SOFTMAX_REGS = BF ? 160 : 168, LOAD_REGS = BF ? 64 : 56;
   static constexpr int LDO = D + 4;                   // output staging row, floats
   static constexpr int STAGES = BF ? 1 : 2;           // raw pairs of blocks of a loader warp
   static constexpr int SMEM = 4 * TILE + 8 * STAGES * 2 * UNIT + 1024;
@@ -96,6 +98,32 @@ __device__ __forceinline__ float pa_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 values per register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pa_pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 pa_unpair(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t pa_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pa_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float pa_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // x = hi + lo as FP16 pairs (first value in the low half).
 __device__ __forceinline__ void pa_split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
@@ -216,36 +244,51 @@ __device__ __forceinline__ void pa_request(uint32_t dst, const unsigned char* sr
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + c + lane * 16), "l"(src + c + lane * 16) : "memory");
 }
 
-// A lane's chunk q of a raw block in shared memory.
+// A lane's chunks of a raw block.
 template <int D, int KV>
-__device__ __forceinline__ uint4 pa_read(const unsigned char* u, int q, int lane) {
-  using S = PaShape<D, KV>;
-  int panel, row, part;
-  pa_chunk<D, KV>(q, lane, panel, row, part);
-  return *reinterpret_cast<const uint4*>(u + row * S::ROWB + (panel * S::PP + part) * 16);
-}
+struct PaRaw {
+  uint4 c[PaShape<D, KV>::NCH];
+  uint16_t sc[PaShape<D, KV>::NCH];                                  // 4-bit: the two groups' scales
+  __device__ __forceinline__ void read(const unsigned char* u, int lane) {
+    using S = PaShape<D, KV>;
+#pragma unroll
+    for (int q = 0; q < S::NCH; ++q) {
+      int panel, row, part;
+      pa_chunk<D, KV>(q, lane, panel, row, part);
+      c[q] = *reinterpret_cast<const uint4*>(u + row * S::ROWB + (panel * S::PP + part) * 16);
+      if (KV == KV_FP4)
+        sc[q] = *reinterpret_cast<const uint16_t*>(u + kBlockTokens * (D / 2) + row * (D / 16) + panel * 4 + part * 2);
+    }
+  }
+};
 
+__device__ __forceinline__ uint32_t pa_max2(uint32_t a, uint32_t b) {   // of two unsigned 16-bit pairs
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Exponent base of a BF16 block's first `keep` tokens: FP16 exponent field =
 // BF16 field - base, the largest finite value's at 30. `high` (uniform): some
 // value is not finite.
 template <int D>
-__device__ __forceinline__ int pa_block_base(const unsigned char* raw, int keep, int lane, bool& high) {
+__device__ __forceinline__ int pa_block_base(const PaRaw<D, KV_BF16>& raw, int keep, int lane, bool& high) {
   using S = PaShape<D, KV_BF16>;
   uint32_t m = 0;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {                             // the second, rare: finite values only
     m = 0;
 #pragma unroll
     for (int q = 0; q < S::NCH; ++q) {
       int panel, row, part;
       pa_chunk<D, KV_BF16>(q, lane, panel, row, part);
-      const uint4 c = pa_read<D, KV_BF16>(raw, q, lane);
+      const uint4 c = raw.c[q];
       uint32_t x[4] = {c.x & 0x7fff7fffu, c.y & 0x7fff7fffu, c.z & 0x7fff7fffu, c.w & 0x7fff7fffu};
       if (pass) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] &= ~__vcmpgeu2(x[e], 0x7f807f80u);
       }
-      const uint32_t y = __vmaxu2(__vmaxu2(x[0], x[1]), __vmaxu2(x[2], x[3]));
-      m = __vmaxu2(m, row < keep ? y : 0u);
+      const uint32_t y = pa_max2(pa_max2(x[0], x[1]), pa_max2(x[2], x[3]));
+      m = pa_max2(m, row < keep ? y : 0u);
     }
     m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
     if (!pass) high = m >= 0x7f80u;
@@ -256,34 +299,27 @@ __device__ __forceinline__ int pa_block_base(const unsigned char* raw, int keep,
 
 // Raw chunks to FP16 values in the tile (rows R0 .. R0 + 15). Tokens from `keep`
 // on are stored as zeros; where `guard`, values that are not finite are too, and
-// the return value says whether there were any. BF16: *base receives the
-// block's exponent base.
-// EDGE: the checks of `keep` and `guard` are compiled in (a branch inside would
-// keep the loop's chains from interleaving).
+// the return value says whether there were any. base: a BF16 block's.
+// EDGE: for blocks that need `keep` or `guard` or (BF16) hold values that are
+// not finite; without it a block is converted with no branch inside, which
+// would keep the loop's chains from interleaving.
 template <int D, int KV, bool EDGE>
-__device__ __forceinline__ bool pa_store(const unsigned char* raw, unsigned char* tile, int R0, int keep, bool guard, int lane, int* base) {
+__device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char* tile, int R0, int keep, bool guard, int lane, int base) {
   using S = PaShape<D, KV>;
-  bool found = false, high = false;
-  uint32_t low = 0, shift = 0;
-  if (S::BF) {
-    const int b = pa_block_base<D>(raw, keep, lane, high);           // nothing past the context sets the exponent
-    *base = b;
-    low = (uint32_t)((b + 1) << 7) * 0x10001u;                       // smallest magnitude kept: FP16 exponent field 1
-    shift = 0u - (uint32_t)(b << 10) * 0x10001u;
-  }
+  bool found = false;
+  const uint32_t low = (uint32_t)((base + 1) << 7) * 0x10001u;       // BF16: smallest magnitude kept, FP16 exponent field 1
+  const uint32_t shift = 0u - (uint32_t)(base << 10) * 0x10001u;
 #pragma unroll
   for (int q = 0; q < S::NCH; ++q) {
     int panel, row, part;
     pa_chunk<D, KV>(q, lane, panel, row, part);
-    const uint4 in = pa_read<D, KV>(raw, q, lane);
-    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    const uint32_t w[4] = {raw.c[q].x, raw.c[q].y, raw.c[q].z, raw.c[q].w};
     const int R = R0 + row;
     unsigned char* dst = tile + panel * S::PANEL + R * 128;
     uint32_t sc[2];
     if (KV == KV_FP4) {
       uint32_t s2;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(*reinterpret_cast<const uint16_t*>(
-          raw + kBlockTokens * (D / 2) + row * (D / 16) + panel * 4 + part * 2)));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(raw.sc[q]));
       sc[0] = __byte_perm(s2, s2, 0x1010);
       sc[1] = __byte_perm(s2, s2, 0x3232);
     }
@@ -301,8 +337,8 @@ __device__ __forceinline__ bool pa_store(const unsigned char* raw, unsigned char
         // (magnitude - (base << 7)) << 3 in both halves at once, sign kept
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          v[e] = (__vmaxu2(w[e] & 0x7fff7fffu, low) * 8u + shift) | (w[e] & 0x80008000u);
-        if (high) {                                                  // non-finite values: FP16 infinity or NaN
+          v[e] = (pa_max2(w[e] & 0x7fff7fffu, low) * 8u + shift) | (w[e] & 0x80008000u);
+        if (EDGE) {                                                  // non-finite values: FP16 infinity or NaN
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t out = 0;
@@ -411,7 +447,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   if (warp < 8) {
     // ---- softmax and output: row r of the tile, half `s` of the columns of
     // every tile and of the output channels ------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFTMAX_REGS));
     const int s = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     // r / G for r < 128 and G <= 16 by a multiplication (exact: 128 * 16 < 2^16)
@@ -472,9 +508,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     float m = -INFINITY, l = 0.f, al_prev = 0.f;
     int vbase = -1000;                                               // BF16: o is in units of 2^(vbase - 112)
     constexpr int C = kPaRows / 2, E = D / 2;                        // columns and channels of this thread
-    float o[E];
+    uint64_t o[E / 2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = 0.f;
+    for (int i = 0; i < E / 2; ++i) o[i] = 0;
     auto exponent = [](int e) { return __int_as_float((e + 15) << 23); };   // 2^(e - 112)
     // adds tile j's P V, rescaling what is there by `al`
     auto drain = [&](int j, float al) {
@@ -486,7 +522,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         pa_ld32(tmem + lanes + kPaO + s * E + c, v);
         pa_ld_wait32(v);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[c + k] = fmaf(o[c + k], al, __uint_as_float(v[k]));
+        for (int k = 0; k < 32; k += 2)
+          o[(c + k) / 2] = pa_fma2(o[(c + k) / 2], pa_pair(al, al), pa_pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
       }
       tc_fence_before();
       __syncwarp();
@@ -514,10 +551,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < C; c += 16) {                              // 16 columns: a cache block
-        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int k = c; k < c + 16; ++k) x[k & 3] = fmaxf(x[k & 3], __uint_as_float(v[k / 32][k % 32]));
-        const float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        auto at = [&](int k) { return __uint_as_float(v[(c + k) / 32][(c + k) % 32]); };
+        const float x0 = pa_max3(pa_max3(at(0), at(1), at(2)), at(3), at(4)), x1 = pa_max3(pa_max3(at(5), at(6), at(7)), at(8), at(9));
+        const float y = pa_max3(pa_max3(x0, x1, at(10)), pa_max3(at(11), at(12), at(13)), fmaxf(at(14), at(15)));
         mx = fmaxf(mx, S::BF ? y * exponent(sm_kbase[j & 3][(s * C + c) / 16]) : y);
       }
       sm_mx[j & 1][s][r] = mx;
@@ -537,29 +573,34 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         vbase = top;
       }
       // P = 2^(score - maximum), for BF16 times 2^(block's base - vbase)
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t ls[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < C; c += 16) {
         const int blk = (s * C + c) / 16;
         const float fc = S::BF ? fac * exponent(sm_kbase[j & 3][blk]) : fac;
         const float off = S::BF ? (float)max(sm_vbase[j & 1][blk] - vbase, -80) : 0.f;   // below: nothing beside the largest
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t part[2] = {0, 0};
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
-          const float p0 = pa_ex2(fmaf(__uint_as_float(v[c / 32][(c + k) % 32]), fc, off - mu));
-          const float p1 = pa_ex2(fmaf(__uint_as_float(v[c / 32][(c + k + 1) % 32]), fc, off - mu));
-          part[k & 2] += p0;
-          part[(k & 2) + 1] += p1;
+          const float2 t2 = pa_unpair(pa_fma2(pa_pair(__uint_as_float(v[c / 32][(c + k) % 32]),
+                                                      __uint_as_float(v[c / 32][(c + k + 1) % 32])),
+                                              pa_pair(fc, fc), pa_pair(off - mu, off - mu)));
+          const float p0 = pa_ex2(t2.x), p1 = pa_ex2(t2.y);
+          uint64_t& sum = S::BF ? part[k / 2 & 1] : ls[k / 2 & 1];
+          sum = pa_add2(sum, pa_pair(p0, p1));
           pa_split(p0, p1, hi[k / 2], lo[k / 2]);
         }
-        const float back = S::BF ? pa_ex2(-off) : 1.f;
+        if (S::BF) {
+          const float back = pa_ex2(-off);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ls[e] = S::BF ? fmaf(part[e], back, ls[e]) : ls[e] + part[e];
+          for (int e = 0; e < 2; ++e) ls[e] = pa_fma2(part[e], pa_pair(back, back), ls[e]);
+        }
         pa_st8(sc + c, hi);                                          // 16 keys: 8 columns high parts, 8 low parts
         pa_st8(sc + c + 8, lo);
       }
-      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      const float2 l2 = pa_unpair(pa_add2(ls[0], ls[1]));
+      l += l2.x + l2.y;
       pa_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -578,8 +619,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     const float wgt = pos < 0 ? 0.f : a.v_scale / L * (S::BF ? exponent(max(vbase, 0)) : 1.f);
     float* stage = reinterpret_cast<float*>(smem) + r * S::LDO + s * E;
 #pragma unroll
-    for (int i = 0; i < E; i += 4)
-      *reinterpret_cast<float4*>(stage + i) = make_float4(o[i] * wgt, o[i + 1] * wgt, o[i + 2] * wgt, o[i + 3] * wgt);
+    for (int i = 0; i < E; i += 4) {
+      const float2 x = pa_unpair(o[i / 2]), y = pa_unpair(o[i / 2 + 1]);
+      *reinterpret_cast<float4*>(stage + i) = make_float4(x.x * wgt, x.y * wgt, y.x * wgt, y.y * wgt);
+    }
     if (sm_poison) {                                                 // rare: non-finite V among the tile's own tokens
       // from the first block whose values the loader guarded
       for (int tok = max(0, t.pos0 + 1) / kBlockTokens * kBlockTokens; tok <= pos; ++tok) {
@@ -604,7 +647,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     // ---- loaders: two blocks of every K (or V) tile per warp; raw blocks are
     // requested as their stage of the ring falls free, block ids (lanes 0..7
     // hold a tile's) a tile before that
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaLoadRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::LOAD_REGS));
     const bool is_k = warp < 12;
     const int lw = warp & 3, nblk = (t.ctx + kBlockTokens - 1) / kBlockTokens;
     constexpr int BT = kPaRows / kBlockTokens;
@@ -641,18 +684,24 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       __syncwarp();
       if (i > 0 && !__all_sync(0xffffffffu, pa_wait(&empty[buf], (i - 1) & 1, &sm_stop))) break;
       unsigned char* tile = (is_k ? kbuf : vbuf) + buf * S::TILE;
-#pragma unroll
+#pragma unroll (S::BF ? 1 : 2)
       for (int half = 0; half < 2; ++half) {
         const int at = half * 4 + lw, tok0 = j * kPaRows + at * kBlockTokens;
         const bool guard = !is_k && tok0 + kBlockTokens - 1 > t.pos0;
-        const unsigned char* raw = ring + ((j % S::STAGES) * 2 + half) * S::UNIT;
+        PaRaw<D, KV> raw;
+        raw.read(ring + ((j % S::STAGES) * 2 + half) * S::UNIT, lane);
+        const int keep = t.ctx - tok0;
+        bool high = false;
         int base = 0;
-        if (guard || t.ctx - tok0 < kBlockTokens) {
-          if (pa_store<D, KV, true>(raw, tile, at * kBlockTokens, t.ctx - tok0, guard, lane, &base)) sm_poison = 1;
-        } else {
-          pa_store<D, KV, false>(raw, tile, at * kBlockTokens, kBlockTokens, false, lane, &base);
+        if constexpr (S::BF) {                                       // nothing past the context sets the exponent
+          base = pa_block_base<D>(raw, keep, lane, high);
+          if (lane == 0) (is_k ? sm_kbase[j & 3] : sm_vbase[buf])[at] = base;
         }
-        if (S::BF && lane == 0) (is_k ? sm_kbase[j & 3] : sm_vbase[buf])[at] = base;
+        if (guard || high || keep < kBlockTokens) {
+          if (pa_store<D, KV, true>(raw, tile, at * kBlockTokens, keep, guard, lane, base)) sm_poison = 1;
+        } else {
+          pa_store<D, KV, false>(raw, tile, at * kBlockTokens, kBlockTokens, false, lane, base);
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();                                                  // every lane has read the raw blocks
