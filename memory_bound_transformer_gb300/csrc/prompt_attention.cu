@@ -62,9 +62,9 @@ struct PaShape {
   static constexpr int NCH = kBlockTokens * (D / CPC) / 32;   // chunks of a block per lane
   static constexpr int PANEL = kPaRows * 128;         // 128 tokens x 64 channels, 128-byte swizzle
   static constexpr int TILE = D / 64 * PANEL;
-  // registers: 256 x 168 + 256 x 56 + 128 x 32 (BF16: 160 and 64, its loader holds
+  // registers: 256 x 168 + 256 x 56 + 128 x 32 (BF16: 144 and 80, its loader holds
   // a raw block) = 640 x 96, what the block is launched with
-  static constexpr int SOFTMAX_REGS = BF ? 160 : 168, LOAD_REGS = BF ? 64 : 56;
+  static constexpr int SOFTMAX_REGS = BF ? 144 : 168, LOAD_REGS = BF ? 80 : 56;
   static constexpr int LDO = D + 4;                   // output staging row, floats
   static constexpr int STAGES = BF ? 1 : 2;           // raw pairs of blocks of a loader warp
   static constexpr int SMEM = 4 * TILE + 8 * STAGES * 2 * UNIT + 1024;
@@ -267,33 +267,36 @@ __device__ __forceinline__ uint32_t pa_max2(uint32_t a, uint32_t b) {   // of tw
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Exponent base of a BF16 block's first `keep` tokens: FP16 exponent field =
-// BF16 field - base, the largest finite value's at 30. `high` (uniform): some
-// value is not finite.
+// Largest magnitude among a block's BF16 bit patterns (`finite`: among those of
+// finite values).
 template <int D>
-__device__ __forceinline__ int pa_block_base(const PaRaw<D, KV_BF16>& raw, int keep, int lane, bool& high) {
-  using S = PaShape<D, KV_BF16>;
-  uint32_t m = 0;
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {                             // the second, rare: finite values only
-    m = 0;
+__device__ __forceinline__ uint32_t pa_block_max(const PaRaw<D, KV_BF16>& raw, bool finite) {
+  uint32_t m[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int q = 0; q < S::NCH; ++q) {
+  for (int q = 0; q < PaShape<D, KV_BF16>::NCH; ++q) {
+    uint32_t x[4] = {raw.c[q].x & 0x7fff7fffu, raw.c[q].y & 0x7fff7fffu, raw.c[q].z & 0x7fff7fffu, raw.c[q].w & 0x7fff7fffu};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = pa_max2(m[e], finite ? x[e] & ~__vcmpgeu2(x[e], 0x7f807f80u) : x[e]);
+  }
+  const uint32_t x = pa_max2(pa_max2(m[0], m[1]), pa_max2(m[2], m[3]));
+  return __reduce_max_sync(0xffffffffu, max(x >> 16, x & 0xffffu));
+}
+// Exponent base of a BF16 block's first `keep` tokens (the others become zeros):
+// FP16 exponent field = BF16 field - base, the largest finite value's at 30.
+// `high` (uniform): some value is not finite.
+template <int D>
+__device__ __forceinline__ int pa_block_base(PaRaw<D, KV_BF16>& raw, int keep, int lane, bool& high) {
+  if (keep < kBlockTokens) {
+#pragma unroll
+    for (int q = 0; q < PaShape<D, KV_BF16>::NCH; ++q) {
       int panel, row, part;
       pa_chunk<D, KV_BF16>(q, lane, panel, row, part);
-      const uint4 c = raw.c[q];
-      uint32_t x[4] = {c.x & 0x7fff7fffu, c.y & 0x7fff7fffu, c.z & 0x7fff7fffu, c.w & 0x7fff7fffu};
-      if (pass) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] &= ~__vcmpgeu2(x[e], 0x7f807f80u);
-      }
-      const uint32_t y = pa_max2(pa_max2(x[0], x[1]), pa_max2(x[2], x[3]));
-      m = pa_max2(m, row < keep ? y : 0u);
+      if (row >= keep) raw.c[q] = make_uint4(0u, 0u, 0u, 0u);
     }
-    m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
-    if (!pass) high = m >= 0x7f80u;
-    if (!high) break;
   }
+  uint32_t m = pa_block_max<D>(raw, false);
+  high = m >= 0x7f80u;
+  if (high) m = pa_block_max<D>(raw, true);                          // rare
   return max(0, (int)(m >> 7) - 30);
 }
 
