@@ -32,6 +32,13 @@ __device__ __forceinline__ void e2m1x8_to_h2(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
 
+// The same for the four codes of a 16-bit word.
+__device__ __forceinline__ void e2m1x4_to_h2(uint32_t w, uint32_t (&h)[2]) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %2;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]) : "r"(w));
+}
+
 __device__ __forceinline__ float2 h2_to_float2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
