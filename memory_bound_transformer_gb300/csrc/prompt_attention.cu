@@ -190,8 +190,9 @@ __device__ __forceinline__ bool pa_find(const PromptArgs& a, int T, long long id
   long long before = 0;
   for (int s0 = 0; s0 < a.nseq; s0 += 32) {
     const int s = s0 + lane;
-    int lo = 0, hi = 0;
+    int lo = 0, hi = 0, ctx = 0;
     if (s < a.nseq) {
+      ctx = a.lens[s];
       lo = min(max(a.cu[s], 0), a.n);
       hi = min(max(a.cu[s + 1], lo), a.n);
     }
@@ -213,7 +214,7 @@ __device__ __forceinline__ bool pa_find(const PromptArgs& a, int T, long long id
       t->seq = s0 + src;
       t->row0 = lo + at;
       t->tokens = min(T, hi - lo - at);
-      t->ctx = a.lens[t->seq];
+      t->ctx = __shfl_sync(0xffffffffu, ctx, src);
       t->pos0 = t->ctx - (hi - lo) + at;
       return true;
     }
@@ -661,30 +662,26 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     uint64_t* empty = is_k ? bars.kempty : bars.vempty;
     auto ids_of = [&](int j) { return lane < BT && j * BT + lane < nblk ? __ldg(bt + j * BT + lane) : 0; };
     int ids = ids_of(0);
-    auto request = [&](int j) {
+    // one block of the warp's two in tile j, a copy group of its own
+    auto request = [&](int j, int half) {
       if (j < ntiles) {
-        if (lane < BT && j * BT + lane < nblk && (uint32_t)ids > (uint32_t)a.num_blocks) {   // out of range: the null block
+        if (half == 0 && lane < BT && j * BT + lane < nblk && (uint32_t)ids > (uint32_t)a.num_blocks) {   // out of range: the null block
           set_err(a.err, MBT_DEV_BLOCK_RANGE);
           ids = a.num_blocks;
         }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int at = half * 4 + lw;
-          const unsigned char* src = pool + (size_t)__shfl_sync(0xffffffffu, ids, at) * a.nkv * S::UNIT;
-          if (j * BT + at < nblk) pa_request<S::UNIT>(smem_u32(ring) + ((j % S::STAGES) * 2 + half) * S::UNIT, src, lane);
-        }
-        ids = ids_of(j + 1);
+        const int at = half * 4 + lw;
+        const unsigned char* src = pool + (size_t)__shfl_sync(0xffffffffu, ids, at) * a.nkv * S::UNIT;
+        if (j * BT + at < nblk) pa_request<S::UNIT>(smem_u32(ring) + ((j % S::STAGES) * 2 + half) * S::UNIT, src, lane);
+        if (half) ids = ids_of(j + 1);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int j = 0; j < S::STAGES; ++j) request(j);
+    for (int i = 0; i < 2 * S::STAGES; ++i) request(i / 2, i & 1);
     const bool go = is_k || __all_sync(0xffffffffu, pa_wait(&bars.qfull, 0, &sm_stop));   // the queries sit in V's place
 #pragma unroll 1
     for (int j = 0; go && j < ntiles; ++j) {
       const int buf = j & 1, i = j >> 1;
-      asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
-      __syncwarp();
       if (i > 0 && !__all_sync(0xffffffffu, pa_wait(&empty[buf], (i - 1) & 1, &sm_stop))) break;
       unsigned char* tile = (is_k ? kbuf : vbuf) + buf * S::TILE;
 #pragma unroll (S::BF ? 1 : 2)
@@ -692,7 +689,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         const int at = half * 4 + lw, tok0 = j * kPaRows + at * kBlockTokens;
         const bool guard = !is_k && tok0 + kBlockTokens - 1 > t.pos0;
         PaRaw<D, KV> raw;
+        asm volatile("cp.async.wait_group %0;" ::"n"(2 * S::STAGES - 1) : "memory");
+        __syncwarp();
         raw.read(ring + ((j % S::STAGES) * 2 + half) * S::UNIT, lane);
+        __syncwarp();                                                // every lane has read: the place is free
+        request(j + S::STAGES, half);
         const int keep = t.ctx - tok0;
         bool high = false;
         int base = 0;
@@ -707,9 +708,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();                                                  // every lane has read the raw blocks
+      __syncwarp();
       if (lane == 0) mbar_arrive(&full[buf]);
-      request(j + S::STAGES);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
