@@ -355,6 +355,7 @@ __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char*
           }
         }
       }
+      if (EDGE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;       // whatever the raw block's place held
       if (EDGE && guard) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -363,7 +364,6 @@ __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char*
           v[e] &= ~bad;
         }
       }
-      if (EDGE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;
       *reinterpret_cast<uint4*>(dst + (((part * (S::CPC / 8) + k) ^ (R & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
