@@ -106,7 +106,7 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// 32-token steps of a row, 0 for a length outside its table.
+// Steps of a row, 0 for a length outside its table.
 __device__ __forceinline__ int steps_of(const AttnFp4Args& a, int seq) {
   return seq < 1 || seq > (long long)a.bt_stride * kBlockTokens ? 0 : (seq + kF4Step - 1) / kF4Step;
 }

@@ -15,7 +15,11 @@ using namespace mbt;
 
 namespace {
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
-bool scale_ok(float s) { return s > 0.f && std::isfinite(s); }
+// A tensor's scale. Beyond these its products with block scales, queries and
+// their reciprocals could leave fp32's range.
+bool scale_ok(float s) { return s >= 0x1p-64f && s <= 0x1p64f; }
+// A row of a block table: its token count, rounded up to tiles, stays an int.
+bool table_ok(const int32_t* bt, int bt_stride) { return bt && bt_stride >= 1 && bt_stride <= (1 << 26); }
 // Heads and head size that the cache's kernels take.
 bool heads_ok(int nq, int nkv, int d) {
   return nq >= 1 && nkv >= 1 && nq % nkv == 0 && nq / nkv <= 16 && (d == 64 || d == 128);
@@ -78,7 +82,7 @@ int op_rope_kv_write_fp4(int n, const float* qkv, int ld_qkv, int nq, int nkv, i
                          int max_pos, void* kpool, void* vpool, int num_blocks, float k_scale, float v_scale,
                          float* q_out, uint32_t* err, void* stream) {
   if (n < 1 || !qkv || nq < 1 || nkv < 1 || (d != 64 && d != 128) || !positions || nseq < 1 || (!row_seq && nseq < n) ||
-      !bt || bt_stride < 1 || !rope || max_pos < 1 || !kpool || !vpool || num_blocks < 1 || !q_out ||
+      !table_ok(bt, bt_stride) || !rope || max_pos < 1 || !kpool || !vpool || num_blocks < 1 || !q_out ||
       !scale_ok(k_scale) || !scale_ok(v_scale))
     return MBT_ERR_BAD_ARG;
   if (ld_qkv % 4 || (long long)ld_qkv < ((long long)nq + 2LL * nkv) * d || !aligned16(qkv) || !aligned16(rope) ||
@@ -97,7 +101,7 @@ int op_rope_kv_write_fp4(int n, const float* qkv, int ld_qkv, int nq, int nkv, i
 int op_kv_read_fp4(int n, const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
                    int nkv, int d, const void* kpool, const void* vpool, int num_blocks, float k_scale, float v_scale,
                    float* k_out, float* v_out, uint32_t* err, void* stream) {
-  if (n < 1 || !positions || nseq < 1 || (!row_seq && nseq < n) || !bt || bt_stride < 1 || nkv < 1 ||
+  if (n < 1 || !positions || nseq < 1 || (!row_seq && nseq < n) || !table_ok(bt, bt_stride) || nkv < 1 ||
       (d != 64 && d != 128) || !kpool || !vpool || num_blocks < 1 || !scale_ok(k_scale) || !scale_ok(v_scale) ||
       !k_out || !v_out)
     return MBT_ERR_BAD_ARG;
@@ -112,8 +116,8 @@ int op_kv_read_fp4(int n, const int32_t* positions, const int32_t* row_seq, int 
 int op_paged_attention_fp4(int B, const float* q, int nq, int nkv, int d, const void* kpool, const void* vpool,
                            float k_scale, float v_scale, const int32_t* bt, int bt_stride, const int32_t* seq_lens,
                            int num_blocks, float* out, uint32_t* err, void* stream) {
-  if (B < 1 || !q || !heads_ok(nq, nkv, d) || !kpool || !vpool || !scale_ok(k_scale) || !scale_ok(v_scale) || !bt ||
-      bt_stride < 1 || !seq_lens || num_blocks < 1 || !out)
+  if (B < 1 || !q || !heads_ok(nq, nkv, d) || !kpool || !vpool || !scale_ok(k_scale) || !scale_ok(v_scale) ||
+      !table_ok(bt, bt_stride) || !seq_lens || num_blocks < 1 || !out)
     return MBT_ERR_BAD_ARG;
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out)) return MBT_ERR_BAD_ARG;
   int sms = 0;
@@ -132,7 +136,7 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
                         float v_scale, const int32_t* bt, int bt_stride, int num_blocks, float* out, uint32_t* err,
                         void* stream) {
   if (n < 1 || !q || !heads_ok(nq, nkv, d) || nseq < 1 || !cu_seqlens || !ctx_lens || !kpool || !vpool ||
-      !scale_ok(k_scale) || !scale_ok(v_scale) || !bt || bt_stride < 1 || num_blocks < 1 || !out)
+      !scale_ok(k_scale) || !scale_ok(v_scale) || !table_ok(bt, bt_stride) || num_blocks < 1 || !out)
     return MBT_ERR_BAD_ARG;
   if (kv_dtype != MBT_DTYPE_BF16 && kv_dtype != MBT_DTYPE_E4M3 && kv_dtype != MBT_DTYPE_E2M1) return MBT_ERR_BAD_ARG;
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out)) return MBT_ERR_BAD_ARG;

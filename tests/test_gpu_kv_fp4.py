@@ -384,3 +384,76 @@ def test_write_then_attend_as_a_serving_loop(cuda_lib):
         ref = rows_attention(y[:, :nq], kv[0], kv[1], bt, np.arange(3), pos)
         assert np.abs(out.double().cpu().numpy() - ref).max() <= 2e-5 * np.abs(kv[1]).max()
     assert int(err.item()) == 0
+
+
+def test_blocks_beyond_four_gigabytes(cuda_lib):
+    """The same rows in a small pool and behind 2^32 bytes of a large one: same bytes, values and outputs."""
+    nq, nkv, d, n = 16, 8, 128, 40
+    per_block = nkv * unit_bytes(d)
+    far = 2 ** 32 // per_block + 3                                    # the large pool's first block past 2^32 bytes
+    rng = np.random.default_rng(50)
+    qkv, table = dev(rng.standard_normal((n, (nq + 2 * nkv) * d)), torch.float32), rope_table(64, d)
+    bt, seq, lens = np.array([[2, 0, 1]], np.int32), dev(np.zeros(n)), dev([n])
+    got = []
+    for first in (0, far):
+        nb = first + 3
+        pools = [torch.empty((nb + 1) * per_block, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        for p in pools:
+            p[first * per_block:].zero_()
+        q, out = torch.zeros((n, nq, d), device=DEV), torch.zeros((1, nq * d), device=DEV)
+        k, v, err = torch.zeros((n, nkv, d), device=DEV), torch.zeros((n, nkv, d), device=DEV), dev([0])
+        at = dev(bt + first)
+        capi.op_rope_kv_write_fp4(qkv, nq, nkv, d, dev(np.arange(n)), at, table, *pools, nb, 0.875, 1.25, q, row_seq=seq, err=err)
+        capi.op_kv_read_fp4(dev(np.arange(n)), at, *pools, nkv, d, nb, 0.875, 1.25, k, v, row_seq=seq, err=err)
+        capi.op_paged_attention_fp4(q[-1:], nkv, *pools, 0.875, 1.25, at, lens, nb, out, err)
+        assert int(err.item()) == 0
+        got.append([x.cpu() for x in (q, k, v, out, pools[0][first * per_block:], pools[1][first * per_block:])])
+        del pools
+    assert got[0][1].any() and got[0][3].any()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_a_graph_follows_its_inputs(cuda_lib):
+    """A captured call reads lengths, tables, queries and pools when it is replayed."""
+    first, then = Decode(16, 2, 128, [300, 40, 1], seed=60), Decode(16, 2, 128, [33, 300, 65], seed=61)
+    width, nb = max(first.bt.shape[1], then.bt.shape[1]), max(first.nb, then.nb)
+    sides = []
+    for c in (first, then):
+        bt = np.full((3, width), -1, np.int32)
+        bt[:, :c.bt.shape[1]] = c.bt
+        pools = np.zeros((2, nb + 1, 2, unit_bytes(128)), np.uint8)
+        pools[0, :c.nb + 1], pools[1, :c.nb + 1] = c.kp, c.vp
+        sides.append((dev(c.q, torch.float32), dev(pools, torch.uint8), dev(bt), dev(c.lens)))
+    q, pools, bt, lens = (t.clone() for t in sides[0])
+    out = torch.zeros((3, 16 * 128), device=DEV)
+    call = lambda: capi.op_paged_attention_fp4(q, 2, pools[0], pools[1], 0.75, 1.25, bt, lens, nb, out)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for c, side in ((then, sides[1]), (first, sides[0])):
+        for mine, new in zip((q, pools, bt, lens), side):
+            mine.copy_(new)
+        g.replay()
+        torch.cuda.synchronize()
+        ref = c.ref()
+        assert np.all(np.abs(out.double().cpu().numpy() - ref) <= 2e-5 * c.vmax)
+
+
+def test_two_threads_at_once(cuda_lib):
+    """Calls from two host threads on streams of their own."""
+    from concurrent.futures import ThreadPoolExecutor
+    cases = [Decode(8, 1, 128, [900, 40], seed=62), Decode(16, 2, 64, [300] * 5, seed=63)]
+    want = [c.run()[0] for c in cases]
+
+    def work(c):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.default_stream())
+        with torch.cuda.stream(s):
+            return [c.run()[0] for _ in range(10)]
+
+    with ThreadPoolExecutor(2) as pool:
+        for w, outs in zip(want, pool.map(work, cases)):
+            assert all(np.array_equal(o, w) for o in outs)

@@ -2,8 +2,9 @@
 oracle.
 
 Tolerance: 2e-5 * max |V|, as for single-token attention (queries and
-probabilities enter the tensor cores as 16-bit high + low parts: 2^-17 relative
-in BF16, 2^-22 in FP16; fp32 scores and sums)."""
+probabilities enter the tensor cores as FP16 high + low parts, 2^-22 relative;
+BF16 caches as FP16 with an exponent per block, 2^-30 of its largest; fp32
+scores and sums)."""
 import numpy as np
 import pytest
 import torch
@@ -246,3 +247,51 @@ def test_prompt_then_decode(cuda_lib):
         ref = rows_attention(y[:, :nq], kv[0], kv[1], bt, seq, pos)
         assert np.abs(out.double().cpu().numpy() - ref).max() <= 2e-5 * np.abs(kv[1]).max()
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_blocks_beyond_four_gigabytes(cuda_lib, kind):
+    """The same prompt in a small pool and behind 2^32 bytes of a large one."""
+    c = Prompt(kind, 16, 2, 128, [70], [20], seed=70)
+    per_block = c.kp[0].nbytes
+    far = 2 ** 32 // per_block + 3
+    got = []
+    for first in (0, far):
+        pools = []
+        for raw in (c.kp, c.vp):
+            p = torch.empty((first + c.nb + 1) * per_block, dtype=torch.uint8, device=DEV)
+            p[first * per_block:].copy_(torch.as_tensor(raw.reshape(-1).view(np.uint8), device=DEV))
+            pools.append(p)
+        out, err = torch.zeros((c.n, c.nq * c.d), device=DEV), dev([0])
+        capi.op_prompt_attention(dev(c.q, torch.float32), c.nkv, dev(c.cu), dev(c.ctx), *pools, KINDS[kind], c.kg, c.vg,
+                                 dev(c.bt + first), first + c.nb, out, err)
+        assert int(err.item()) == 0
+        got.append(out.cpu())
+        del pools
+    assert got[0].any() and torch.equal(*got)
+
+
+def test_a_graph_follows_its_inputs(cuda_lib):
+    """One captured call, replayed for other boundaries, lengths, tables, queries and cache contents."""
+    cases = [Prompt("fp4", 8, 2, 64, [60, 0, 5], [0, 9, 30], seed=71, width=12), Prompt("fp4", 8, 2, 64, [1, 33, 31], [150, 0, 2], seed=72, width=12)]
+    nb = max(c.nb for c in cases)
+    sides = []
+    for c in cases:
+        pools = np.zeros((2, nb + 1, 2, unit_bytes(64)), np.uint8)
+        pools[0, :c.nb + 1], pools[1, :c.nb + 1] = c.kp, c.vp
+        sides.append((dev(c.q, torch.float32), dev(c.cu), dev(c.ctx), dev(pools, torch.uint8), dev(c.bt)))
+    q, cu, ctx, pools, bt = live = [t.clone() for t in sides[0]]
+    out = torch.zeros((65, 8 * 64), device=DEV)
+    call = lambda: capi.op_prompt_attention(q, 2, cu, ctx, pools[0], pools[1], capi.DTYPE_E2M1, 0.75, 1.25, bt, nb, out)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for c, side in ((cases[1], sides[1]), (cases[0], sides[0])):
+        for mine, new in zip(live, side):
+            mine.copy_(new)
+        g.replay()
+        torch.cuda.synchronize()
+        ref = c.ref()
+        assert np.all(np.abs(out.double().cpu().numpy() - ref) <= 2e-5 * c.vmax)

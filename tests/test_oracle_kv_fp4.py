@@ -145,3 +145,9 @@ def test_binding_refuses_host_tensors(lib):
         capi.op_kv_read_fp4(i[:, 0].contiguous(), i, p, p, 2, 64, 5, 1.0, 1.0, z, z)
     with pytest.raises(ValueError):
         capi.op_rope_kv_write_fp4(torch.zeros((4, 384)), 2, 2, 64, i[:, 0].contiguous(), i, z, p, p, 5, 1.0, 1.0, z)
+
+
+@pytest.mark.parametrize("fn", list(BAD))
+@pytest.mark.parametrize("name,value", [("k_scale", 2.0 ** -65), ("v_scale", 2.0 ** 65), ("bt_stride", (1 << 26) + 1)])
+def test_limits_of_scales_and_tables(lib, fn, name, value):
+    assert getattr(lib, fn)(*dict(BAD[fn][0], **{name: value}).values()) == -1
