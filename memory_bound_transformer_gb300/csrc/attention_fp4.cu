@@ -25,10 +25,19 @@
 // * The tensor core's fp32 accumulation truncates, so chains are kept short
 //   (D / 16 steps for S, four for P V) and the sums over steps are IEEE fp32.
 // Conversions and multiplies issue every second cycle and an MMA every eighth
-// per SM quarter (measured), so 32 tokens' 64 MMAs, 128 conversions and 128
-// multiplies take 512, 256 and 256 cycles of three pipes, against 790 at the HBM
-// rate; with the ~400 instructions around them the loop reaches 4.8 TB/s.
+// per SM quarter (measured), so a 64-token step's 128 MMAs, 256 conversions and
+// 256 multiplies take 1024, 512 and 512 cycles of three pipes, against 1580 at
+// the HBM rate; with the ~700 instructions around them a quarter takes 2390
+// cycles a step (2130 without the loads), with two warps as with three or four:
+// 4.5 TB/s over long contexts. Taking one part out saves what it issues: half the
+// MMAs 470, the softmax 250, K's or V's multiplies 130, the nibble interleave
+// 120, the scales 105.
+// Around the loop a launch has ~5 us: the lengths, ids and queries (one round
+// trip), the first step's blocks, one step, the merges. 64 rows of 64 + 2 x 8
+// heads of 128 over 2048 tokens: 51 us (3.0 TB/s: 512 CTAs are 1.7 waves of two
+// an SM); one row of 32 + 2 x 8 heads over 2048: 5.7 us.
 #include <algorithm>
+#include <climits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -332,9 +341,30 @@ __device__ __forceinline__ float merge_warps(const float* so, const float (*sm_m
   return acc;
 }
 
+// The row with `rank` longer ones before it (equal lengths in order), for at
+// most kF4Threads rows; all threads call it.
+__device__ __forceinline__ int row_of_rank(const AttnFp4Args& a, int rank) {
+  __shared__ __align__(16) int sm_len[kF4Threads], sm_row;
+  const int tid = threadIdx.x, mine = tid < a.B ? __ldg(a.seq_lens + tid) : INT_MIN;
+  sm_len[tid] = mine;
+  __syncthreads();
+  int before = 0;
+  for (int j = 0; j < a.B; j += 4) {
+    const int4 v = *reinterpret_cast<const int4*>(sm_len + j);
+    before += (v.x > mine || (v.x == mine && j < tid)) + (v.y > mine || (v.y == mine && j + 1 < tid)) +
+              (v.z > mine || (v.z == mine && j + 2 < tid)) + (v.w > mine || (v.w == mine && j + 3 < tid));
+  }
+  if (tid < a.B && before == rank) sm_row = tid;
+  __syncthreads();
+  return sm_row;
+}
+
 // One cluster of 1..8 CTAs per pair (row, KV head, group of eight heads), whose
 // warps take the row's steps in turn; the CTAs' parts merge through distributed
-// shared memory. One launch, no scratch.
+// shared memory. One launch, no scratch. (One wave of clusters of four that share
+// all pairs' steps evenly balances better, but finding the shares from the
+// lengths costs 4 us: 37 / 54 / 94 us against 38 / 49 / 45 for 64 rows of 256 to
+// 2048 tokens, 64 of 2048 and 4 of 32k.)
 template <int D>
 __global__ void __launch_bounds__(kF4Threads, kF4PerSm) attention_fp4_kernel(const AttnFp4Args a) {
   using S = Fp4Shape<D>;
@@ -344,20 +374,30 @@ __global__ void __launch_bounds__(kF4Threads, kF4PerSm) attention_fp4_kernel(con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sp = (int)(blockIdx.x % (unsigned)a.cluster);
   const int pair = (int)(blockIdx.x / (unsigned)a.cluster);          // (row, KV head, group of 8 heads)
-  const int hb = pair % a.hblocks, h = (pair / a.hblocks) % a.nkv, b = pair / a.hblocks / a.nkv;
+  const int hb = pair % a.hblocks, h = (pair / a.hblocks) % a.nkv;
+  int b = pair / a.hblocks / a.nkv;
   const int gn = min(kF4Heads, a.nq / a.nkv - hb * kF4Heads);
-  const size_t head0 = (size_t)b * a.nq + (size_t)h * (a.nq / a.nkv) + hb * kF4Heads;
+  auto first_head = [&]() { return (size_t)b * a.nq + (size_t)h * (a.nq / a.nkv) + hb * kF4Heads; };
 
   // Three loads that do not depend on one another: the row's length, the
   // queries, and the block ids of this warp's first steps (its steps are dealt
   // over the cluster's warps in turn, so they are known without the length).
-  const int seq = __ldg(a.seq_lens + b);
   const int first = sp * kF4Warps + warp, stride = a.cluster * kF4Warps;
-  int id = step_ids(a, b, first, a.bt_stride - kF4Blocks * first, lane);
-  int id2 = step_ids(a, b, first + stride, a.bt_stride - kF4Blocks * (first + stride), lane);
+  int seq, id, id2;
   Fp4Warp<D> w;
   float x[D / 4];
-  w.load(a, head0, gn, lane, x);
+  auto load_row = [&]() {
+    seq = __ldg(a.seq_lens + b);
+    id = step_ids(a, b, first, a.bt_stride - kF4Blocks * first, lane);
+    id2 = step_ids(a, b, first + stride, a.bt_stride - kF4Blocks * (first + stride), lane);
+    w.load(a, first_head(), gn, lane, x);
+  };
+  load_row();
+  if (a.sorted) {                                                    // under way for the row in order; often it is that one
+    const int row = row_of_rank(a, b);
+    if (row != b) { b = row; load_row(); }
+  }
+  const size_t head0 = first_head();
   const int steps = steps_of(a, seq);
   if (!steps && tid == 0 && sp == 0 && h == 0 && hb == 0) set_err(a.err, MBT_DEV_SEQLEN_RANGE);
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kF4Stages * S::STAGE;
@@ -449,6 +489,13 @@ cudaError_t attn_fp4_plan(AttnFp4Args* a, int num_sms) {
   const long long steps = ((long long)a->bt_stride * kBlockTokens + kF4Step - 1) / kF4Step;
   const long long want = std::min(steps / kF4Warps, (long long)kF4PerSm * num_sms / pairs);
   a->cluster = (int)std::max<long long>(1, std::min<long long>(kF4Cluster, want));
+  // More than a wave of long rows: the longest first, so that the last wave's are
+  // short. Finding them costs ~500 cycles a CTA, and a round trip where the row is
+  // another than in order: 64 x 8 pairs of 256..2048 tokens 39.1 -> 32.7 us, of
+  // 2048 each 49.4 -> 50.6; 128 x 8 of 64..8192 193 -> 164, of 100..1000 43.0 ->
+  // 46.6; 40 x 8 (1.05 waves) of 128..4096 39.1 -> 40.9. So from 32 steps and five
+  // quarters of a wave on.
+  a->sorted = a->B <= kF4Threads && steps >= 32 && 4 * pairs * a->cluster > 5LL * kF4PerSm * num_sms;
   return cudaSuccess;
 }
 

@@ -297,9 +297,9 @@ struct AttnFp4Args {
   const void* kpool; const void* vpool; float k_scale, v_scale;
   const int* bt; int bt_stride; const int* seq_lens; int num_blocks;
   float* out; uint32_t* err;
-  int hblocks, cluster;
+  int hblocks, cluster, sorted;
 };
-cudaError_t attn_fp4_plan(AttnFp4Args* a, int num_sms);     // sets hblocks and cluster
+cudaError_t attn_fp4_plan(AttnFp4Args* a, int num_sms);     // sets hblocks, cluster and sorted (longest rows first)
 cudaError_t launch_attention_fp4(const AttnFp4Args& a, cudaStream_t s);
 cudaError_t attn_fp4_init();
 

@@ -34,6 +34,19 @@
 // each: for 16 keys 8 columns of high and 8 of low parts), P V (128), queries
 // (D / 2 high, D / 2 low).
 //
+// What bounds it: a key tile costs an SM 2830 cycles in a long loop, the MMAs
+// 2048 of them; the softmax warps' chain is the longer one (maximum 620 to 750,
+// exponentials and split 1250, adding P V 500, waiting 200). A CTA's start (its
+// place, its queries, the first scores) and its end cost 12,000 cycles and the
+// launch of the next 2,000; at one CTA an SM nothing overlaps them, which is a
+// third of the time at eight key tiles a CTA. 1000 tokens after 8200, 64 + 2 x 8
+// heads of 128, 4-bit: 391 us, 730 TFLOP/s of the formula's operations; 2048
+// tokens, 32 + 2 x 8 heads: 71 us, 485; 4096, 64 + 2 x 8, e4m3: 426 us, 640. BF16
+// tiles take two thirds more work to load: 582 us for those 4096.
+// CTAs that stay for all their query tiles were slower in each form tried (the
+// next queries loaded by the softmax warps 443 us, by the V loaders 418, for the
+// first of these): the state they carry takes the loop's registers.
+//
 // A value of V that is not finite at a token some rows of the tile do not attend
 // to would reach them as 0 x inf: the loader stores 0 for it and raises a flag,
 // and the rows that do attend to it add it at the end.

@@ -457,3 +457,19 @@ def test_two_threads_at_once(cuda_lib):
     with ThreadPoolExecutor(2) as pool:
         for w, outs in zip(want, pool.map(work, cases)):
             assert all(np.array_equal(o, w) for o in outs)
+
+
+def test_attention_many_uneven_rows_in_a_wide_table(cuda_lib):
+    """More than a wave of CTAs and a table of 2048 tokens: rows are taken longest first. Equal, empty and too long
+    lengths among them."""
+    rng = np.random.default_rng(64)
+    lens = rng.integers(1, 200, 128)
+    lens[[3, 50, 127]] = 700, 1500, 1500
+    lens[10:20] = 77
+    c = Decode(8, 4, 64, lens, seed=65, width=128)
+    c.check()
+    c.lens = lens.copy()
+    c.lens[[0, 64, 126]] = 0, 128 * 16 + 1, -5
+    got, err = c.run()
+    assert err == capi.DEV_SEQLEN_RANGE and not got[[0, 64, 126]].any()
+    assert np.all(np.abs(got - c.ref()) <= 2e-5 * c.vmax)
