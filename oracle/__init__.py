@@ -37,7 +37,13 @@ pins live in tests/test_oracle_*.py):
   probabilities (chi-square), arg-max at top_k = 1, at a vanishing temperature
   and at a tiny top_p, draws inside the top-k set; sampling.keep_set: the
   top-p set is the minimal most-probable prefix.
+* kv_fp4.round_e2m1: the format's eight magnitudes, every midpoint (ties to
+  even), saturation at 6; kv_fp4.encode / decode: each value's nearest code
+  under its scale by exhaustive comparison, the scale within an e4m3 half step,
+  zero, NaN, infinite, tiny and saturating groups; pack_pool / unpack_pool: a
+  round trip and single bytes at hand-computed offsets; rows_attention /
+  prompt_positions: softmax sums written out over a gathered context.
 
 No function is "parity unpinned".
 """
-from . import numerics, decode, sampling  # noqa: F401
+from . import numerics, decode, sampling, kv_fp4  # noqa: F401
