@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
 #pragma unroll
       for (int i = 0; i < D / 2; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
       sm_big[s][r] = big;
-      named_bar(1, 256);
+      named_bar(2 + (warp & 3), 64);
       big = max(big, sm_big[s ^ 1][r]);
       const int e = min(120, 140 - (int)(big >> 23));
       const float up = __int_as_float((e + 127) << 23);
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         mx = fmaxf(mx, S::BF ? y * exponent(sm_kbase[j & 3][(s * C + c) / 16]) : y);
       }
       sm_mx[j & 1][s][r] = mx;
-      named_bar(1, 256);
+      named_bar(2 + (warp & 3), 64);                                 // the rows' two warps
       mx = fmaxf(mx, sm_mx[j & 1][s ^ 1][r]);
       const float mn = fmaxf(m, mx * fac), mu = mn == -INFINITY ? 0.f : mn;
       float al = pa_ex2(m - mu);
