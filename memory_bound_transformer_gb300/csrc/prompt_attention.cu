@@ -200,15 +200,30 @@ struct PaTile { int seq, row0, tokens, pos0, ctx; };   // pos0: position of the 
 // The tile of index `idx` among all sequences' tiles of T tokens, in order of
 // the sequences; false past the last. One warp; every lane gets the result.
 __device__ __forceinline__ bool pa_find(const PromptArgs& a, int T, long long idx, int lane, PaTile* t) {
+  auto rows_of = [&](int s, int& lo, int& hi) {
+    lo = hi = 0;
+    if (s >= a.nseq) return;
+    lo = min(max(a.cu[s], 0), a.n);
+    hi = min(max(a.cu[s + 1], lo), a.n);
+  };
   long long before = 0;
-  for (int s0 = 0; s0 < a.nseq; s0 += 32) {
-    const int s = s0 + lane;
-    int lo = 0, hi = 0, ctx = 0;
-    if (s < a.nseq) {
-      ctx = a.lens[s];
-      lo = min(max(a.cu[s], 0), a.n);
-      hi = min(max(a.cu[s + 1], lo), a.n);
+  int s0 = 0;
+  for (; s0 + 256 < a.nseq; s0 += 256) {                             // many sequences: 256 per round trip
+    int sum = 0, lo, hi;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      rows_of(s0 + 32 * k + lane, lo, hi);
+      sum += (hi - lo + T - 1) / T;
     }
+    const long long all = __reduce_add_sync(0xffffffffu, sum);
+    if (before + all > idx) break;
+    before += all;
+  }
+  for (; s0 < a.nseq; s0 += 32) {
+    const int s = s0 + lane;
+    int lo, hi;
+    rows_of(s, lo, hi);
+    const int ctx = s < a.nseq ? a.lens[s] : 0;
     const int mine = (hi - lo + T - 1) / T;
     int inc = mine;
 #pragma unroll

@@ -295,3 +295,11 @@ def test_a_graph_follows_its_inputs(cuda_lib):
         torch.cuda.synchronize()
         ref = c.ref()
         assert np.all(np.abs(out.double().cpu().numpy() - ref) <= 2e-5 * c.vmax)
+
+
+def test_hundreds_of_sequences(cuda_lib):
+    """Boundaries are searched 256 sequences at a time before 32."""
+    rng = np.random.default_rng(73)
+    lens = rng.integers(0, 4, 901)
+    lens[[255, 256, 512, 900]] = 40, 0, 70, 3
+    Prompt("fp8", 8, 2, 64, lens.tolist(), rng.integers(0, 30, 901).tolist(), seed=74, tail=2).check()
