@@ -648,12 +648,15 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     sm_mx[0][s][r] = l;
     named_bar(1, 256);
     const float L = l + sm_mx[0][s ^ 1][r];
-    const float wgt = pos < 0 ? 0.f : a.v_scale / L * (S::BF ? exponent(max(vbase, 0)) : 1.f);
+    // BF16: o / L, the exponent and the scale one after the other (the product of
+    // the last two with 1 / L can be too small for fp32 where the output is not)
+    const float wgt = pos < 0 ? 0.f : S::BF ? 1.f / L : a.v_scale / L, unit = exponent(max(vbase, 0));
+    auto result = [&](float x) { return S::BF ? x * wgt * unit * a.v_scale : x * wgt; };
     float* stage = reinterpret_cast<float*>(smem) + r * S::LDO + s * E;
 #pragma unroll
     for (int i = 0; i < E; i += 4) {
       const float2 x = pa_unpair(o[i / 2]), y = pa_unpair(o[i / 2 + 1]);
-      *reinterpret_cast<float4*>(stage + i) = make_float4(x.x * wgt, x.y * wgt, y.x * wgt, y.y * wgt);
+      *reinterpret_cast<float4*>(stage + i) = make_float4(result(x.x), result(x.y), result(y.x), result(y.y));
     }
     if (sm_poison) {                                                 // rare: non-finite V among the tile's own tokens
       // from the first block whose values the loader guarded

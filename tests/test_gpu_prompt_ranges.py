@@ -1,0 +1,48 @@
+"""Prompt attention where values of very different sizes meet: queries of zero,
+of the smallest and the largest magnitudes, cached values that differ by many
+powers of two, infinities and NaN in single channels, extreme scales.
+
+Tolerance: 2e-5 of the largest |V| among the tokens a row attends to (queries and
+probabilities as FP16 high and low parts, 2^-22 relative; BF16 caches as FP16
+with an exponent per 16 tokens, 2^-30 of the largest)."""
+import numpy as np
+import pytest
+import torch
+
+from memory_bound_transformer_gb300 import capi
+from oracle.kv_fp4 import pool_values, prompt_positions, rows_attention
+from oracle.numerics import bf16_decode, round_bf16
+from tests.test_gpu_kv_fp4 import Decode
+from tests.test_gpu_prompt_attention import KINDS, Prompt
+
+pytestmark = pytest.mark.gpu
+
+
+def check_rows(c, rows=None):
+    """Rows (all, or those of the mask) against the oracle, each within 2e-5 of the largest |V| it attends to."""
+    got, err = c.run()
+    assert err == 0
+    seq, pos = prompt_positions(c.cu, c.ctx, c.n)
+    k, v = pool_values(c.kp, c.kind, c.d, c.kg), pool_values(c.vp, c.kind, c.d, c.vg)
+    pick = np.flatnonzero((seq >= 0) & (pos >= 0) & (True if rows is None else rows))
+    ref = rows_attention(c.q[pick], k, v, c.bt, seq[pick], pos[pick]).reshape(len(pick), c.nq, c.d)
+    got = got.reshape(c.n, c.nq, c.d)[pick]
+    for i, at in enumerate(pick):
+        seen = v[c.bt[seq[at], :pos[at] // 16 + 1]].transpose(1, 0, 2, 3).reshape(c.nkv, -1, c.d)[:, :pos[at] + 1]
+        most = np.abs(seen).max((1, 2)).repeat(c.nq // c.nkv)[:, None]
+        # (a V of zeros reads as up to 2^-126 of either sign: FP16's smallest normal at the lowest exponent)
+        assert np.all(np.abs(got[i] - ref[i]) <= 2e-5 * most + c.vg * 2.0 ** -126), (at, np.abs(got[i] - ref[i]).max(), most.max())
+    return got
+
+
+# --- scales at their limits --------------------------------------------------
+
+@pytest.mark.parametrize("kind,vg,up", [(k, vg, 0) for k in KINDS for vg in (2.0 ** -64, 2.0 ** 64)] +
+                         [("bf16", 2.0 ** -64, -20), ("bf16", 2.0 ** -64, -60), ("bf16", 2.0 ** 64, -80), ("bf16", 2.0 ** 64, 50)])
+def test_extreme_value_scales(cuda_lib, kind, vg, up):
+    """Outputs in fp32's normal range are right for every v_scale that is taken."""
+    c = Prompt(kind, 4, 2, 64, [40], [30], seed=90, vg=1.0)
+    if up:
+        c.vp[...] = round_bf16(bf16_decode(c.vp) * 2.0 ** up)
+    c.vg = vg
+    check_rows(c)
