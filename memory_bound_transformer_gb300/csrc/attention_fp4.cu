@@ -11,7 +11,10 @@
 //   parts (2^-22 relative) stacked on M: rows 0..7 the high parts of the group's
 //   heads, rows 8..15 the low parts. One MMA serves both, S = row g + row g + 8
 //   sits in one thread, and the S accumulators are the A fragments of P V as
-//   they stand: nothing is transposed or shuffled.
+//   they stand: nothing is transposed or shuffled. Probabilities are relative to
+//   2^-14 of the largest so far, not to the largest: FP16's smallest steps, which
+//   take from many small ones what their sum still counts, then lie at 2^-39 of
+//   the largest (2^-22 holds down to 2^-17 of it). The factor cancels in o / l.
 // * K and V fragments come straight from the raw codes. The contraction may
 //   run over the channels in any order, so thread (g, t) of a warp takes D / 4
 //   neighbouring channels of a token (one 16-byte load at d = 128) and the
@@ -54,6 +57,7 @@ constexpr int kF4Step = 64;                 // tokens per step: four cache block
 constexpr int kF4Blocks = kF4Step / kBlockTokens;
 constexpr int kF4Heads = 8;                 // query heads per CTA (MMA rows, high and low parts)
 constexpr int kF4Cluster = 8;               // most CTAs of a cluster
+constexpr float kF4Up = 14.f;               // probabilities go up to 2^14
 
 template <int D>
 struct Fp4Shape {
@@ -148,7 +152,8 @@ __device__ __forceinline__ int blocks_from(int seq, int j) {          // cache b
 }
 
 // One warp's part of a (row, KV head): queries of up to eight heads as MMA
-// fragments, running maximum (log2 domain), sum (this lane's share) and output.
+// fragments, running maximum less kF4Up (log2 domain), sum (this lane's share)
+// and output.
 template <int D>
 struct Fp4Warp {
   using S = Fp4Shape<D>;
@@ -240,7 +245,7 @@ struct Fp4Warp {
     for (int nt = 0; nt < TT; ++nt) mx = fmaxf(mx, fmaxf(p[nt][0], p[nt][1]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const float mn = fmaxf(m, mx * fac), mu = mn == -INFINITY ? 0.f : mn;
+    const float mn = fmaxf(m, fmaf(mx, fac, -kF4Up)), mu = mn == -INFINITY ? 0.f : mn;
     const float al = ex2(m - mu);
     m = mn;
     l *= al;

@@ -18,7 +18,10 @@
 //                    an M = 128 MMA per ~100 cycles, two reach the pipe's 64)
 // Accuracy is that of single-token attention: queries and probabilities enter
 // as FP16 high and low parts (2^-22), two MMAs per product, low part first. So
-// the floor is twice the formula's operations at the tensor rate. e4m3 and 4-bit
+// the floor is twice the formula's operations at the tensor rate. Probabilities
+// are relative to 2^-14 of the row's largest so far (the factor cancels in o / l),
+// which puts FP16's smallest steps at 2^-39 of it: many small ones behind one
+// large one keep their share. e4m3 and 4-bit
 // values widen to FP16 exactly. BF16 values get one exponent per 16 tokens (a
 // cache block of a head) that puts the largest just below 2^16: exact down to
 // 2^-29 of it, 2^-30 of it off below; scores take the exponent with the query
@@ -64,6 +67,7 @@ constexpr int kPaRows = 128;                // query rows and keys per tile
 constexpr int kPaThreads = 640;
 constexpr uint32_t kPaO = 256, kPaQ = 384;  // TMEM columns (scores at 0 and 128)
 constexpr int kPaIssueRegs = 32;
+constexpr float kPaUp = 14.f;               // probabilities go up to 2^14
 
 template <int D, int KV>
 struct PaShape {
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       sm_mx[j & 1][s][r] = mx;
       named_bar(2 + (warp & 3), 64);                                 // the rows' two warps
       mx = fmaxf(mx, sm_mx[j & 1][s ^ 1][r]);
-      const float mn = fmaxf(m, mx * fac), mu = mn == -INFINITY ? 0.f : mn;
+      const float mn = fmaxf(m, fmaf(mx, fac, -kPaUp)), mu = mn == -INFINITY ? 0.f : mn;
       float al = pa_ex2(m - mu);
       m = mn;
       l *= al;
@@ -604,7 +608,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         al *= pa_ex2((float)(vbase - top));
         vbase = top;
       }
-      // P = 2^(score - maximum), for BF16 times 2^(block's base - vbase)
+      // P = 2^(score - maximum + 14), for BF16 times 2^(block's base - vbase)
       uint64_t ls[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < C; c += 16) {
