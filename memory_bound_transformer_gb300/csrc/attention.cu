@@ -357,7 +357,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* smem, i
       }
 
   // softmax state of this thread's two heads per n-tile (nt*8 + 2*t4, +1),
-  // the same in every lane of a column group
+  // the same in every lane of a column group. The running maximum is kept less
+  // `up`: FP16 probabilities go up to 2^14, so that their smallest steps lie at
+  // 2^-39 of the largest and not at 2^-25, where thousands of small ones lose
+  // what the sum still counts; the factor cancels in o / l
+  constexpr float up = KV8 ? 14.f : 0.f;
   float mst[NT][2], lst[NT][2];
   float o[NT][S::MT][4];                                              // O^T: 16 d x 8 heads per m-tile
 #pragma unroll
@@ -470,7 +474,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* smem, i
         float al[2], ps[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float mn = fmaxf(mst[nt][c], mx[c]);
+          const float mn = fmaxf(mst[nt][c], mx[c] - up);
           const float mu = mn == -INFINITY ? 0.f : mn;
           al[c] = exp2f(mst[nt][c] - mu);
           const float pa = exp2f(st[nt][c] - mu), pb = exp2f(st[nt][c + 2] - mu);

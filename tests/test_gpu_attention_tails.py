@@ -75,3 +75,17 @@ def test_prompt(cuda_lib, kind, nq, nkv, d, n, nats):
     capi.op_prompt_attention(dev(q, torch.float32), nkv, dev([0, 3]), dev([n + 1]), k, v, KINDS[kind], 1.0, 1.0, dev(bt), nb, out)
     for i, got in enumerate(out.double().cpu().numpy()):
         assert np.abs(got - one * share(n - 2 + i, nats)).max() <= 2e-5 * one
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,nats", TAILS)
+@pytest.mark.parametrize("rows,nq,nkv,d", [(1, 4, 1, 64), (48, 16, 8, 128), (3, 16, 1, 128)])
+def test_single_token_bf16_and_e4m3(cuda_lib, kind, rows, nq, nkv, d, n, nats):
+    lens = [n + 1] * rows if rows < 40 else [n + 1] + [20] * (rows - 1)
+    k, v, bt, nb, one = pools(kind, lens, nkv, d)
+    bt[bt < 0] = nb
+    q, nats = queries(rows, nq, d, nats)
+    out = torch.zeros((rows, nq * d), device=DEV)
+    capi.op_paged_attention(dev(q, torch.float32), nkv, k, v, KINDS[kind], 1.0, 1.0, dev(bt), dev(lens), nb, out)
+    for got, size in zip(out.double().cpu().numpy(), lens):
+        assert np.abs(got - one * share(size - 1, nats)).max() <= 2e-5 * one
