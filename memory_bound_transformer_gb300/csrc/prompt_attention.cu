@@ -526,7 +526,6 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       const float up = __int_as_float((e + 127) << 23);
       fac = 1.4426950408889634f / sqrtf((float)D) * a.k_scale * __int_as_float((127 - e) << 23);
       fac = fmaxf(fac, 1.2e-38f);                                    // masked scores (-inf) stay -inf
-      if (big >= 0x7f800000u) fac = __int_as_float(0x7fc00000);      // a non-finite query: its row is NaN
 #pragma unroll
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t hi[8], lo[8];
@@ -654,7 +653,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     const float L = l + sm_mx[0][s ^ 1][r];
     // BF16: o / L, the exponent and the scale one after the other (the product of
     // the last two with 1 / L can be too small for fp32 where the output is not)
-    const float wgt = pos < 0 ? 0.f : S::BF ? 1.f / L : a.v_scale / L, unit = exponent(max(vbase, 0));
+    const bool finite = max(sm_big[0][r], sm_big[1][r]) < 0x7f800000u;   // the query; NaN where it is not
+    const float wgt = pos < 0 ? 0.f : !finite ? __int_as_float(0x7fc00000) : S::BF ? 1.f / L : a.v_scale / L, unit = exponent(max(vbase, 0));
     auto result = [&](float x) { return S::BF ? x * wgt * unit * a.v_scale : x * wgt; };
     float* stage = reinterpret_cast<float*>(smem) + r * S::LDO + s * E;
 #pragma unroll

@@ -46,3 +46,22 @@ def test_extreme_value_scales(cuda_lib, kind, vg, up):
         c.vp[...] = round_bf16(bf16_decode(c.vp) * 2.0 ** up)
     c.vg = vg
     check_rows(c)
+
+
+# --- queries that are not finite --------------------------------------------
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_queries_that_are_not_finite(cuda_lib, kind):
+    """A row whose query is not finite is NaN in that head; before position 0 a row is 0 whatever its query."""
+    c = Prompt(kind, 4, 2, 64, [60], [0], seed=89)
+    c.ctx[0] = 50                                           # the first 10 rows lie before position 0
+    want = c.ref().reshape(c.n, 4, 64)
+    for row in (0, 3, 20, 41):
+        c.q[row, 1, 7] = np.nan
+        c.q[row + 1, 2, 0] = np.inf
+    got, err = c.run()
+    got = got.reshape(c.n, 4, 64)
+    assert err == 0 and not got[:10].any()
+    bad = np.zeros((c.n, 4), bool)
+    bad[[20, 41], 1] = bad[[21, 42], 2] = True
+    assert np.isnan(got[bad]).all() and np.abs(got - want)[~bad].max() <= 2e-5 * c.vmax
