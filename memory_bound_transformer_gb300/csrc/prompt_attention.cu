@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     const int rows = t.tokens * G;
     const int pos = r < rows ? t.pos0 + (int)((r * inv) >> 16) : -1;
     constexpr int RL = D / 4, RW = 32 / RL;                          // lanes of a row's 16-byte chunks, rows per warp and access
-    float fac;
+    float fac, f1, f2;                                               // fac = f1 f2 above a lower limit
+    constexpr float kFacMin = 1.2e-38f;                              // masked scores (-inf) stay -inf
     {
       // the query rows, whole rows at a time, into the V tiles' place (the V
       // loader waits), chunks swizzled by row
@@ -524,8 +525,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       big = max(big, sm_big[s ^ 1][r]);
       const int e = min(120, 140 - (int)(big >> 23));
       const float up = __int_as_float((e + 127) << 23);
-      fac = 1.4426950408889634f / sqrtf((float)D) * a.k_scale * __int_as_float((127 - e) << 23);
-      fac = fmaxf(fac, 1.2e-38f);                                    // masked scores (-inf) stay -inf
+      // in two parts of about the same size: a product with a block's exponent
+      // then leaves fp32's range only where the whole does
+      f1 = 1.4426950408889634f / sqrtf((float)D) * a.k_scale;
+      const int half = ((__float_as_int(f1) >> 23) - 127 - e) >> 1;
+      f1 *= __int_as_float((127 - e - half) << 23);
+      f2 = __int_as_float((127 + half) << 23);
+      fac = fmaxf(f1 * f2, kFacMin);
 #pragma unroll
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t hi[8], lo[8];
@@ -547,6 +553,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) o[i] = 0;
     auto exponent = [](int e) { return __int_as_float((e + 15) << 23); };   // 2^(e - 112)
+    // BF16: the factor of a block's scores (a block of zeros has exponent 2^-112)
+    auto factor = [&](int base) { return fmaxf(exponent(base) * f2 * f1, kFacMin); };
     // adds tile j's P V, rescaling what is there by `al`
     auto drain = [&](int j, float al) {
       if (!__all_sync(0xffffffffu, pa_wait(&bars.ofull[j & 1], (j >> 1) & 1, &sm_stop))) return false;
@@ -589,12 +597,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         auto at = [&](int k) { return __uint_as_float(v[(c + k) / 32][(c + k) % 32]); };
         const float x0 = pa_max3(pa_max3(at(0), at(1), at(2)), at(3), at(4)), x1 = pa_max3(pa_max3(at(5), at(6), at(7)), at(8), at(9));
         const float y = pa_max3(pa_max3(x0, x1, at(10)), pa_max3(at(11), at(12), at(13)), fmaxf(at(14), at(15)));
-        mx = fmaxf(mx, S::BF ? y * exponent(sm_kbase[j & 3][(s * C + c) / 16]) : y);
+        mx = fmaxf(mx, S::BF ? y * factor(sm_kbase[j & 3][(s * C + c) / 16]) : y);
       }
       sm_mx[j & 1][s][r] = mx;
       named_bar(2 + (warp & 3), 64);                                 // the rows' two warps
       mx = fmaxf(mx, sm_mx[j & 1][s ^ 1][r]);
-      const float mn = fmaxf(m, fmaf(mx, fac, -kPaUp)), mu = mn == -INFINITY ? 0.f : mn;
+      const float mn = fmaxf(m, S::BF ? mx - kPaUp : fmaf(mx, fac, -kPaUp)), mu = mn == -INFINITY ? 0.f : mn;
       float al = pa_ex2(m - mu);
       m = mn;
       l *= al;
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
 #pragma unroll
       for (int c = 0; c < C; c += 16) {
         const int blk = (s * C + c) / 16;
-        const float fc = S::BF ? fac * exponent(sm_kbase[j & 3][blk]) : fac;
+        const float fc = S::BF ? factor(sm_kbase[j & 3][blk]) : fac;
         const float off = S::BF ? (float)max(sm_vbase[j & 1][blk] - vbase, -80) : 0.f;   // below: nothing beside the largest
         uint64_t part[2] = {0, 0};
         uint32_t hi[8], lo[8];

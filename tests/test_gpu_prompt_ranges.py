@@ -65,3 +65,34 @@ def test_queries_that_are_not_finite(cuda_lib, kind):
     bad = np.zeros((c.n, 4), bool)
     bad[[20, 41], 1] = bad[[21, 42], 2] = True
     assert np.isnan(got[bad]).all() and np.abs(got - want)[~bad].max() <= 2e-5 * c.vmax
+
+
+# --- small and zero queries -------------------------------------------------
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("kg", [0.75, 2.0 ** -30, 2.0 ** -64])
+@pytest.mark.parametrize("lens,prefix", [([37], [0]), ([5, 150], [40, 3])])
+def test_small_and_zero_queries(cuda_lib, kind, kg, lens, prefix):
+    """Scores of 0, or as good as: those rows are the mean of their V."""
+    c = Prompt(kind, 4, 2, 64, lens, prefix, seed=80, kg=kg)
+    for i, scale in enumerate((0.0, 2.0 ** -20, 2.0 ** -30, 2.0 ** -60, 2.0 ** -100, 2.0 ** -126, 1.0)):
+        c.q[i::7] *= np.float32(scale)
+    check_rows(c)
+
+
+def test_small_and_zero_queries_of_single_tokens(cuda_lib):
+    for kg in (0.75, 2.0 ** -64):
+        c = Decode(8, 2, 64, [37, 1, 300, 64, 16, 5, 90], seed=81, kg=kg)
+        for i, scale in enumerate((0.0, 2.0 ** -20, 2.0 ** -30, 2.0 ** -60, 2.0 ** -100, 2.0 ** -126, 1.0)):
+            c.q[i] *= np.float32(scale)
+        c.check()
+
+
+@pytest.mark.parametrize("up", [40, 80, 110])
+def test_small_queries_meet_large_keys(cuda_lib, up):
+    """Queries of 2^-up over BF16 keys of 2^up, and the other way round: ordinary scores."""
+    for q, k in ((-up, up), (up, -up)):
+        c = Prompt("bf16", 4, 2, 64, [70], [100], seed=82, kg=1.0)
+        c.kp[...] = round_bf16(bf16_decode(c.kp) * 2.0 ** k)
+        c.q *= np.float32(2.0 ** q)
+        check_rows(c)
