@@ -370,21 +370,13 @@ __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char*
         v[0] = e4m3x2_to_h2bits(w[2 * k]); v[1] = e4m3x2_to_h2bits(w[2 * k] >> 16);
         v[2] = e4m3x2_to_h2bits(w[(2 * k + 1) & 3]); v[3] = e4m3x2_to_h2bits(w[(2 * k + 1) & 3] >> 16);
       } else {
-        // (magnitude - (base << 7)) << 3 in both halves at once, sign kept
+        // (magnitude - (base << 7)) << 3 in both halves at once, sign kept; values
+        // that are not finite (zeros meanwhile, which stay in their half) to FP16's
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = (pa_max2(w[e] & 0x7fff7fffu, low) * 8u + shift) | (w[e] & 0x80008000u);
-        if (EDGE) {                                                  // non-finite values: FP16 infinity or NaN
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t out = 0;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t x = w[e] >> (16 * half) & 0xffffu, f = v[e] >> (16 * half) & 0xffffu;
-              out |= ((x & 0x7f80u) == 0x7f80u ? (x & 0x8000u) | 0x7c00u | ((x & 0x7fu) ? 0x200u : 0u) : f) << (16 * half);
-            }
-            v[e] = out;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = w[e] & 0x7fff7fffu, bad = EDGE ? __vcmpgeu2(x, 0x7f807f80u) : 0u;
+          v[e] = (pa_max2(x & ~bad, low) * 8u + shift) | (w[e] & 0x80008000u);
+          if (EDGE) v[e] = (v[e] & ~(bad & 0x7fff7fffu)) | (bad & 0x7c007c00u) | (__vcmpgtu2(x, 0x7f807f80u) & 0x02000200u);
         }
       }
       if (EDGE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;       // whatever the raw block's place held

@@ -96,3 +96,26 @@ def test_small_queries_meet_large_keys(cuda_lib, up):
         c.kp[...] = round_bf16(bf16_decode(c.kp) * 2.0 ** k)
         c.q *= np.float32(2.0 ** q)
         check_rows(c)
+
+
+# --- single values that are not finite --------------------------------------
+
+def one_bad_channel(tok, ch, bits):
+    """(output with V's channel `ch` of token `tok` in KV head 1 replaced, output without, where it counts, tolerance)."""
+    c = Prompt("bf16", 4, 2, 128, [90], [100], seed=86, kg=1.0, vg=1.0)
+    want = c.ref().reshape(c.n, c.nq, c.d)
+    c.vp[c.bt[0, tok // 16], 1, tok % 16, ch] = bits
+    got, err = c.run()
+    assert err == 0
+    at = np.zeros(want.shape, bool)
+    at[max(0, tok - 100):, 2:, ch] = True
+    return got.reshape(want.shape), want, at, 2e-5 * c.vmax
+
+
+@pytest.mark.parametrize("tok", [3, 99, 100, 131, 180])
+@pytest.mark.parametrize("bits", [0x7F80, 0xFF80, 0x7FC0])
+def test_neighbours_of_a_value_that_is_not_finite(cuda_lib, tok, bits):
+    """An infinity or a NaN in one channel of one token's V leaves the other channels, and the rows before it, alone."""
+    for ch in (6, 7, 64, 127):
+        got, want, at, tol = one_bad_channel(tok, ch, bits)
+        assert np.abs(got - want)[~at].max() <= tol and not np.isfinite(got[at]).any()
