@@ -51,9 +51,12 @@
 // first of these): the state they carry takes the loop's registers.
 //
 // A value of V that is not finite at a token some rows of the tile do not attend
-// to would reach them as 0 x inf: the loader stores 0 for it and raises a flag,
-// and the rows that do attend to it add it at the end.
+// to would reach them as 0 x inf, and an infinity those that do as inf + 0 x inf
+// (a probability's low part): the loader stores 0 for it and notes its block, and
+// the rows that attend to it add it at the end. (NaN, all that e4m3 and 4-bit
+// caches have, is left where every row of the tile attends to it.)
 #include <algorithm>
+#include <climits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -418,8 +421,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   __shared__ uint32_t tmem_slot, sm_big[2][kPaRows];
   __shared__ float sm_mx[2][2][kPaRows];                             // halves' maxima: even and odd tiles
   __shared__ PaTile sm_tile;
-  // BF16 exponent bases of the tiles' blocks; a K tile's outlive its buffer
-  __shared__ int sm_ok, sm_poison, sm_kbase[4][8], sm_vbase[2][8];
+  // cache blocks with values of V replaced by 0; BF16 exponent bases of the tiles'
+  // blocks, a K tile's outlive its buffer
+  __shared__ int sm_ok, sm_bad_first, sm_bad_last, sm_kbase[4][8], sm_vbase[2][8];
   __shared__ volatile int sm_stop;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int G = a.nq / a.nkv, T = kPaRows / G, h = (int)(blockIdx.x % (unsigned)a.nkv);
@@ -431,7 +435,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       sm_ok = ok;
       if (ok) sm_tile = t;
       sm_stop = 0;
-      sm_poison = 0;
+      sm_bad_first = INT_MAX;
+      sm_bad_last = -1;
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -662,15 +667,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       const float2 x = pa_unpair(o[i / 2]), y = pa_unpair(o[i / 2 + 1]);
       *reinterpret_cast<float4*>(stage + i) = make_float4(result(x.x), result(x.y), result(y.x), result(y.y));
     }
-    if (sm_poison) {                                                 // rare: non-finite V among the tile's own tokens
-      // from the first block whose values the loader guarded
-      for (int tok = max(0, t.pos0 + 1) / kBlockTokens * kBlockTokens; tok <= pos; ++tok) {
+    if (sm_bad_last >= 0) {                                          // rare
+      for (int tok = sm_bad_first * kBlockTokens; tok <= min(pos, sm_bad_last * kBlockTokens + kBlockTokens - 1); ++tok) {
         int id = a.bt[(size_t)t.seq * a.bt_stride + tok / kBlockTokens];
         if ((uint32_t)id > (uint32_t)a.num_blocks) id = a.num_blocks;
         const unsigned char* u = reinterpret_cast<const unsigned char*>(a.vpool) + ((size_t)id * a.nkv + h) * S::UNIT;
         for (int ch = 0; ch < E; ++ch) {
           const float x = pa_value<D, KV>(u, tok % kBlockTokens, s * E + ch);
-          if (!(fabsf(x) <= 3.0e38f)) stage[ch] += x;
+          if (!isfinite(x)) stage[ch] += x;
         }
       }
     }
@@ -737,7 +741,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
           if (lane == 0) (is_k ? sm_kbase[j & 3] : sm_vbase[buf])[at] = base;
         }
         if (guard || high || keep < kBlockTokens) {
-          if (pa_store<D, KV, true>(raw, tile, at * kBlockTokens, keep, guard, lane, base)) sm_poison = 1;
+          if (pa_store<D, KV, true>(raw, tile, at * kBlockTokens, keep, guard || (high && !is_k), lane, base)) {
+            atomicMin(&sm_bad_first, tok0 / kBlockTokens);
+            atomicMax(&sm_bad_last, tok0 / kBlockTokens);
+          }
         } else {
           pa_store<D, KV, false>(raw, tile, at * kBlockTokens, kBlockTokens, false, lane, base);
         }

@@ -119,3 +119,38 @@ def test_neighbours_of_a_value_that_is_not_finite(cuda_lib, tok, bits):
     for ch in (6, 7, 64, 127):
         got, want, at, tol = one_bad_channel(tok, ch, bits)
         assert np.abs(got - want)[~at].max() <= tol and not np.isfinite(got[at]).any()
+
+
+@pytest.mark.parametrize("tok", [3, 99, 100, 131, 180])
+@pytest.mark.parametrize("bits,what", [(0x7F80, np.inf), (0xFF80, -np.inf), (0x7FC0, np.nan)])
+def test_one_channel_that_is_not_finite(cuda_lib, tok, bits, what):
+    """The rows that attend to an infinity have it, wherever it lies: it is added with a weight above 0."""
+    got, _, at, _ = one_bad_channel(tok, 6, bits)
+    assert np.all(np.isnan(got[at])) if np.isnan(what) else np.all(got[at] == what)
+
+
+@pytest.mark.parametrize("tok", [20, 120])
+def test_infinities_of_both_signs_are_nan(cuda_lib, tok):
+    c = Prompt("bf16", 4, 2, 64, [50], [100], seed=87)
+    c.vp[c.bt[0, tok // 16], 0, tok % 16, 5] = 0x7F80
+    c.vp[c.bt[0, 135 // 16], 0, 135 % 16, 5] = 0xFF80
+    got = c.run()[0].reshape(c.n, 4, 64)[:, :2, 5]
+    first = max(0, tok - 100)
+    assert np.all(np.isfinite(got[:first])) and np.all(got[first:35] == np.inf) and np.isnan(got[35:]).all()
+
+
+def test_large_finite_values_beside_a_nan(cuda_lib):
+    """BF16 values above 3.0e38 are finite, also where the slow path for values that are not finite runs."""
+    c = Prompt("bf16", 4, 2, 64, [60], [100], seed=88, kg=1.0, vg=1.0)
+    c.ref()                                                 # sets vmax, of the ordinary values
+    c.vp[c.bt[0, 130 // 16], :, 130 % 16, 3] = 0x7F7F       # 3.39e38
+    c.vp[c.bt[0, 120 // 16], :, 120 % 16, 9] = 0x7FC0
+    got, err = c.run()
+    got = got.reshape(c.n, 4, 64)
+    v = pool_values(c.vp, "bf16", 64, 1.0)
+    v[c.bt[0, 120 // 16], :, 120 % 16, 9] = 0.0
+    seq, pos = prompt_positions(c.cu, c.ctx, c.n)
+    ref = rows_attention(c.q, pool_values(c.kp, "bf16", 64, 1.0), v, c.bt, seq, pos).reshape(c.n, 4, 64)
+    assert err == 0 and np.isnan(got[20:, :, 9]).all()
+    assert np.abs(got - ref)[30:, :, 3].max() <= 2e-5 * 3.39e38
+    assert np.abs(got - ref)[:20].max() <= 2e-5 * c.vmax
