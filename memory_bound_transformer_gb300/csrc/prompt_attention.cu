@@ -60,6 +60,7 @@
 
 #include "fp4.cuh"
 #include "internal.h"
+#include "pair_loop.h"
 #include "tcgen05.cuh"
 
 namespace mbt {
@@ -570,16 +571,16 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       if (lane == 0) mbar_arrive(&bars.ofree);
       return true;
     };
-    bool ok = true;
-#pragma unroll 1
-    for (int j = 0; j < ntiles; ++j) {
-      ok = __all_sync(0xffffffffu, pa_wait(&bars.sfull[j & 1], (j >> 1) & 1, &sm_stop));
-      if (!ok) break;
+    auto wait_all = [&](uint64_t* b, int j) { return __all_sync(0xffffffffu, pa_wait(b + (j & 1), (j >> 1) & 1, &sm_stop)); };
+    auto columns = [&](int j) { return tmem + lanes + 128u * (j & 1) + s * C; };   // of tile j's scores
+    uint32_t v[2][32];
+    float mx;
+    auto maximum = [&](int j, bool ok) {
+      ok = ok && wait_all(bars.sfull, j);
       tc_fence_after();
-      const uint32_t sc = tmem + lanes + 128u * (j & 1) + s * C;
+      const uint32_t sc = columns(j);
       const int lim = pos - j * kPaRows - s * C;                     // columns 0..lim are seen
       const bool masked = __any_sync(0xffffffffu, lim < C - 1);
-      uint32_t v[2][32];
       pa_ld32(sc, v[0]);
       pa_ld32(sc + 32, v[1]);
       pa_ld_wait32(v[0]);
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
 #pragma unroll
         for (int k = 0; k < C; ++k) if (k > lim) v[k / 32][k % 32] = 0xff800000u;
       }
-      float mx = -INFINITY;
+      mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < C; c += 16) {                              // 16 columns: a cache block
         auto at = [&](int k) { return __uint_as_float(v[(c + k) / 32][(c + k) % 32]); };
@@ -597,15 +598,17 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         mx = fmaxf(mx, S::BF ? y * factor(sm_kbase[j & 3][(s * C + c) / 16]) : y);
       }
       sm_mx[j & 1][s][r] = mx;
-      named_bar(2 + (warp & 3), 64);                                 // the rows' two warps
+      return ok;
+    };
+    auto rest = [&](int j) {
+      const uint32_t sc = columns(j);
       mx = fmaxf(mx, sm_mx[j & 1][s ^ 1][r]);
       const float mn = fmaxf(m, S::BF ? mx - kPaUp : fmaf(mx, fac, -kPaUp)), mu = mn == -INFINITY ? 0.f : mn;
       float al = pa_ex2(m - mu);
       m = mn;
       l *= al;
       if (S::BF) {                                                   // V's largest exponent so far
-        ok = __all_sync(0xffffffffu, pa_wait(&bars.vfull[j & 1], (j >> 1) & 1, &sm_stop));
-        if (!ok) break;
+        if (!wait_all(bars.vfull, j)) return false;
         int top = vbase;
 #pragma unroll
         for (int c = 0; c < kPaRows / 16; ++c) top = max(top, sm_vbase[j & 1][c]);
@@ -646,11 +649,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.pfull[j & 1]);
       // the previous tile's P V, done meanwhile
-      if (j && !(ok = drain(j - 1, al_prev))) break;
+      const bool ok = !j || drain(j - 1, al_prev);
       al_prev = al;
-    }
-    if (ok) ok = drain(ntiles - 1, al_prev);
-    if (!ok && tid == 0) set_err(a.err, MBT_DEV_WAIT_LIMIT);
+      return ok;
+    };
+    auto meet = [&](int, bool ok) { return named_bar_and(2 + (warp & 3), 64, ok); };   // the rows' two warps
+    if (pair_tiles(0, ntiles, true, maximum, meet, rest)) drain(ntiles - 1, al_prev);
 
     // all products and copies are done: rows through the drained tiles, stored whole
     sm_mx[0][s][r] = l;
@@ -798,13 +802,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       }
       if (pa_elect()) umma_commit(&bars.done[s]);
       __syncwarp();
-      mbar_wait(&bars.done[s], 0);
+      if (!mbar_wait(&bars.done[s], 0)) sm_stop = 1;
     }
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (tid == 0 && sm_stop) set_err(a.err, MBT_DEV_WAIT_LIMIT);       // some warp's wait ran out
   release();
 }
 

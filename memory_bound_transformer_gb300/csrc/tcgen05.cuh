@@ -106,15 +106,22 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
 }
-// Barrier among `n` threads (a multiple of 32) under id `id` (1..15).
 __device__ __forceinline__ int ld_acquire_gpu(const int* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 
+// Barrier among `n` threads (a multiple of 32) under id `id` (1..15).
 __device__ __forceinline__ void named_bar(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// The same; whether `ok` holds in all of them.
+__device__ __forceinline__ bool named_bar_and(int id, int n, bool ok) {
+  uint32_t all;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n bar.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(all) : "r"(id), "r"(n), "r"((uint32_t)ok) : "memory");
+  return all != 0;
 }
 
 }  // namespace mbt
