@@ -25,7 +25,10 @@
 // values widen to FP16 exactly. BF16 values get one exponent per 16 tokens (a
 // cache block of a head) that puts the largest just below 2^16: exact down to
 // 2^-29 of it, 2^-30 of it off below; scores take the exponent with the query
-// scale, probabilities with the softmax's offset, both for free.
+// scale, probabilities with the softmax's offset, both for free. In tiles of keys
+// that some query row does not see whole, the last one or two, the exponent is
+// per token and of the largest value up to it, and a row takes V relative to the
+// largest exponent of what it attends to: nothing depends on later tokens.
 // Queries and probabilities are the A operand in tensor memory (the tile of K
 // or V is then the only operand read from shared memory: an M = N = 128 MMA with
 // both there needs all of its bandwidth); probabilities take the place of the
@@ -83,9 +86,9 @@ struct PaShape {
   static constexpr int NCH = kBlockTokens * (D / CPC) / 32;   // chunks of a block per lane
   static constexpr int PANEL = kPaRows * 128;         // 128 tokens x 64 channels, 128-byte swizzle
   static constexpr int TILE = D / 64 * PANEL;
-  // registers: 256 x 168 + 256 x 56 + 128 x 32 (BF16: 144 and 80, its loader holds
+  // registers: 256 x 168 + 256 x 56 + 128 x 32 (BF16: 152 and 72, its loader holds
   // a raw block) = 640 x 96, what the block is launched with
-  static constexpr int SOFTMAX_REGS = BF ? 144 : 168, LOAD_REGS = BF ? 80 : 56;
+  static constexpr int SOFTMAX_REGS = BF ? 152 : 168, LOAD_REGS = BF ? 72 : 56;
   static constexpr int LDO = D + 4;                   // output staging row, floats
   static constexpr int STAGES = BF ? 1 : 2;           // raw pairs of blocks of a loader warp
   static constexpr int SMEM = 4 * TILE + 8 * STAGES * 2 * UNIT + 1024;
@@ -134,6 +137,11 @@ __device__ __forceinline__ float2 pa_unpair(uint64_t p) {
 __device__ __forceinline__ uint64_t pa_fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pa_mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t pa_add2(uint64_t a, uint64_t b) {
@@ -318,37 +326,57 @@ __device__ __forceinline__ uint32_t pa_block_max(const PaRaw<D, KV_BF16>& raw, b
   const uint32_t x = pa_max2(pa_max2(m[0], m[1]), pa_max2(m[2], m[3]));
   return __reduce_max_sync(0xffffffffu, max(x >> 16, x & 0xffffu));
 }
-// Exponent base of a BF16 block's first `keep` tokens (the others become zeros):
-// FP16 exponent field = BF16 field - base, the largest finite value's at 30.
-// `high` (uniform): some value is not finite.
+// Exponent base of a BF16 block: FP16 exponent field = BF16 field - base, the
+// largest finite value's at 30. `high` (uniform): some value is not finite.
 template <int D>
-__device__ __forceinline__ int pa_block_base(PaRaw<D, KV_BF16>& raw, int keep, int lane, bool& high) {
-  if (keep < kBlockTokens) {
-#pragma unroll
-    for (int q = 0; q < PaShape<D, KV_BF16>::NCH; ++q) {
-      int panel, row, part;
-      pa_chunk<D, KV_BF16>(q, lane, panel, row, part);
-      if (row >= keep) raw.c[q] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
+__device__ __forceinline__ int pa_block_base(const PaRaw<D, KV_BF16>& raw, bool& high) {
   uint32_t m = pa_block_max<D>(raw, false);
   high = m >= 0x7f80u;
   if (high) m = pa_block_max<D>(raw, true);                          // rare
   return max(0, (int)(m >> 7) - 30);
 }
+// The same per token of a raw block's first `keep`, each over the tokens up to it.
+// Two lanes per token, half of its channels each.
+template <int D>
+__device__ __forceinline__ void pa_token_bases(const unsigned char* u, int keep, int lane, int* out, bool& high) {
+  constexpr int N = D / 16;                                          // 16-byte chunks per lane
+  const int token = lane >> 1, half = lane & 1;
+  const unsigned char* row = u + token * (2 * D) + half * N * 16;
+  auto largest = [&](bool finite) {                                  // chunks in an order that keeps eight lanes in different banks
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint4 c = *reinterpret_cast<const uint4*>(row + ((i + token + 4 * half) & (N - 1)) * 16);
+      const uint32_t w[4] = {c.x & 0x7fff7fffu, c.y & 0x7fff7fffu, c.z & 0x7fff7fffu, c.w & 0x7fff7fffu};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x = pa_max2(x, finite ? w[e] & ~__vcmpgeu2(w[e], 0x7f807f80u) : w[e]);
+    }
+    return token < keep ? max(x >> 16, x & 0xffffu) : 0u;
+  };
+  uint32_t m = largest(false);
+  high = __any_sync(0xffffffffu, m >= 0x7f80u);
+  if (high) m = largest(true);                                       // rare
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+#pragma unroll
+  for (int o = 2; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(0xffffffffu, m, o);
+    if (lane >= o) m = max(m, t);
+  }
+  if (!half) out[token] = max(0, (int)(m >> 7) - 30);
+}
 
 // Raw chunks to FP16 values in the tile (rows R0 .. R0 + 15). Tokens from `keep`
 // on are stored as zeros; where `guard`, values that are not finite are too, and
-// the return value says whether there were any. base: a BF16 block's.
-// EDGE: for blocks that need `keep` or `guard` or (BF16) hold values that are
-// not finite; without it a block is converted with no branch inside, which
-// would keep the loop's chains from interleaving.
-template <int D, int KV, bool EDGE>
-__device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char* tile, int R0, int keep, bool guard, int lane, int base) {
+// the return value says whether there were any. BF16: `base` is the block's
+// exponent base, `tok` its tokens'.
+// MODE: PA_WHOLE converts a block with no branch inside, which would keep the
+// loop's chains from interleaving; PA_ANY takes `keep`, `guard`, values that are
+// not finite and (BF16) `tok`; PA_TOKENS (BF16) `keep` and `tok` alone.
+enum { PA_WHOLE, PA_TOKENS, PA_ANY };
+template <int D, int KV, int MODE>
+__device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char* tile, int R0, int keep, bool guard, int lane, int base, const int* tok) {
   using S = PaShape<D, KV>;
   bool found = false;
-  const uint32_t low = (uint32_t)((base + 1) << 7) * 0x10001u;       // BF16: smallest magnitude kept, FP16 exponent field 1
-  const uint32_t shift = 0u - (uint32_t)(base << 10) * 0x10001u;
 #pragma unroll
   for (int q = 0; q < S::NCH; ++q) {
     int panel, row, part;
@@ -356,6 +384,9 @@ __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char*
     const uint32_t w[4] = {raw.c[q].x, raw.c[q].y, raw.c[q].z, raw.c[q].w};
     const int R = R0 + row;
     unsigned char* dst = tile + panel * S::PANEL + R * 128;
+    const int b = MODE != PA_WHOLE && S::BF ? tok[row] : base;
+    const uint32_t low = (uint32_t)((b + 1) << 7) * 0x10001u;        // BF16: smallest magnitude kept, FP16 exponent field 1
+    const uint32_t shift = 0u - (uint32_t)(b << 10) * 0x10001u;
     uint32_t sc[2];
     if (KV == KV_FP4) {
       uint32_t s2;
@@ -378,13 +409,13 @@ __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char*
         // that are not finite (zeros meanwhile, which stay in their half) to FP16's
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t x = w[e] & 0x7fff7fffu, bad = EDGE ? __vcmpgeu2(x, 0x7f807f80u) : 0u;
+          const uint32_t x = w[e] & 0x7fff7fffu, bad = MODE == PA_ANY ? __vcmpgeu2(x, 0x7f807f80u) : 0u;
           v[e] = (pa_max2(x & ~bad, low) * 8u + shift) | (w[e] & 0x80008000u);
-          if (EDGE) v[e] = (v[e] & ~(bad & 0x7fff7fffu)) | (bad & 0x7c007c00u) | (__vcmpgtu2(x, 0x7f807f80u) & 0x02000200u);
+          if (MODE == PA_ANY) v[e] = (v[e] & ~(bad & 0x7fff7fffu)) | (bad & 0x7c007c00u) | (__vcmpgtu2(x, 0x7f807f80u) & 0x02000200u);
         }
       }
-      if (EDGE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;       // whatever the raw block's place held
-      if (EDGE && guard) {
+      if (MODE != PA_WHOLE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;       // whatever the raw block's place held
+      if (MODE == PA_ANY && guard) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t bad = __vcmpeq2(v[e] & 0x7c007c00u, 0x7c007c00u);
@@ -397,6 +428,8 @@ __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char*
   }
   return found;
 }
+
+__device__ __forceinline__ float pa_exponent(int base) { return __int_as_float((base + 15) << 23); }   // 2^(base - 112)
 
 // One cached value as fp32 (the slow path's).
 template <int D, int KV>
@@ -422,9 +455,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   __shared__ uint32_t tmem_slot, sm_big[2][kPaRows];
   __shared__ float sm_mx[2][2][kPaRows];                             // halves' maxima: even and odd tiles
   __shared__ PaTile sm_tile;
-  // cache blocks with values of V replaced by 0; BF16 exponent bases of the tiles'
-  // blocks, a K tile's outlive its buffer
-  __shared__ int sm_ok, sm_bad_first, sm_bad_last, sm_kbase[4][8], sm_vbase[2][8];
+  __shared__ int sm_ok, sm_bad_first, sm_bad_last;                   // cache blocks whose V was replaced by zeros
+  // BF16 exponent bases of the tiles' blocks, and of their tokens; a K tile's outlive its buffer
+  __shared__ int sm_kbase[4][8], sm_vbase[2][8];
+  __shared__ __align__(16) int sm_ktok[S::BF ? 4 : 1][kPaRows], sm_vtok[S::BF ? 2 : 1][kPaRows];
   __shared__ volatile int sm_stop;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int G = a.nq / a.nkv, T = kPaRows / G, h = (int)(blockIdx.x % (unsigned)a.nkv);
@@ -475,6 +509,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     release();
     return;
   }
+  // BF16: the tiles that every row sees whole have an exponent per block, those after them one per token
+  const int whole = S::BF ? min(max(t.pos0 + 1, 0) / kPaRows, ntiles) : ntiles;
   unsigned char* kbuf = smem;
   unsigned char* vbuf = smem + 2 * S::TILE;
 
@@ -550,9 +586,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     uint64_t o[E / 2];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) o[i] = 0;
-    auto exponent = [](int e) { return __int_as_float((e + 15) << 23); };   // 2^(e - 112)
-    // BF16: the factor of a block's scores (a block of zeros has exponent 2^-112)
-    auto factor = [&](int base) { return fmaxf(exponent(base) * f2 * f1, kFacMin); };
+    // BF16: the factor of scores whose keys have this exponent base
+    auto factor = [&](int base) { return pa_exponent(base) * f2 * f1; };
     // adds tile j's P V, rescaling what is there by `al`
     auto drain = [&](int j, float al) {
       if (!__all_sync(0xffffffffu, pa_wait(&bars.ofull[j & 1], (j >> 1) & 1, &sm_stop))) return false;
@@ -573,19 +608,42 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     };
     auto wait_all = [&](uint64_t* b, int j) { return __all_sync(0xffffffffu, pa_wait(b + (j & 1), (j >> 1) & 1, &sm_stop)); };
     auto columns = [&](int j) { return tmem + lanes + 128u * (j & 1) + s * C; };   // of tile j's scores
+    float mx, al;
+    // exchanges maxima with the rows' other warp; al: what the sum and the output are rescaled by
+    auto meet = [&](int j, bool ok) {
+      sm_mx[j & 1][s][r] = mx;
+      ok = named_bar_and(2 + (warp & 3), 64, ok);
+      mx = fmaxf(mx, sm_mx[j & 1][s ^ 1][r]);
+      const float mn = fmaxf(m, S::BF ? mx - kPaUp : fmaf(mx, fac, -kPaUp));
+      al = pa_ex2(m - (mn == -INFINITY ? 0.f : mn));
+      m = mn;
+      l *= al;
+      return ok;
+    };
+    // probabilities are in place: their tile's P V may start; adds the one before it, done meanwhile
+    auto next = [&](int j, float sum) {
+      l += sum;
+      pa_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.pfull[j & 1]);
+      const bool ok = !j || drain(j - 1, al_prev);
+      al_prev = al;
+      return ok;
+    };
+    // P = 2^(score - maximum + 14), for BF16 times 2^(V's base - vbase)
     uint32_t v[2][32];
-    float mx;
-    auto maximum = [&](int j, bool ok) {
+    float fcs[4];
+    bool ok = pair_tiles(0, whole, true, [&](int j, bool ok) {
       ok = ok && wait_all(bars.sfull, j);
       tc_fence_after();
       const uint32_t sc = columns(j);
-      const int lim = pos - j * kPaRows - s * C;                     // columns 0..lim are seen
-      const bool masked = __any_sync(0xffffffffu, lim < C - 1);
       pa_ld32(sc, v[0]);
       pa_ld32(sc + 32, v[1]);
       pa_ld_wait32(v[0]);
       pa_ld_wait32(v[1]);
-      if (masked) {
+      const int lim = pos - j * kPaRows - s * C;                     // columns 0..lim are seen
+      if (!S::BF && __any_sync(0xffffffffu, lim < C - 1)) {
 #pragma unroll
         for (int k = 0; k < C; ++k) if (k > lim) v[k / 32][k % 32] = 0xff800000u;
       }
@@ -595,18 +653,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         auto at = [&](int k) { return __uint_as_float(v[(c + k) / 32][(c + k) % 32]); };
         const float x0 = pa_max3(pa_max3(at(0), at(1), at(2)), at(3), at(4)), x1 = pa_max3(pa_max3(at(5), at(6), at(7)), at(8), at(9));
         const float y = pa_max3(pa_max3(x0, x1, at(10)), pa_max3(at(11), at(12), at(13)), fmaxf(at(14), at(15)));
-        mx = fmaxf(mx, S::BF ? y * factor(sm_kbase[j & 3][(s * C + c) / 16]) : y);
+        if (S::BF) fcs[c / 16] = factor(sm_kbase[j & 3][(s * C + c) / 16]);
+        mx = fmaxf(mx, S::BF ? y * fcs[c / 16] : y);
       }
-      sm_mx[j & 1][s][r] = mx;
       return ok;
-    };
-    auto rest = [&](int j) {
+    }, meet, [&](int j) {
       const uint32_t sc = columns(j);
-      mx = fmaxf(mx, sm_mx[j & 1][s ^ 1][r]);
-      const float mn = fmaxf(m, S::BF ? mx - kPaUp : fmaf(mx, fac, -kPaUp)), mu = mn == -INFINITY ? 0.f : mn;
-      float al = pa_ex2(m - mu);
-      m = mn;
-      l *= al;
       if (S::BF) {                                                   // V's largest exponent so far
         if (!wait_all(bars.vfull, j)) return false;
         int top = vbase;
@@ -615,12 +667,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         al *= pa_ex2((float)(vbase - top));
         vbase = top;
       }
-      // P = 2^(score - maximum + 14), for BF16 times 2^(block's base - vbase)
+      const float mu = m == -INFINITY ? 0.f : m;
       uint64_t ls[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < C; c += 16) {
         const int blk = (s * C + c) / 16;
-        const float fc = S::BF ? factor(sm_kbase[j & 3][blk]) : fac;
+        const float fc = S::BF ? fcs[c / 16] : fac;
         const float off = S::BF ? (float)max(sm_vbase[j & 1][blk] - vbase, -80) : 0.f;   // below: nothing beside the largest
         uint64_t part[2] = {0, 0};
         uint32_t hi[8], lo[8];
@@ -643,18 +695,88 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         pa_st8(sc + c + 8, lo);
       }
       const float2 l2 = pa_unpair(pa_add2(ls[0], ls[1]));
-      l += l2.x + l2.y;
-      pa_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.pfull[j & 1]);
-      // the previous tile's P V, done meanwhile
-      const bool ok = !j || drain(j - 1, al_prev);
-      al_prev = al;
-      return ok;
-    };
-    auto meet = [&](int, bool ok) { return named_bar_and(2 + (warp & 3), 64, ok); };   // the rows' two warps
-    if (pair_tiles(0, ntiles, true, maximum, meet, rest)) drain(ntiles - 1, al_prev);
+      return next(j, l2.x + l2.y);
+    });
+    // BF16: the tiles with tokens that some row does not see, an exponent per
+    // token. 16 columns at a time, read twice, for the sake of registers: one loop
+    // that held 64 with both kinds of exponents spilled in the whole tiles, too
+    // (1000 tokens after 8200: 812 us against 614)
+    if constexpr (S::BF) {
+      auto tokens = [](const int* from, int (&to)[16]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int4 x = reinterpret_cast<const int4*>(from)[i];
+          to[4 * i] = x.x; to[4 * i + 1] = x.y; to[4 * i + 2] = x.z; to[4 * i + 3] = x.w;
+        }
+      };
+      auto limit = [&](int j) { return pos - j * kPaRows - s * C; };  // columns 0..limit are seen
+      auto most_of = [&](int j) { return min(last - j * kPaRows - s * C + 1, C); };   // those that some row sees
+      ok = pair_tiles(whole, ntiles, ok, [&](int j, bool ok) {
+        ok = ok && wait_all(bars.sfull, j);
+        tc_fence_after();
+        const uint32_t sc = columns(j);
+        const int lim = limit(j), most = most_of(j), *ktok = sm_ktok[j & 3] + s * C;
+        mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < most; c += 16) {
+          uint32_t x[16];
+          int kt[16];
+          tmem_ld16_async(sc + c, x);
+          tokens(ktok + c, kt);
+          tmem_ld_wait16(x);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float y = __uint_as_float(x[k]) * factor(kt[k]);
+            mx = fmaxf(mx, c + k <= lim ? y : -INFINITY);
+          }
+        }
+        return ok;
+      }, meet, [&](int j) {
+        if (!wait_all(bars.vfull, j)) return false;
+        const uint32_t sc = columns(j);
+        const int lim = limit(j), most = most_of(j), *ktok = sm_ktok[j & 3] + s * C, *vtok = sm_vtok[j & 1];
+        int top = vbase;
+        const int seen = min(pos - j * kPaRows, kPaRows - 1);        // the row's last token in this tile
+#pragma unroll
+        for (int c = 0; c < kPaRows; c += kBlockTokens)
+          if (c <= seen) top = max(top, vtok[min(c + kBlockTokens - 1, seen)]);
+        al *= pa_ex2((float)(vbase - top));
+        vbase = top;
+        const float mu = m == -INFINITY ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < C; c += 16) {
+          uint32_t hi[8] = {}, lo[8] = {};
+          if (c < most) {
+            uint32_t x[16];
+            int kt[16], vt[16];
+            tmem_ld16_async(sc + c, x);
+            tokens(ktok + c, kt);
+            tokens(vtok + s * C + c, vt);
+            tmem_ld_wait16(x);
+            float part = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float p[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float y = pa_ex2(fmaf(__uint_as_float(x[k + e]), factor(kt[k + e]), -mu));
+                p[e] = c + k + e <= lim ? y : 0.f;
+              }
+              part += p[0] + p[1];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) p[e] *= __int_as_float(max(127 + min(vt[k + e] - vbase, 0), 0) << 23);
+              pa_split(p[0], p[1], hi[k / 2], lo[k / 2]);
+            }
+            sum += part;
+          }
+          pa_st8(sc + c, hi);
+          pa_st8(sc + c + 8, lo);
+        }
+        return next(j, sum);
+      });
+    }
+    if (ok) drain(ntiles - 1, al_prev);
 
     // all products and copies are done: rows through the drained tiles, stored whole
     sm_mx[0][s][r] = l;
@@ -663,7 +785,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     // BF16: o / L, the exponent and the scale one after the other (the product of
     // the last two with 1 / L can be too small for fp32 where the output is not)
     const bool finite = max(sm_big[0][r], sm_big[1][r]) < 0x7f800000u;   // the query; NaN where it is not
-    const float wgt = pos < 0 ? 0.f : !finite ? __int_as_float(0x7fc00000) : S::BF ? 1.f / L : a.v_scale / L, unit = exponent(max(vbase, 0));
+    const float wgt = pos < 0 ? 0.f : !finite ? __int_as_float(0x7fc00000) : S::BF ? 1.f / L : a.v_scale / L;
+    const float unit = pa_exponent(max(vbase, 0));
     auto result = [&](float x) { return S::BF ? x * wgt * unit * a.v_scale : x * wgt; };
     float* stage = reinterpret_cast<float*>(smem) + r * S::LDO + s * E;
 #pragma unroll
@@ -722,40 +845,84 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
 #pragma unroll
     for (int i = 0; i < 2 * S::STAGES; ++i) request(i / 2, i & 1);
     const bool go = is_k || __all_sync(0xffffffffu, pa_wait(&bars.qfull, 0, &sm_stop));   // the queries sit in V's place
+    auto raw_block = [&](int j, int half) {                          // in its place of the ring, once it has arrived
+      asm volatile("cp.async.wait_group %0;" ::"n"(2 * S::STAGES - 1) : "memory");
+      __syncwarp();
+      return ring + ((j % S::STAGES) * 2 + half) * S::UNIT;
+    };
+    auto wait_empty = [&](int j) {
+      return j < 2 || __all_sync(0xffffffffu, pa_wait(&empty[j & 1], (j / 2 - 1) & 1, &sm_stop));
+    };
+    auto arrive_full = [&](int j) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[j & 1]);
+    };
+    auto note_bad = [&](bool bad, int tok0) {
+      if (bad) { atomicMin(&sm_bad_first, tok0 / kBlockTokens); atomicMax(&sm_bad_last, tok0 / kBlockTokens); }
+    };
 #pragma unroll 1
-    for (int j = 0; go && j < ntiles; ++j) {
-      const int buf = j & 1, i = j >> 1;
-      if (i > 0 && !__all_sync(0xffffffffu, pa_wait(&empty[buf], (i - 1) & 1, &sm_stop))) break;
-      unsigned char* tile = (is_k ? kbuf : vbuf) + buf * S::TILE;
+    for (int j = 0; go && j < whole; ++j) {
+      if (!wait_empty(j)) break;
+      unsigned char* tile = (is_k ? kbuf : vbuf) + (j & 1) * S::TILE;
 #pragma unroll (S::BF ? 1 : 2)
       for (int half = 0; half < 2; ++half) {
         const int at = half * 4 + lw, tok0 = j * kPaRows + at * kBlockTokens;
-        const bool guard = !is_k && tok0 + kBlockTokens - 1 > t.pos0;
+        const bool guard = !S::BF && !is_k && tok0 + kBlockTokens - 1 > t.pos0;
         PaRaw<D, KV> raw;
-        asm volatile("cp.async.wait_group %0;" ::"n"(2 * S::STAGES - 1) : "memory");
-        __syncwarp();
-        raw.read(ring + ((j % S::STAGES) * 2 + half) * S::UNIT, lane);
+        raw.read(raw_block(j, half), lane);
         __syncwarp();                                                // every lane has read: the place is free
         request(j + S::STAGES, half);
-        const int keep = t.ctx - tok0;
+        const int keep = S::BF ? kBlockTokens : t.ctx - tok0;
         bool high = false;
-        int base = 0;
-        if constexpr (S::BF) {                                       // nothing past the context sets the exponent
-          base = pa_block_base<D>(raw, keep, lane, high);
-          if (lane == 0) (is_k ? sm_kbase[j & 3] : sm_vbase[buf])[at] = base;
-        }
-        if (guard || high || keep < kBlockTokens) {
-          if (pa_store<D, KV, true>(raw, tile, at * kBlockTokens, keep, guard || (high && !is_k), lane, base)) {
-            atomicMin(&sm_bad_first, tok0 / kBlockTokens);
-            atomicMax(&sm_bad_last, tok0 / kBlockTokens);
+        int base = 0, *tok = nullptr;
+        if constexpr (S::BF) {
+          base = pa_block_base<D>(raw, high);
+          if (lane == 0) (is_k ? sm_kbase[j & 3] : sm_vbase[j & 1])[at] = base;
+          if (high) {
+            tok = (is_k ? sm_ktok[j & 3] : sm_vtok[j & 1]) + at * kBlockTokens;
+            if (lane < kBlockTokens) tok[lane] = base;
+            __syncwarp();
           }
-        } else {
-          pa_store<D, KV, false>(raw, tile, at * kBlockTokens, kBlockTokens, false, lane, base);
         }
+        if (guard || high || keep < kBlockTokens)
+          note_bad(pa_store<D, KV, PA_ANY>(raw, tile, at * kBlockTokens, keep, guard || (high && !is_k), lane, base, tok), tok0);
+        else
+          pa_store<D, KV, PA_WHOLE>(raw, tile, at * kBlockTokens, kBlockTokens, false, lane, base, tok);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[buf]);
+      arrive_full(j);
+    }
+    if constexpr (S::BF) {
+#pragma unroll 1
+      for (int j = whole; go && j < ntiles; ++j) {
+        if (!wait_empty(j)) break;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int at = half * 4 + lw, tok0 = j * kPaRows + at * kBlockTokens;
+          int* tok = (is_k ? sm_ktok[j & 3] : sm_vtok[j & 1]) + at * kBlockTokens;
+          unsigned char* tile = (is_k ? kbuf : vbuf) + (j & 1) * S::TILE;
+          const int keep = last + 1 - tok0;                          // tokens that some row of the tile sees
+          const unsigned char* place = raw_block(j, half);
+          if (keep <= 0) {
+            request(j + S::STAGES, half);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {                       // 16 rows of D / 64 panels, in any order
+              const int id = i * 32 + lane;
+              *reinterpret_cast<uint4*>(tile + id / 128 * S::PANEL + at * (kBlockTokens * 128) + id % 128 * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            continue;
+          }
+          bool high;
+          PaRaw<D, KV> raw;
+          pa_token_bases<D>(place, keep, lane, tok, high);
+          raw.read(place, lane);
+          __syncwarp();
+          request(j + S::STAGES, half);
+          if (high) note_bad(pa_store<D, KV, PA_ANY>(raw, tile, at * kBlockTokens, keep, !is_k, lane, 0, tok), tok0);
+          else pa_store<D, KV, PA_TOKENS>(raw, tile, at * kBlockTokens, keep, false, lane, 0, tok);
+        }
+        arrive_full(j);
+      }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {

@@ -154,3 +154,32 @@ def test_large_finite_values_beside_a_nan(cuda_lib):
     assert err == 0 and np.isnan(got[20:, :, 9]).all()
     assert np.abs(got - ref)[30:, :, 3].max() <= 2e-5 * 3.39e38
     assert np.abs(got - ref)[:20].max() <= 2e-5 * c.vmax
+
+
+# --- later tokens of a finite, much larger value ----------------------------
+
+@pytest.mark.parametrize("nq,nkv,d", [(4, 2, 64), (2, 2, 128), (16, 1, 128)])
+@pytest.mark.parametrize("up", [10, 14, 18, 26, 30, 60, 120])
+@pytest.mark.parametrize("what", ["k", "v", "kv"])
+def test_later_finite_values_never_reach_a_row(cuda_lib, nq, nkv, d, up, what):
+    """2^up in one token of a BF16 cache: the rows before it are as they would be without it, whether it lies in the same
+    block, in the same tile of 128 or in the next one; rows from it on see it."""
+    for tok in (101, 110, 127, 128, 150, 229):
+        c = Prompt("bf16", nq, nkv, d, [130], [100], seed=83, kg=1.0, vg=1.0)
+        for name, pool in (("k", c.kp), ("v", c.vp)):
+            if name in what:
+                pool[c.bt[0, tok // 16], :, tok % 16] = round_bf16(np.float64(2.0 ** up))
+        check_rows(c, np.arange(c.n) + 100 < tok if "k" in what else None)
+
+
+def test_values_grow_and_shrink_along_the_context(cuda_lib):
+    """V and K of every token on a scale of its own, tokens of zeros among them, from the first on."""
+    rng = np.random.default_rng(84)
+    for lens, prefix in (([200], [0]), ([60, 33, 1], [0, 100, 17])):
+        c = Prompt("bf16", 4, 2, 64, lens, prefix, seed=85, kg=1.0, vg=1.0)
+        for pool, spread in ((c.kp, 6), (c.vp, 40)):
+            f = 2.0 ** rng.integers(-spread, spread if spread > 6 else 1, pool.shape[:1] + (1, 16, 1))
+            f[rng.random(f.shape) < 0.2] = 0.0
+            f[c.bt[:, 0], :, 0] = 0.0
+            pool[...] = round_bf16(bf16_decode(pool) * f)
+        check_rows(c)
