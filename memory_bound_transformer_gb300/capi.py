@@ -393,6 +393,8 @@ def _device(fn: str, name: str, t) -> int:
 def _shape(fn: str, name: str, t, dims: int):
     if not isinstance(t, torch.Tensor) or t.dim() != dims:
         raise ValueError(f"{fn}: {name} must be a tensor of {dims} dimensions")
+    if max(t.shape) > 0x7fffffff:                          # ctypes would pass what is left of it in 32 bits
+        raise ValueError(f"{fn}: {name} has a dimension beyond 2^31 - 1")
     return t.shape
 
 
@@ -402,7 +404,10 @@ _UNIT = {(d, k): b for d in (64, 128) for k, b in ((DTYPE_BF16, 32 * d), (DTYPE_
 
 def _pools(fn: str, k, v, dev: int, nkv: int, d: int, num_blocks: int, kv_dtype: int):
     """Addresses of two pools of at least num_blocks + 1 blocks in the cache format (any shape and element type)."""
-    need = (num_blocks + 1) * nkv * _UNIT.get((d, kv_dtype), 0)
+    unit = _UNIT.get((d, kv_dtype))
+    if unit is None or nkv < 1 or num_blocks < 1:          # here, before ctypes takes 32 bits of them
+        raise MbtError(fn, -1)
+    need = (num_blocks + 1) * nkv * unit
     for name, t in (("kpool", k), ("vpool", v)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be a contiguous device tensor")
@@ -453,6 +458,8 @@ def op_rope_kv_write_fp4(qkv, nq, nkv, d, positions, bt, rope, kpool, vpool, num
     if qkv.dtype is not torch.float32 or cols < (nq + 2 * nkv) * d or qkv.stride(1) != 1:
         raise ValueError(f"{fn}: qkv must be fp32 with (nq + 2 nkv) d neighbouring columns")
     ld = max(qkv.stride(0), cols) if n < 2 else qkv.stride(0)
+    if ld > 0x7fffffff:
+        raise ValueError(f"{fn}: qkv's rows are more than 2^31 - 1 values apart")
     nseq, width = _shape(fn, "bt", bt, 2)
     max_pos = _shape(fn, "rope", rope, 3)[0]
     pk, pv = _pools(fn, kpool, vpool, dev, nkv, d, num_blocks, DTYPE_E2M1)
