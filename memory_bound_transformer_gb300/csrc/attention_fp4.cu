@@ -34,11 +34,12 @@
 // cycles a step (2130 without the loads), with two warps as with three or four:
 // 4.5 TB/s over long contexts. Taking one part out saves what it issues: half the
 // MMAs 470, the softmax 250, K's or V's multiplies 130, the nibble interleave
-// 120, the scales 105.
+// 120, the scales 105. (With four heads per KV head half of the MMAs' rows are
+// zeros, with more than eight the stream is read and converted once per eight.)
 // Around the loop a launch has ~5 us: the lengths, ids and queries (one round
 // trip), the first step's blocks, one step, the merges. 64 rows of 64 + 2 x 8
 // heads of 128 over 2048 tokens: 51 us (3.0 TB/s: 512 CTAs are 1.7 waves of two
-// an SM); one row of 32 + 2 x 8 heads over 2048: 5.7 us.
+// an SM); one row of 32 + 2 x 8 heads over 2048: 5.6 us (both in a graph).
 #include <algorithm>
 #include <climits>
 
@@ -368,8 +369,8 @@ __device__ __forceinline__ int row_of_rank(const AttnFp4Args& a, int rank) {
 // warps take the row's steps in turn; the CTAs' parts merge through distributed
 // shared memory. One launch, no scratch. (One wave of clusters of four that share
 // all pairs' steps evenly balances better, but finding the shares from the
-// lengths costs 4 us: 37 / 54 / 94 us against 38 / 49 / 45 for 64 rows of 256 to
-// 2048 tokens, 64 of 2048 and 4 of 32k.)
+// lengths costs 4 us: 37 / 54 / 94 us against 33 / 51 / 45, longest rows first, for
+// 64 rows of 256 to 2048 tokens, 64 of 2048 and 4 of 32k.)
 template <int D>
 __global__ void __launch_bounds__(kF4Threads, kF4PerSm) attention_fp4_kernel(const AttnFp4Args a) {
   using S = Fp4Shape<D>;

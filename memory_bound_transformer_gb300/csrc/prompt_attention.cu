@@ -40,18 +40,21 @@
 // each: for 16 keys 8 columns of high and 8 of low parts), P V (128), queries
 // (D / 2 high, D / 2 low).
 //
-// What bounds it: a key tile costs an SM 2830 cycles in a long loop, the MMAs
-// 2048 of them; the softmax warps' chain is the longer one (maximum 620 to 750,
-// exponentials and split 1250, adding P V 500, waiting 200). A CTA's start (its
-// place, its queries, the first scores) and its end cost 12,000 cycles and the
-// launch of the next 2,000; at one CTA an SM nothing overlaps them, which is a
-// third of the time at eight key tiles a CTA. 1000 tokens after 8200, 64 + 2 x 8
-// heads of 128, 4-bit: 391 us, 730 TFLOP/s of the formula's operations; 2048
-// tokens, 32 + 2 x 8 heads: 71 us, 485; 4096, 64 + 2 x 8, e4m3: 426 us, 640. BF16
-// tiles take two thirds more work to load: 582 us for those 4096.
+// What bounds it: a key tile costs an SM 2550 cycles with a 4-bit cache, 2700
+// with e4m3, 4100 with BF16 (widening takes that much more), the MMAs 2048 of
+// them; the softmax warps' chain is the longer one (maximum 620 to 750,
+// exponentials and split 1250, adding P V 500). A CTA's start (its place, its
+// queries, the first scores) and its end cost 13,000 cycles and the launch of the
+// next 2,000; at one CTA an SM nothing overlaps them, which is a third of the
+// time at eight key tiles a CTA. 1000 tokens after 8200, 64 + 2 x 8 heads of 128,
+// 4-bit: 389 us, 730 TFLOP/s of the formula's operations; 2048 tokens, 32 + 2 x 8
+// heads: 73 us, 475; 4096, 64 + 2 x 8, e4m3: 424 us, 650; the same over BF16: 600.
+// The keys of a tile of queries are not split: few tokens over a long context run
+// on as many SMs as they have tiles (33 after 8200, 32 + 2 x 8 heads: 16 CTAs).
 // CTAs that stay for all their query tiles were slower in each form tried (the
-// next queries loaded by the softmax warps 443 us, by the V loaders 418, for the
-// first of these): the state they carry takes the loop's registers.
+// next queries loaded by the softmax warps 443 us, by the V loaders 418, against
+// 391 for the first of these at the time): the state they carry takes the loop's
+// registers.
 //
 // A value of V that is not finite at a token some rows of the tile do not attend
 // to would reach them as 0 x inf, and an infinity those that do as inf + 0 x inf
@@ -137,11 +140,6 @@ __device__ __forceinline__ float2 pa_unpair(uint64_t p) {
 __device__ __forceinline__ uint64_t pa_fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t pa_mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t pa_add2(uint64_t a, uint64_t b) {
@@ -414,7 +412,7 @@ __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char*
           if (MODE == PA_ANY) v[e] = (v[e] & ~(bad & 0x7fff7fffu)) | (bad & 0x7c007c00u) | (__vcmpgtu2(x, 0x7f807f80u) & 0x02000200u);
         }
       }
-      if (MODE != PA_WHOLE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;       // whatever the raw block's place held
+      if (MODE != PA_WHOLE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;   // whatever the raw block's place held
       if (MODE == PA_ANY && guard) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
