@@ -305,10 +305,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* smem, i
   }
 
   // queries of the group, pre-scaled into the log2 domain with the K dequant scale
-  // (e4m3 caches: Q is split in FP16, so the K scale is applied to the fp32
-  // scores instead, keeping Q's range independent of it)
-  const float qscale = 1.4426950408889634f / sqrtf((float)D) * (KV8 ? 1.f : a.k_scale);
-  const float sscale = KV8 ? a.k_scale : 1.f;
+  // (e4m3 caches: Q is split in FP16, so the K scale's magnitude is applied to
+  // the fp32 scores instead, keeping Q's range independent of it; not 0, so that
+  // masked scores stay -inf)
+  const float qscale = 1.4426950408889634f / sqrtf((float)D) * (KV8 ? copysignf(1.f, a.k_scale) : a.k_scale);
+  const float sscale = KV8 ? fmaxf(fabsf(a.k_scale), 1.2e-38f) : 1.f;
   if (a.qkv) {
     // RoPE (rotate-half: element i pairs with i + D/2) straight from the QKV
     // projection's partial sums
@@ -357,11 +358,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* smem, i
       }
 
   // softmax state of this thread's two heads per n-tile (nt*8 + 2*t4, +1),
-  // the same in every lane of a column group. The running maximum is kept less
-  // `up`: FP16 probabilities go up to 2^14, so that their smallest steps lie at
+  // the same in every lane of a column group. e4m3: the running maximum is kept
+  // less `up`: FP16 probabilities go up to 2^14, so that their smallest steps lie at
   // 2^-39 of the largest and not at 2^-25, where thousands of small ones lose
   // what the sum still counts; the factor cancels in o / l
-  constexpr float up = KV8 ? 14.f : 0.f;
+  constexpr float up = 14.f;
   float mst[NT][2], lst[NT][2];
   float o[NT][S::MT][4];                                              // O^T: 16 d x 8 heads per m-tile
 #pragma unroll
@@ -462,7 +463,6 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* smem, i
       const bool v0 = n0 + g < nvalid, v1 = n0 + g + 8 < nvalid;     // tokens of c0/c1 and c2/c3
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (KV8) { st[nt][0] *= sscale; st[nt][1] *= sscale; st[nt][2] *= sscale; st[nt][3] *= sscale; }
         if (!v0) { st[nt][0] = -INFINITY; st[nt][1] = -INFINITY; }
         if (!v1) { st[nt][2] = -INFINITY; st[nt][3] = -INFINITY; }
         // online softmax per head: the 16 tokens of a column sit in the 8 lanes of one t4
@@ -474,10 +474,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* smem, i
         float al[2], ps[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float mn = fmaxf(mst[nt][c], mx[c] - up);
+          const float mn = fmaxf(mst[nt][c], KV8 ? fmaf(mx[c], sscale, -up) : mx[c]);
           const float mu = mn == -INFINITY ? 0.f : mn;
           al[c] = exp2f(mst[nt][c] - mu);
-          const float pa = exp2f(st[nt][c] - mu), pb = exp2f(st[nt][c + 2] - mu);
+          const float pa = exp2f(KV8 ? fmaf(st[nt][c], sscale, -mu) : st[nt][c] - mu);
+          const float pb = exp2f(KV8 ? fmaf(st[nt][c + 2], sscale, -mu) : st[nt][c + 2] - mu);
           st[nt][c] = pa;
           st[nt][c + 2] = pb;
           ps[c] = pa + pb;

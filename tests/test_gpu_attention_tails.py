@@ -15,7 +15,7 @@ import pytest
 import torch
 
 from memory_bound_transformer_gb300 import capi
-from oracle.kv_fp4 import encode, pack_pool, pool_values
+from oracle.kv_fp4 import encode, pack_pool, pool_values, rows_attention
 from oracle.numerics import round_bf16, round_e4m3
 from tests.test_gpu_kv_fp4 import dev, tables
 from tests.test_gpu_prompt_attention import KINDS, to_gpu
@@ -89,3 +89,20 @@ def test_single_token_bf16_and_e4m3(cuda_lib, kind, rows, nq, nkv, d, n, nats):
     capi.op_paged_attention(dev(q, torch.float32), nkv, k, v, KINDS[kind], 1.0, 1.0, dev(bt), dev(lens), nb, out)
     for got, size in zip(out.double().cpu().numpy(), lens):
         assert np.abs(got - one * share(size - 1, nats)).max() <= 2e-5 * one
+
+
+@pytest.mark.parametrize("k_scale", [-0.75, 0.0, 2.0 ** -130, 1.5])
+def test_single_token_e4m3_takes_any_k_scale(cuda_lib, k_scale):
+    """A scale of either sign, 0 and one below fp32's normal range."""
+    nq, nkv, d, lens = 8, 2, 64, [37, 1, 300, 64]
+    bt, nb = tables(lens, 5)
+    bt[bt < 0] = nb
+    rng = np.random.default_rng(6)
+    k, v = (round_e4m3(rng.standard_normal((nb + 1, nkv, 16, d))) for _ in range(2))
+    q = (rng.standard_normal((len(lens), nq, d)) * 0.6).astype(np.float32)
+    out = torch.zeros((len(lens), nq * d), device=DEV)
+    capi.op_paged_attention(dev(q, torch.float32), nkv, to_gpu(k), to_gpu(v), capi.DTYPE_E4M3, k_scale, 1.25, dev(bt), dev(lens),
+                            nb, out)
+    vals = pool_values(v, "fp8", d, 1.25)
+    ref = rows_attention(q, pool_values(k, "fp8", d, k_scale), vals, bt, np.arange(len(lens)), np.array(lens) - 1)
+    assert np.abs(out.double().cpu().numpy() - ref).max() <= 2e-5 * np.abs(vals).max()
