@@ -59,8 +59,11 @@
 // A value of V that is not finite at a token some rows of the tile do not attend
 // to would reach them as 0 x inf, and an infinity those that do as inf + 0 x inf
 // (a probability's low part): the loader stores 0 for it and notes its block, and
-// the rows that attend to it add it at the end. (NaN, all that e4m3 and 4-bit
-// caches have, is left where every row of the tile attends to it.)
+// the rows that attend to it add it at the end. Of the tiles that every row sees
+// whole they are added up once for all rows (the order of infinities and NaN does
+// not matter); NaN, all that e4m3 and 4-bit caches have, can stay where it is
+// there. BF16 keys that are not finite become zeros, too, and the rows that attend
+// to them NaN.
 #include <algorithm>
 #include <climits>
 
@@ -310,33 +313,29 @@ __device__ __forceinline__ uint32_t pa_max2(uint32_t a, uint32_t b) {   // of tw
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Largest magnitude among a block's BF16 bit patterns (`finite`: among those of
-// finite values).
+// Exponent base of a BF16 block: FP16 exponent field = BF16 field - base, the
+// largest value's at 30. `high` (uniform): some value is not finite, and the base
+// is not to be used.
 template <int D>
-__device__ __forceinline__ uint32_t pa_block_max(const PaRaw<D, KV_BF16>& raw, bool finite) {
+__device__ __forceinline__ int pa_block_base(const PaRaw<D, KV_BF16>& raw, bool& high) {
   uint32_t m[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int q = 0; q < PaShape<D, KV_BF16>::NCH; ++q) {
-    uint32_t x[4] = {raw.c[q].x & 0x7fff7fffu, raw.c[q].y & 0x7fff7fffu, raw.c[q].z & 0x7fff7fffu, raw.c[q].w & 0x7fff7fffu};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = pa_max2(m[e], finite ? x[e] & ~__vcmpgeu2(x[e], 0x7f807f80u) : x[e]);
+    m[0] = pa_max2(m[0], raw.c[q].x & 0x7fff7fffu);
+    m[1] = pa_max2(m[1], raw.c[q].y & 0x7fff7fffu);
+    m[2] = pa_max2(m[2], raw.c[q].z & 0x7fff7fffu);
+    m[3] = pa_max2(m[3], raw.c[q].w & 0x7fff7fffu);
   }
   const uint32_t x = pa_max2(pa_max2(m[0], m[1]), pa_max2(m[2], m[3]));
-  return __reduce_max_sync(0xffffffffu, max(x >> 16, x & 0xffffu));
-}
-// Exponent base of a BF16 block: FP16 exponent field = BF16 field - base, the
-// largest finite value's at 30. `high` (uniform): some value is not finite.
-template <int D>
-__device__ __forceinline__ int pa_block_base(const PaRaw<D, KV_BF16>& raw, bool& high) {
-  uint32_t m = pa_block_max<D>(raw, false);
-  high = m >= 0x7f80u;
-  if (high) m = pa_block_max<D>(raw, true);                          // rare
-  return max(0, (int)(m >> 7) - 30);
+  const uint32_t top = __reduce_max_sync(0xffffffffu, max(x >> 16, x & 0xffffu));
+  high = top >= 0x7f80u;
+  return max(0, (int)(top >> 7) - 30);
 }
 // The same per token of a raw block's first `keep`, each over the tokens up to it.
-// Two lanes per token, half of its channels each.
+// Two lanes per token, half of its channels each. Returns the first token with a
+// value that is not finite, 16 where there is none.
 template <int D>
-__device__ __forceinline__ void pa_token_bases(const unsigned char* u, int keep, int lane, int* out, bool& high) {
+__device__ __forceinline__ int pa_token_bases(const unsigned char* u, int keep, int lane, int* out) {
   constexpr int N = D / 16;                                          // 16-byte chunks per lane
   const int token = lane >> 1, half = lane & 1;
   const unsigned char* row = u + token * (2 * D) + half * N * 16;
@@ -352,7 +351,7 @@ __device__ __forceinline__ void pa_token_bases(const unsigned char* u, int keep,
     return token < keep ? max(x >> 16, x & 0xffffu) : 0u;
   };
   uint32_t m = largest(false);
-  high = __any_sync(0xffffffffu, m >= 0x7f80u);
+  const uint32_t high = __ballot_sync(0xffffffffu, m >= 0x7f80u);
   if (high) m = largest(true);                                       // rare
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
 #pragma unroll
@@ -361,16 +360,24 @@ __device__ __forceinline__ void pa_token_bases(const unsigned char* u, int keep,
     if (lane >= o) m = max(m, t);
   }
   if (!half) out[token] = max(0, (int)(m >> 7) - 30);
+  return high ? (__ffs(high) - 1) >> 1 : kBlockTokens;
+}
+
+// Values of a BF16 block that are not finite become zeros (rare).
+template <int D>
+__device__ __forceinline__ void pa_clear(PaRaw<D, KV_BF16>& raw) {
+  auto clear = [](uint32_t& w) { w &= ~__vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u); };
+#pragma unroll
+  for (int q = 0; q < PaShape<D, KV_BF16>::NCH; ++q) { clear(raw.c[q].x); clear(raw.c[q].y); clear(raw.c[q].z); clear(raw.c[q].w); }
 }
 
 // Raw chunks to FP16 values in the tile (rows R0 .. R0 + 15). Tokens from `keep`
 // on are stored as zeros; where `guard`, values that are not finite are too, and
 // the return value says whether there were any. BF16: `base` is the block's
-// exponent base, `tok` its tokens'.
+// exponent base, `tok` its tokens'; all values are finite (pa_clear).
 // MODE: PA_WHOLE converts a block with no branch inside, which would keep the
-// loop's chains from interleaving; PA_ANY takes `keep`, `guard`, values that are
-// not finite and (BF16) `tok`; PA_TOKENS (BF16) `keep` and `tok` alone.
-enum { PA_WHOLE, PA_TOKENS, PA_ANY };
+// loop's chains from interleaving; PA_KEEP takes `keep`, `guard` and `tok`.
+enum { PA_WHOLE, PA_KEEP };
 template <int D, int KV, int MODE>
 __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char* tile, int R0, int keep, bool guard, int lane, int base, const int* tok) {
   using S = PaShape<D, KV>;
@@ -403,17 +410,13 @@ __device__ __forceinline__ bool pa_store(const PaRaw<D, KV>& raw, unsigned char*
         v[0] = e4m3x2_to_h2bits(w[2 * k]); v[1] = e4m3x2_to_h2bits(w[2 * k] >> 16);
         v[2] = e4m3x2_to_h2bits(w[(2 * k + 1) & 3]); v[3] = e4m3x2_to_h2bits(w[(2 * k + 1) & 3] >> 16);
       } else {
-        // (magnitude - (base << 7)) << 3 in both halves at once, sign kept; values
-        // that are not finite (zeros meanwhile, which stay in their half) to FP16's
+        // (magnitude - (base << 7)) << 3 in both halves at once, sign kept
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t x = w[e] & 0x7fff7fffu, bad = MODE == PA_ANY ? __vcmpgeu2(x, 0x7f807f80u) : 0u;
-          v[e] = (pa_max2(x & ~bad, low) * 8u + shift) | (w[e] & 0x80008000u);
-          if (MODE == PA_ANY) v[e] = (v[e] & ~(bad & 0x7fff7fffu)) | (bad & 0x7c007c00u) | (__vcmpgtu2(x, 0x7f807f80u) & 0x02000200u);
-        }
+        for (int e = 0; e < 4; ++e)
+          v[e] = (pa_max2(w[e] & 0x7fff7fffu, low) * 8u + shift) | (w[e] & 0x80008000u);
       }
       if (MODE != PA_WHOLE && row >= keep) v[0] = v[1] = v[2] = v[3] = 0u;   // whatever the raw block's place held
-      if (MODE == PA_ANY && guard) {
+      if (MODE != PA_WHOLE && !S::BF && guard) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t bad = __vcmpeq2(v[e] & 0x7c007c00u, 0x7c007c00u);
@@ -453,7 +456,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   __shared__ uint32_t tmem_slot, sm_big[2][kPaRows];
   __shared__ float sm_mx[2][2][kPaRows];                             // halves' maxima: even and odd tiles
   __shared__ PaTile sm_tile;
-  __shared__ int sm_ok, sm_bad_first, sm_bad_last;                   // cache blocks whose V was replaced by zeros
+  // first and last cache block with values of V replaced by zeros, of BF16's whole
+  // tiles and of the others; first token whose K was
+  __shared__ int sm_ok, sm_bad_whole[2], sm_bad_last_tiles[2], sm_bad_key;
+  __shared__ float sm_bad_sum[S::BF ? D : 1];
   // BF16 exponent bases of the tiles' blocks, and of their tokens; a K tile's outlive its buffer
   __shared__ int sm_kbase[4][8], sm_vbase[2][8];
   __shared__ __align__(16) int sm_ktok[S::BF ? 4 : 1][kPaRows], sm_vtok[S::BF ? 2 : 1][kPaRows];
@@ -468,9 +474,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       sm_ok = ok;
       if (ok) sm_tile = t;
       sm_stop = 0;
-      sm_bad_first = INT_MAX;
-      sm_bad_last = -1;
+      sm_bad_whole[0] = sm_bad_last_tiles[0] = sm_bad_key = INT_MAX;
+      sm_bad_whole[1] = sm_bad_last_tiles[1] = -1;
     }
+  } else if (warp == 2) {
+    if (S::BF)
+      for (int i = lane; i < D; i += 32) sm_bad_sum[i] = 0.f;
   } else if (warp == 1) {
     if (lane == 0) {
       for (int s = 0; s < 2; ++s) {
@@ -782,7 +791,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     const float L = l + sm_mx[0][s ^ 1][r];
     // BF16: o / L, the exponent and the scale one after the other (the product of
     // the last two with 1 / L can be too small for fp32 where the output is not)
-    const bool finite = max(sm_big[0][r], sm_big[1][r]) < 0x7f800000u;   // the query; NaN where it is not
+    // the query and (BF16) all keys; NaN where they are not
+    const bool finite = max(sm_big[0][r], sm_big[1][r]) < 0x7f800000u && pos < sm_bad_key;
     const float wgt = pos < 0 ? 0.f : !finite ? __int_as_float(0x7fc00000) : S::BF ? 1.f / L : a.v_scale / L;
     const float unit = pa_exponent(max(vbase, 0));
     auto result = [&](float x) { return S::BF ? x * wgt * unit * a.v_scale : x * wgt; };
@@ -792,11 +802,31 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       const float2 x = pa_unpair(o[i / 2]), y = pa_unpair(o[i / 2 + 1]);
       *reinterpret_cast<float4*>(stage + i) = make_float4(result(x.x), result(x.y), result(y.x), result(y.y));
     }
-    if (sm_bad_last >= 0) {                                          // rare
-      for (int tok = sm_bad_first * kBlockTokens; tok <= min(pos, sm_bad_last * kBlockTokens + kBlockTokens - 1); ++tok) {
-        int id = a.bt[(size_t)t.seq * a.bt_stride + tok / kBlockTokens];
-        if ((uint32_t)id > (uint32_t)a.num_blocks) id = a.num_blocks;
-        const unsigned char* u = reinterpret_cast<const unsigned char*>(a.vpool) + ((size_t)id * a.nkv + h) * S::UNIT;
+    auto unit_of = [&](int blk) {
+      int id = a.bt[(size_t)t.seq * a.bt_stride + blk];
+      if ((uint32_t)id > (uint32_t)a.num_blocks) id = a.num_blocks;
+      return reinterpret_cast<const unsigned char*>(a.vpool) + ((size_t)id * a.nkv + h) * S::UNIT;
+    };
+    if (S::BF && sm_bad_whole[1] >= 0) {                             // rare: the same for all rows, so all threads search
+      constexpr int N = S::UNIT / 16;                                // 16-byte chunks of a block
+#pragma unroll 1
+      for (long long i = tid; i < (sm_bad_whole[1] - sm_bad_whole[0] + 1LL) * N; i += 256) {
+        const int at = (int)(i % N) * 8;
+        const uint4 c = *reinterpret_cast<const uint4*>(unit_of(sm_bad_whole[0] + (int)(i / N)) + at * 2);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = __uint_as_float(w[e / 2] << (e & 1 ? 0 : 16) & 0xffff0000u);
+          if (!isfinite(x)) atomicAdd(&sm_bad_sum[(at + e) % D], x);
+        }
+      }
+      named_bar(1, 256);
+      for (int ch = 0; pos >= 0 && ch < E; ++ch) stage[ch] += sm_bad_sum[s * E + ch];
+    }
+    if (sm_bad_last_tiles[1] >= 0) {                                 // rare: at most two tiles
+      const int end = min(pos, sm_bad_last_tiles[1] * kBlockTokens + kBlockTokens - 1);
+      for (int tok = sm_bad_last_tiles[0] * kBlockTokens; tok <= end; ++tok) {
+        const unsigned char* u = unit_of(tok / kBlockTokens);
         for (int ch = 0; ch < E; ++ch) {
           const float x = pa_value<D, KV>(u, tok % kBlockTokens, s * E + ch);
           if (!isfinite(x)) stage[ch] += x;
@@ -856,8 +886,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[j & 1]);
     };
-    auto note_bad = [&](bool bad, int tok0) {
-      if (bad) { atomicMin(&sm_bad_first, tok0 / kBlockTokens); atomicMax(&sm_bad_last, tok0 / kBlockTokens); }
+    auto note_bad = [&](bool bad, int tok0, int (&range)[2]) {
+      if (bad) { atomicMin(&range[0], tok0 / kBlockTokens); atomicMax(&range[1], tok0 / kBlockTokens); }
     };
 #pragma unroll 1
     for (int j = 0; go && j < whole; ++j) {
@@ -872,21 +902,23 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         __syncwarp();                                                // every lane has read: the place is free
         request(j + S::STAGES, half);
         const int keep = S::BF ? kBlockTokens : t.ctx - tok0;
-        bool high = false;
-        int base = 0, *tok = nullptr;
+        int base = 0;
         if constexpr (S::BF) {
+          bool high;
           base = pa_block_base<D>(raw, high);
-          if (lane == 0) (is_k ? sm_kbase[j & 3] : sm_vbase[j & 1])[at] = base;
           if (high) {
-            tok = (is_k ? sm_ktok[j & 3] : sm_vtok[j & 1]) + at * kBlockTokens;
-            if (lane < kBlockTokens) tok[lane] = base;
-            __syncwarp();
+            pa_clear<D>(raw);
+            base = pa_block_base<D>(raw, high);
+            if (is_k) atomicMin(&sm_bad_key, tok0);
+            else note_bad(true, tok0, sm_bad_whole);
           }
+          if (lane == 0) (is_k ? sm_kbase[j & 3] : sm_vbase[j & 1])[at] = base;
         }
-        if (guard || high || keep < kBlockTokens)
-          note_bad(pa_store<D, KV, PA_ANY>(raw, tile, at * kBlockTokens, keep, guard || (high && !is_k), lane, base, tok), tok0);
-        else
-          pa_store<D, KV, PA_WHOLE>(raw, tile, at * kBlockTokens, kBlockTokens, false, lane, base, tok);
+        if (guard || keep < kBlockTokens) {
+          note_bad(pa_store<D, KV, PA_KEEP>(raw, tile, at * kBlockTokens, keep, guard, lane, base, nullptr), tok0, sm_bad_last_tiles);
+        } else {
+          pa_store<D, KV, PA_WHOLE>(raw, tile, at * kBlockTokens, kBlockTokens, false, lane, base, nullptr);
+        }
       }
       arrive_full(j);
     }
@@ -910,14 +942,17 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
             }
             continue;
           }
-          bool high;
           PaRaw<D, KV> raw;
-          pa_token_bases<D>(place, keep, lane, tok, high);
+          const int bad = pa_token_bases<D>(place, keep, lane, tok);
           raw.read(place, lane);
           __syncwarp();
           request(j + S::STAGES, half);
-          if (high) note_bad(pa_store<D, KV, PA_ANY>(raw, tile, at * kBlockTokens, keep, !is_k, lane, 0, tok), tok0);
-          else pa_store<D, KV, PA_TOKENS>(raw, tile, at * kBlockTokens, keep, false, lane, 0, tok);
+          if (bad < kBlockTokens) {
+            pa_clear<D>(raw);
+            if (is_k) atomicMin(&sm_bad_key, tok0 + bad);
+            else note_bad(true, tok0, sm_bad_last_tiles);
+          }
+          pa_store<D, KV, PA_KEEP>(raw, tile, at * kBlockTokens, keep, false, lane, 0, tok);
         }
         arrive_full(j);
       }

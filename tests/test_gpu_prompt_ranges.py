@@ -183,3 +183,49 @@ def test_values_grow_and_shrink_along_the_context(cuda_lib):
             f[c.bt[:, 0], :, 0] = 0.0
             pool[...] = round_bf16(bf16_decode(pool) * f)
         check_rows(c)
+
+
+# --- infinities far before the prompt ----------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinities_far_before_the_prompt(cuda_lib, d):
+    """In key tiles that every row sees whole, beside others in the last tiles: as such in their channels, NaN where both
+    signs meet, and nothing else changes."""
+    c = Prompt("bf16", 4, 2, d, [90, 30], [400, 0], seed=91, kg=1.0, vg=1.0)
+    want = c.ref().reshape(c.n, 4, d)
+    for tok, head, ch, bits in ((5, 0, 6, 0x7F80), (5, 0, 7, 0xFF80), (200, 1, 8, 0x7F80), (210, 1, 8, 0xFF80),
+                                (300, 0, 6, 0x7F80), (383, 1, d - 1, 0x7FC0), (430, 0, 7, 0x7F80), (430, 0, 9, 0x7F80)):
+        c.vp[c.bt[0, tok // 16], head, tok % 16, ch] = bits
+    got, err = c.run()
+    got = got.reshape(want.shape)
+    assert err == 0
+    assert np.all(got[:90, :2, 6] == np.inf)
+    assert np.all(got[:30, :2, 7] == -np.inf) and np.isnan(got[30:90, :2, 7]).all()
+    assert np.isnan(got[:90, 2:, 8]).all() and np.isnan(got[:90, 2:, d - 1]).all()
+    assert np.isfinite(got[:30, :2, 9]).all() and np.all(got[30:90, :2, 9] == np.inf)
+    ok = np.ones(got.shape, bool)
+    ok[:90, :2, [6, 7, 9]] = ok[:90, 2:, 8] = ok[:90, 2:, d - 1] = False
+    ok[:30, :2, 9] = True
+    assert np.abs(got - want)[ok].max() <= 2e-5 * c.vmax
+
+
+@pytest.mark.parametrize("tok", [7, 250, 399, 400, 431, 489])
+@pytest.mark.parametrize("bits", [0x7F80, 0xFF80, 0x7FC0])
+def test_keys_that_are_not_finite(cuda_lib, tok, bits):
+    """One channel of one token's K: the rows that attend to it are NaN in its KV head, the others as they were."""
+    for ch in (0, 63):
+        c = Prompt("bf16", 4, 2, 64, [90, 30], [400, 0], seed=92, kg=1.0, vg=1.0)
+        want = c.ref().reshape(c.n, 4, 64)
+        c.kp[c.bt[0, tok // 16], 1, tok % 16, ch] = bits
+        got, err = c.run()
+        got = got.reshape(want.shape)
+        bad = np.zeros(want.shape, bool)
+        bad[max(0, tok - 400):90, 2:] = True
+        assert err == 0 and np.isnan(got[bad]).all() and np.abs(got - want)[~bad].max() <= 2e-5 * c.vmax
+
+
+def test_a_cache_full_of_infinities(cuda_lib):
+    c = Prompt("bf16", 4, 2, 64, [40], [4000], seed=93)
+    c.vp[...] = 0x7F80
+    got, err = c.run()
+    assert err == 0 and np.all(got == np.inf)
