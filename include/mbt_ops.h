@@ -257,13 +257,13 @@ int op_paged_attention_fp4(int B, const float* q, int nq, int nkv, int d, const 
  * MBT_DEV_SEQLEN_RANGE and the sequence's rows are 0; an out-of-range block id
  * sets MBT_DEV_BLOCK_RANGE and reads the null block. Tokens after a row's own
  * never reach it, whatever they hold. A query that is not finite makes its row
- * NaN in that head, a NaN in K the rows that attend to it (an infinity in K
- * leaves them unspecified); an infinity or a NaN in V reaches them in its
- * channel. Queries and probabilities are exact to 2^-22, probabilities below
- * 2^-17 of the row's largest to 2^-39 of that. Values of a BF16 cache are exact
- * down to 2^-29 of the largest that the row attends to among their block's 16
- * tokens of a head, and 2^-30 of it off below; where V's blocks differ in size,
- * 2^-39 of the largest |V| that the row attends to is the smallest share that counts. */
+ * NaN in that head, a key that is not the rows that attend to it; an infinity
+ * or a NaN in V reaches them in its channel. Queries and probabilities are
+ * exact to 2^-22, probabilities below 2^-17 of the row's largest to 2^-39 of
+ * that. Values of a BF16 cache are exact down to 2^-29 of the largest that the
+ * row attends to among their block's 16 tokens of a head, and 2^-30 of it
+ * (2^-126 at least) off below; where V's blocks differ in size, 2^-39 of the
+ * largest |V| that the row attends to is the smallest share that counts. */
 int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq, const int32_t* cu_seqlens,
                         const int32_t* ctx_lens, const void* kpool, const void* vpool, int kv_dtype, float k_scale,
                         float v_scale, const int32_t* bt, int bt_stride, int num_blocks, float* out, uint32_t* err,

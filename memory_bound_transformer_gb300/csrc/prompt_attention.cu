@@ -41,14 +41,14 @@
 // (D / 2 high, D / 2 low).
 //
 // What bounds it: a key tile costs an SM 2550 cycles with a 4-bit cache, 2700
-// with e4m3, 4100 with BF16 (widening takes that much more), the MMAs 2048 of
+// with e4m3, 3900 with BF16 (widening takes that much more), the MMAs 2048 of
 // them; the softmax warps' chain is the longer one (maximum 620 to 750,
 // exponentials and split 1250, adding P V 500). A CTA's start (its place, its
 // queries, the first scores) and its end cost 13,000 cycles and the launch of the
 // next 2,000; at one CTA an SM nothing overlaps them, which is a third of the
 // time at eight key tiles a CTA. 1000 tokens after 8200, 64 + 2 x 8 heads of 128,
 // 4-bit: 389 us, 730 TFLOP/s of the formula's operations; 2048 tokens, 32 + 2 x 8
-// heads: 73 us, 475; 4096, 64 + 2 x 8, e4m3: 424 us, 650; the same over BF16: 600.
+// heads: 72 us, 475; 4096, 64 + 2 x 8, e4m3: 424 us, 650; the same over BF16: 562.
 // The keys of a tile of queries are not split: few tokens over a long context run
 // on as many SMs as they have tiles (33 after 8200, 32 + 2 x 8 heads: 16 CTAs).
 // CTAs that stay for all their query tiles were slower in each form tried (the
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     // BF16: the tiles with tokens that some row does not see, an exponent per
     // token. 16 columns at a time, read twice, for the sake of registers: one loop
     // that held 64 with both kinds of exponents spilled in the whole tiles, too
-    // (1000 tokens after 8200: 812 us against 614)
+    // (1000 tokens after 8200: 812 us against 570)
     if constexpr (S::BF) {
       auto tokens = [](const int* from, int (&to)[16]) {
 #pragma unroll
