@@ -301,6 +301,11 @@ def _values(raw, kv, d, dtype):
     return (lut[codes.int()].unflatten(-1, (-1, 16)) * scale.unsqueeze(-1)).flatten(-2)
 
 
+def _power(e):
+    """2^e in 64 bits, from its bits: torch.ldexp goes through a power that a GPU rounds."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _plain_bounds(s):
     """Every row works on its block as its last row in the block has it (rows of a block write the same)."""
     c = s["c"]
@@ -319,7 +324,7 @@ def _plain_bounds(s):
         bad = ~torch.where(live, k, zero).isfinite().all(-1).all(-1)
         frac, e = torch.frexp(torch.where(bad, zero, most))
         e = (e - torch.where(frac <= 127.0 / 128.0, 7, 6)).clamp(min=-100)
-        unit = torch.ldexp(torch.ones_like(e, dtype=torch.float64), e)[..., None]
+        unit = _power(e)[..., None]
         low = (torch.where(live, k, math.inf).amin(-2).double() / unit).floor()
         high = (torch.where(live, k, -math.inf).amax(-2).double() / unit).ceil()
         code = torch.where((bad | (most == 0))[..., None, None], 0.0, torch.stack((low, high), 2))
@@ -340,7 +345,7 @@ def _plain_select(s):
         most = q.abs().amax((-1, -2), keepdim=True)
         fine = most.isfinite() & (most > 0)
         x = torch.frexp(torch.where(fine, most, 1.0))[1]
-        u = torch.where(fine, torch.round(torch.ldexp(q, 10 - x)), 0.0)
+        u = torch.where(fine, torch.round(q * _power(10 - x)), 0.0)
         w = torch.cat((u.clamp(max=0).sum(2), u.clamp(min=0).sum(2)), -1)          # [rows, nkv, 2 d]: with low, with high
         ids = s["bt"][seq].long()
         ids = torch.where((ids < 0) | (ids > s["blocks"]), s["blocks"], ids)
