@@ -269,6 +269,103 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
                         float v_scale, const int32_t* bt, int bt_stride, int num_blocks, float* out, uint32_t* err,
                         void* stream);
 
+/* ---- attention over selected blocks of the paged cache -------------------- *
+ * Long contexts make a decode step read all of their K and V ("GPU Inference
+ * Internals", "The KV-Cache Ledger"). These entry points let every query read
+ * k blocks per KV head instead, chosen by a bound on its scores that costs 1/32
+ * of the BF16 cache's bytes, and lay out a step's rows on the GPU. In the order
+ * of a serving step: op_kv_extend (blocks and rows for the new tokens), the
+ * cache write (op_rope_kv_write, op_rope_kv_write_fp4), op_key_bounds (the
+ * ranges of the blocks written to), op_block_select, op_block_attention.
+ * All take cache formats, head sizes, groups, scales and table widths as the
+ * 4-bit section above says, and rows of any sequences: row i is at positions[i]
+ * of sequence row_seq[i] (NULL: sequence i, nseq >= n) of bt [nseq][bt_stride].
+ * A row whose position or sequence is outside the table sets MBT_DEV_POS_RANGE;
+ * an out-of-range block id sets MBT_DEV_BLOCK_RANGE. They keep nothing between
+ * calls and use no scratch memory. */
+
+/* op_kv_extend: block tables and row layout for a step's new tokens, from the
+ * sequences' lengths ("Kernels, Fusion & CUDA Graphs", "The serving engine's
+ * kernel stack": the paged cache behind block tables). Sequence s holds
+ * ctx_lens[s] tokens and gets new_lens[s] more: its table entries from
+ * ceil(ctx / 16) on are taken, sequences in order, from free_blocks[free_at[0]
+ * ..] of nfree ids; *free_next is where the next call goes on. Outputs:
+ *   held[nseq]          tokens afterwards
+ *   cu_seqlens[nseq+1]  first packed row of each sequence's new tokens
+ *   positions, row_seq, slots [n]: position, sequence and cache slot (block id *
+ *                       16 + position % 16) of each packed row. Rows from
+ *                       cu_seqlens[nseq] on are padding: sequence nseq,
+ *                       position 0, slot num_blocks * 16 (the null block; a table
+ *                       with one more row that names it makes the other entry
+ *                       points write and read there).
+ * held may be ctx_lens and free_next may be free_at (in place), so that a
+ * captured graph advances by replaying; the other arrays must be distinct. A
+ * sequence whose blocks or rows no longer fit (counting those of all before it)
+ * gets none and keeps its table: MBT_DEV_BLOCK_RANGE or MBT_DEV_POS_RANGE. One
+ * with a negative length or beyond its table gets none: MBT_DEV_SEQLEN_RANGE. A
+ * free_at[0] outside [0, nfree] sets MBT_DEV_BLOCK_RANGE and no blocks are
+ * taken. Ids outside [0, num_blocks] are entered as they are, set
+ * MBT_DEV_BLOCK_RANGE and make their rows' slots -1. free_blocks may be NULL if
+ * nfree is 0. */
+int op_kv_extend(int nseq, const int32_t* ctx_lens, const int32_t* new_lens, int32_t* bt, int bt_stride, int num_blocks,
+                 const int32_t* free_blocks, int nfree, const int32_t* free_at, int n, int32_t* held, int32_t* cu_seqlens,
+                 int32_t* positions, int32_t* row_seq, int64_t* slots, int32_t* free_next, uint32_t* err, void* stream);
+
+/* op_key_bounds: for each block that the rows are in, and each KV head, a range
+ * per channel that holds the keys of its tokens up to the row's own. With M the
+ * largest magnitude among them (in the cache's units: k_scale is a factor of
+ * all scores alike) and e the smallest exponent >= -100 with M <= 127 * 2^e,
+ *   bounds[block][head][0][i] = floor(min k_i / 2^e),
+ *   bounds[block][head][1][i] = ceil(max k_i / 2^e),   scales[block][head] = 2^e;
+ * scale 0 where M is 0, +infinity (and codes 0) where a key is not finite.
+ * bounds [num_blocks + 1][nkv][2][d] int8, scales [num_blocks + 1][nkv] fp32.
+ * A row leaves its block to the next row when that is in the same block of the
+ * same sequence; rows that are in one block otherwise must have the same
+ * position, or which of them counts is unspecified. A row with an error is left
+ * out; every other range stays as it was. */
+int op_key_bounds(int n, const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
+                  int nkv, int d, const void* kpool, int kv_dtype, int num_blocks, int8_t* bounds, float* scales,
+                  uint32_t* err, void* stream);
+
+/* Widest table (blocks per sequence) that op_block_select takes. */
+#define MBT_SELECT_MAX_BLOCKS (1 << 18)
+
+/* op_block_select: per row and KV head the k blocks of the row's context (tokens
+ * 0 .. positions[i]) that can hold the largest scores. Over the group's query
+ * heads q_g and with 2^x the smallest power of two above their largest
+ * magnitude,
+ *   u_gi = rint(q_gi * 2^(10 - x)),  P_i = sum_g max(u_gi, 0),  N_i = sum_g min(u_gi, 0),
+ *   score = fp32(sum_i P_i high_i + N_i low_i) * scale
+ * (all u are 0 where a query is not finite): above the sum of the group's scores
+ * with any key of the block, up to the rounding of u. The integer sum is exact,
+ * so the choice does not depend on an order of summation. A block whose scale is
+ * not finite scores +infinity. The first keep_first and the last keep_last
+ * blocks of the context are taken in any case (keep_last >= 1: a row sees itself;
+ * keep_first + keep_last <= k), then the largest scores; of equal ones the
+ * earlier block. sel [n][nkv][k] int32: the taken blocks' places in the table,
+ * ascending, then -1 where the context has fewer than k blocks. q [n][nq][d]
+ * fp32. An out-of-range id counts with the null block's range; a row outside
+ * its table gets -1 throughout. MBT_ERR_UNSUPPORTED for bt_stride above
+ * MBT_SELECT_MAX_BLOCKS. */
+int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t* bounds, const float* scales,
+                    const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
+                    int num_blocks, int keep_first, int keep_last, int k, int32_t* sel, uint32_t* err, void* stream);
+
+/* op_block_attention: softmax attention of n rows over selected blocks of the
+ * cache: out[i][h] = sum_t softmax_t(q[i][h] . K_t / sqrt(d)) V_t over the tokens
+ * t <= positions[i] of the blocks sel[i][KV head of h][0 .. k). Negative entries
+ * of sel are skipped; one beyond the row's context sets MBT_DEV_BLOCK_RANGE and
+ * is skipped. Entries may come in any order; a block entered twice counts twice.
+ * A row that is left with no token, or outside its table, is 0. q [n][nq][d]
+ * fp32, out [n][nq * d] fp32. An out-of-range id reads the null block. Cache
+ * contents past a row's position never reach it. A query that is not finite
+ * makes its row NaN in that head, a key that is not the rows that attend to it;
+ * an infinity or a NaN in V reaches them in its channel. */
+int op_block_attention(int n, const float* q, int nq, int nkv, int d, const void* kpool, const void* vpool, int kv_dtype,
+                       float k_scale, float v_scale, const int32_t* positions, const int32_t* row_seq, int nseq,
+                       const int32_t* bt, int bt_stride, const int32_t* sel, int k, int num_blocks, float* out,
+                       uint32_t* err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -65,6 +65,10 @@ SIGNATURES = {
     "op_kv_read_fp4": (_I, [_I, _P, _P, _I, _P, _I, _I, _I, _P, _P, _I, _F, _F, _P, _P, _P, _P]),
     "op_paged_attention_fp4": (_I, [_I, _P, _I, _I, _I, _P, _P, _F, _F, _P, _I, _P, _I, _P, _P, _P]),
     "op_prompt_attention": (_I, [_I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _F, _F, _P, _I, _I, _P, _P, _P]),
+    "op_kv_extend": (_I, [_I, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "op_key_bounds": (_I, [_I, _P, _P, _I, _P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P]),
+    "op_block_select": (_I, [_I, _P, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "op_block_attention": (_I, [_I, _P, _I, _I, _I, _P, _P, _I, _F, _F, _P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -515,3 +519,79 @@ def op_prompt_attention(q, nkv, cu_seqlens, ctx_lens, kpool, vpool, kv_dtype, k_
         _tensor(fn, "ctx_lens", ctx_lens, dev, torch.int32, (nseq,)), pk, pv, kv_dtype, k_scale, v_scale,
         _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, num_blocks,
         _tensor(fn, "out", out, dev, torch.float32, (n, nq * d)), _err(fn, err, dev), _stream_of(stream, dev)))
+
+
+def op_kv_extend(ctx_lens, new_lens, bt, num_blocks, free_blocks, free_at, held, cu_seqlens, positions, row_seq, slots,
+                 free_next, err=None, stream=None) -> None:
+    """Table entries from the free list and the packed rows' layout for new_lens[s] more tokens of each sequence: ctx_lens,
+    new_lens, held [sequences], bt [sequences][width], free_blocks [any], free_at, free_next [1], cu_seqlens
+    [sequences + 1], positions, row_seq [n] (all int32), slots [n] int64. held may be ctx_lens, free_next free_at."""
+    fn = "op_kv_extend"
+    nseq, width = _shape(fn, "bt", bt, 2)
+    n, = _shape(fn, "positions", positions, 1)
+    nfree, = _shape(fn, "free_blocks", free_blocks, 1)
+    dev = _device(fn, "bt", bt)
+    if not 1 <= num_blocks <= 0x7fffffff:
+        raise MbtError(fn, -1)
+    i32, seqs, rows, one = torch.int32, (nseq,), (n,), (1,)
+    _check(fn, load().op_kv_extend(
+        nseq, _tensor(fn, "ctx_lens", ctx_lens, dev, i32, seqs), _tensor(fn, "new_lens", new_lens, dev, i32, seqs),
+        _tensor(fn, "bt", bt, dev, i32, (nseq, width)), width, num_blocks,
+        _tensor(fn, "free_blocks", free_blocks, dev, i32, (nfree,)), nfree, _tensor(fn, "free_at", free_at, dev, i32, one), n,
+        _tensor(fn, "held", held, dev, i32, seqs), _tensor(fn, "cu_seqlens", cu_seqlens, dev, i32, (nseq + 1,)),
+        _tensor(fn, "positions", positions, dev, i32, rows), _tensor(fn, "row_seq", row_seq, dev, i32, rows),
+        _tensor(fn, "slots", slots, dev, torch.int64, rows), _tensor(fn, "free_next", free_next, dev, i32, one),
+        _err(fn, err, dev), _stream_of(stream, dev)))
+
+
+def op_key_bounds(positions, bt, kpool, nkv, d, kv_dtype, num_blocks, bounds, scales, row_seq=None, err=None,
+                  stream=None) -> None:
+    """Per-channel ranges of the keys in the blocks that the rows are in: bounds [num_blocks + 1][nkv][2][d] int8, scales
+    [num_blocks + 1][nkv] fp32; kv_dtype DTYPE_BF16, DTYPE_E4M3 or DTYPE_E2M1."""
+    fn = "op_key_bounds"
+    n, = _shape(fn, "positions", positions, 1)
+    dev = _device(fn, "positions", positions)
+    nseq, width = _shape(fn, "bt", bt, 2)
+    pk, _ = _pools(fn, kpool, kpool, dev, nkv, d, num_blocks, kv_dtype)
+    _check(fn, load().op_key_bounds(
+        n, _tensor(fn, "positions", positions, dev, torch.int32, (n,)), _rows_of(fn, n, row_seq, nseq, dev), nseq,
+        _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, nkv, d, pk, kv_dtype, num_blocks,
+        _tensor(fn, "bounds", bounds, dev, torch.int8, (num_blocks + 1, nkv, 2, d)),
+        _tensor(fn, "scales", scales, dev, torch.float32, (num_blocks + 1, nkv)), _err(fn, err, dev), _stream_of(stream, dev)))
+
+
+def op_block_select(q, nkv, bounds, scales, positions, bt, num_blocks, keep_first, keep_last, sel, row_seq=None, err=None,
+                    stream=None) -> None:
+    """The blocks with the largest possible scores per row and KV head: q [n][nq][d] fp32, bounds and scales as
+    op_key_bounds leaves them, sel [n][nkv][k] int32 (ascending places in the table, then -1)."""
+    fn = "op_block_select"
+    n, nq, d = _shape(fn, "q", q, 3)
+    dev = _device(fn, "q", q)
+    nseq, width = _shape(fn, "bt", bt, 2)
+    k = _shape(fn, "sel", sel, 3)[2]
+    if num_blocks < 1 or keep_first < 0 or keep_last < 1 or keep_first + keep_last > k:   # before ctypes takes 32 bits of them
+        raise MbtError(fn, -1)
+    _check(fn, load().op_block_select(
+        n, _tensor(fn, "q", q, dev, torch.float32, (n, nq, d)), nq, nkv, d,
+        _tensor(fn, "bounds", bounds, dev, torch.int8, (num_blocks + 1, nkv, 2, d)),
+        _tensor(fn, "scales", scales, dev, torch.float32, (num_blocks + 1, nkv)),
+        _tensor(fn, "positions", positions, dev, torch.int32, (n,)), _rows_of(fn, n, row_seq, nseq, dev), nseq,
+        _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, num_blocks, keep_first, keep_last, k,
+        _tensor(fn, "sel", sel, dev, torch.int32, (n, nkv, k)), _err(fn, err, dev), _stream_of(stream, dev)))
+
+
+def op_block_attention(q, nkv, kpool, vpool, kv_dtype, k_scale, v_scale, positions, bt, sel, num_blocks, out, row_seq=None,
+                       err=None, stream=None) -> None:
+    """Attention over the selected blocks of a paged cache: q [n][nq][d] fp32, sel [n][nkv][k] int32, out [n][nq * d]
+    fp32; kv_dtype DTYPE_BF16, DTYPE_E4M3 or DTYPE_E2M1."""
+    fn = "op_block_attention"
+    n, nq, d = _shape(fn, "q", q, 3)
+    dev = _device(fn, "q", q)
+    nseq, width = _shape(fn, "bt", bt, 2)
+    k = _shape(fn, "sel", sel, 3)[2]
+    pk, pv = _pools(fn, kpool, vpool, dev, nkv, d, num_blocks, kv_dtype)
+    _check(fn, load().op_block_attention(
+        n, _tensor(fn, "q", q, dev, torch.float32, (n, nq, d)), nq, nkv, d, pk, pv, kv_dtype, k_scale, v_scale,
+        _tensor(fn, "positions", positions, dev, torch.int32, (n,)), _rows_of(fn, n, row_seq, nseq, dev), nseq,
+        _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, _tensor(fn, "sel", sel, dev, torch.int32, (n, nkv, k)),
+        k, num_blocks, _tensor(fn, "out", out, dev, torch.float32, (n, nq * d)), _err(fn, err, dev), _stream_of(stream, dev)))

@@ -1,0 +1,383 @@
+// Ranges of the keys in a cache block and the choice of blocks by them.
+//
+// key_bounds_kernel: per (block, KV head) and channel the smallest and largest
+// key as 8-bit codes, rounded outwards on a power-of-two grid.
+//
+// block_select_kernel: for integers u = rint(q 2^(10 - x)) of the group's
+// queries, P_i and N_i the sums of the positive and negative ones,
+//   sum_g u_g . k <= sum_i P_i max k_i + N_i min k_i
+// for every key of the block; the right side with the 8-bit codes is an exact
+// integer (|.| < 2^29: P - N <= 2^14, codes <= 127, 128 channels), so that no
+// order of summation can move a block over the border of the chosen ones.
+#include "fp4.cuh"
+#include "internal.h"
+#include "../../include/mbt_ops.h"
+
+namespace mbt {
+
+namespace {
+
+// Row i's sequence if its position and sequence are inside the table, else -1.
+__device__ __forceinline__ int row_in_table(const int* positions, const int* row_seq, int nseq, int bt_stride, int i, int& pos) {
+  pos = positions[i];
+  const int seq = row_seq ? row_seq[i] : i;
+  return pos >= 0 && pos / kBlockTokens < bt_stride && seq >= 0 && seq < nseq ? seq : -1;
+}
+
+// ---------------------------------------------------------------------------
+// ranges
+
+__device__ __forceinline__ uint32_t min_nan(uint32_t a, uint32_t b, bool bf) {
+  uint32_t r;
+  if (bf) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b, bool bf) {
+  uint32_t r;
+  if (bf) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Channels 8 c .. 8 c + 7 of a token's key as four 16-bit pairs, exactly: BF16
+// values as they are, e4m3 and 4-bit ones as FP16 (e2m1 * e4m3 has at most six
+// significant bits and lies in FP16's range).
+template <int D, int KV>
+__device__ __forceinline__ void key_pairs(const unsigned char* unit, int token, int c, uint32_t (&p)[4]) {
+  if constexpr (KV == KV_BF16) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(unit + token * 2 * D + 16 * c));
+    p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+  } else if constexpr (KV == KV_E4M3) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(unit + token * D + 8 * c));
+    p[0] = e4m3x2_to_h2bits(v.x); p[1] = e4m3x2_to_h2bits(v.x >> 16);
+    p[2] = e4m3x2_to_h2bits(v.y); p[3] = e4m3x2_to_h2bits(v.y >> 16);
+  } else {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(unit + token * (D / 2) + 4 * c));
+    const uint32_t s = __ldg(unit + kBlockTokens * (D / 2) + token * (D / kFp4Group) + c / 2), g = e4m3x2_to_h2bits(s | s << 8);
+    e2m1x8_to_h2(w, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(p[i]) : "r"(g));
+  }
+}
+
+constexpr int kBoundsWarps = 8;
+
+// One row per CTA, its KV heads over the warps. A lane holds eight channels; the
+// lanes of a warp cover 256 / D tokens at a time. Tokens past the row's are
+// replaced by its own.
+template <int D, int KV>
+__global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const KeyBoundsArgs a) {
+  constexpr int LANES = D / 8, TOK = 32 / LANES;
+  constexpr bool BF = KV == KV_BF16;
+  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int pos, next;
+  const int seq = row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, row, pos);
+  if (seq < 0) {
+    if (threadIdx.x == 0) set_err(a.err, MBT_DEV_POS_RANGE);
+    return;
+  }
+  if (row + 1 < a.n && row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, row + 1, next) == seq &&
+      next / kBlockTokens == pos / kBlockTokens)
+    return;                                                          // the next row's work
+  const int blk = a.bt[(size_t)seq * a.bt_stride + pos / kBlockTokens];
+  if (blk < 0 || blk > a.num_blocks) {
+    if (threadIdx.x == 0) set_err(a.err, MBT_DEV_BLOCK_RANGE);
+    return;
+  }
+  constexpr size_t UNIT = KV == KV_BF16 ? kBlockTokens * D * 2 : KV == KV_E4M3 ? kBlockTokens * D : fp4_unit_bytes(D);
+  const int c = lane % LANES, upto = pos % kBlockTokens;
+  for (int h = warp; h < a.nkv; h += kBoundsWarps) {
+    const size_t at = (size_t)blk * a.nkv + h;
+    const unsigned char* unit = reinterpret_cast<const unsigned char*>(a.kpool) + at * UNIT;
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int t = 0; t < kBlockTokens / TOK; ++t) {
+      uint32_t p[4];
+      key_pairs<D, KV>(unit, min(t * TOK + lane / LANES, upto), c, p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = t ? min_nan(lo[i], p[i], BF) : p[i];
+        hi[i] = t ? max_nan(hi[i], p[i], BF) : p[i];
+      }
+    }
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = min_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o), BF);
+        hi[i] = max_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o), BF);
+      }
+    float l[8], u[8];
+    uint32_t big = 0;                                                // a NaN's bits are larger than an infinity's
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = BF ? make_float2(bf16_lo(lo[i]), bf16_hi(lo[i])) : h2_to_float2(lo[i]);
+      const float2 y = BF ? make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])) : h2_to_float2(hi[i]);
+      l[2 * i] = x.x; l[2 * i + 1] = x.y;
+      u[2 * i] = y.x; u[2 * i + 1] = y.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) big = max(big, max(__float_as_uint(l[i]) & 0x7fffffffu, __float_as_uint(u[i]) & 0x7fffffffu));
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+    const bool bad = big >= 0x7f800000u;
+    // big = f 2^x with f in [1/2, 1): 127 * 2^(x - 7) holds it up to f = 127 / 128
+    const int e = max((int)(big >> 23) - 126 - ((big & 0x7fffffu) <= 0x7e0000u ? 7 : 6), -100);
+    const float down = bad || big == 0 ? 0.f : __int_as_float((127 - e) << 23);
+    uint32_t w[2][2] = {{0, 0}, {0, 0}};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // a product too small for fp32 is still on its side of 0
+      float x = bad ? 0.f : floorf(l[i] * down), y = bad ? 0.f : ceilf(u[i] * down);
+      if (down != 0.f && l[i] < 0.f) x = fminf(x, -1.f);
+      if (down != 0.f && u[i] > 0.f) y = fmaxf(y, 1.f);
+      w[0][i / 4] |= ((uint32_t)(int)x & 0xffu) << (8 * (i % 4));
+      w[1][i / 4] |= ((uint32_t)(int)y & 0xffu) << (8 * (i % 4));
+    }
+    if (lane < LANES) {
+      uint2* dst = reinterpret_cast<uint2*>(a.bounds + at * 2 * D) + c;
+      dst[0] = make_uint2(w[0][0], w[0][1]);
+      dst[LANES] = make_uint2(w[1][0], w[1][1]);
+    }
+    if (lane == 0) a.scales[at] = bad ? __int_as_float(0x7f800000) : big == 0 ? 0.f : __int_as_float((e + 127) << 23);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// choice
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelCluster = 8;
+constexpr int kBins = 256;
+constexpr uint32_t kKept = 0xffffffffu;      // key of a block that is taken in any case; scores' are lower
+
+// Dot product of four unsigned with four signed bytes, added to c.
+__device__ __forceinline__ int dp4a_us(uint32_t u, uint32_t s, int c) {
+  int r;
+  asm("dp4a.u32.s32 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(s), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
+  return __float_as_uint(ld_dsmem_f32(p, rank));
+}
+// Order-preserving bits of a float that is not NaN; -0 counts as 0.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// A cluster per (row, KV head); its CTAs take equal runs of the context's blocks
+// and leave their keys in shared memory. The k-th largest key is found by
+// histograms of 256 bins over the range that is left, summed over the cluster.
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSelectArgs a) {
+  constexpr int REC = 2 * D, LANES = REC / 16, PER = 32 / LANES;      // bytes of a range, lanes on one, ranges per load
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ __align__(16) uint8_t digit[2][REC];                     // weights' low and high bytes
+  __shared__ uint32_t red[kSelWarps][2], hist[2][kBins], sum[kBins + 1], ends[2], found[2], counts[2], per_warp[kSelWarps][2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)(blockIdx.x % (unsigned)a.cluster), pair = (int)(blockIdx.x / (unsigned)a.cluster);
+  const int h = pair % a.nkv, row = pair / a.nkv, G = a.nq / a.nkv;
+  int* sel = a.sel + (size_t)pair * a.k;
+  int pos;
+  const int seq = row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, row, pos);
+  const int held = seq < 0 ? 0 : pos / kBlockTokens + 1;
+  const int* table = a.bt + (size_t)max(seq, 0) * a.bt_stride;
+  if (seq < 0 && tid == 0 && rank == 0 && h == 0) set_err(a.err, MBT_DEV_POS_RANGE);
+  if (held <= a.k) {                                                  // all of them; the cluster's CTAs agree
+    for (int j = rank * kSelThreads + tid; j < a.k; j += a.cluster * kSelThreads) {
+      if (j < held && (uint32_t)table[j] > (uint32_t)a.num_blocks) set_err(a.err, MBT_DEV_BLOCK_RANGE);
+      sel[j] = j < held ? j : -1;
+    }
+    return;
+  }
+
+  // weights: the group's rounded queries
+  const float* q = a.q + ((size_t)row * a.nq + (size_t)h * G) * D;
+  uint32_t big = 0;
+  for (int i = tid; i < G * D; i += kSelThreads) big = max(big, __float_as_uint(__ldg(q + i)) & 0x7fffffffu);
+  big = __reduce_max_sync(0xffffffffu, big);
+  if (lane == 0) red[warp][0] = big;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) big = max(big, red[w][0]);
+  for (int i = tid; i < D; i += kSelThreads) {
+    int up = 0, down = 0;
+    if (big != 0 && big < 0x7f800000u) {
+      int x;
+      frexpf(__uint_as_float(big), &x);
+      for (int g = 0; g < G; ++g) {
+        const int u = (int)rintf(ldexpf(__ldg(q + g * D + i), 10 - x));
+        up += max(u, 0);
+        down += max(-u, 0);
+      }
+    }
+    digit[0][i] = (uint8_t)down; digit[1][i] = (uint8_t)(down >> 8);
+    digit[0][D + i] = (uint8_t)up; digit[1][D + i] = (uint8_t)(up >> 8);
+  }
+  __syncthreads();
+  const int l = lane % LANES;
+  const uint4 w0 = *reinterpret_cast<const uint4*>(digit[0] + 16 * l), w1 = *reinterpret_cast<const uint4*>(digit[1] + 16 * l);
+  const int side = l < LANES / 2 ? -1 : 1;
+
+  // keys of this CTA's blocks [j0, j0 + cnt)
+  const int share = (held + a.cluster - 1) / a.cluster, j0 = min(rank * share, held), cnt = min(share, held - j0);
+  uint32_t lowest = 0xffffffffu, highest = 0;
+  for (int i0 = warp * PER; i0 < cnt; i0 += kSelWarps * PER) {
+    const int i = i0 + lane / LANES, j = j0 + i;
+    int id = i < cnt ? __ldg(table + j) : 0;
+    if ((uint32_t)id > (uint32_t)a.num_blocks) {
+      set_err(a.err, MBT_DEV_BLOCK_RANGE);
+      id = a.num_blocks;
+    }
+    const size_t at = (size_t)id * a.nkv + h;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.bounds + at * REC) + l);
+    const float scale = __ldg(a.scales + at);
+    int lo = dp4a_us(w0.w, v.w, dp4a_us(w0.z, v.z, dp4a_us(w0.y, v.y, dp4a_us(w0.x, v.x, 0))));
+    int hi = dp4a_us(w1.w, v.w, dp4a_us(w1.z, v.z, dp4a_us(w1.y, v.y, dp4a_us(w1.x, v.x, 0))));
+    int dot = side * (hi * 256 + lo);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (l == 0 && i < cnt) {
+      const float inf = __int_as_float(0x7f800000);
+      uint32_t key = key_of(scale < inf ? (float)dot * scale : inf);
+      if (j < a.keep_first || j >= held - a.keep_last) key = kKept;
+      else { lowest = min(lowest, key); highest = max(highest, key); }
+      keys[i] = key;
+    }
+  }
+
+  // the cluster's range of keys
+  lowest = __reduce_min_sync(0xffffffffu, lowest);
+  highest = __reduce_max_sync(0xffffffffu, highest);
+  if (lane == 0) { red[warp][0] = lowest; red[warp][1] = highest; }
+  for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = hist[1][i] = 0;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 0; w < kSelWarps; ++w) { lowest = min(lowest, red[w][0]); highest = max(highest, red[w][1]); }
+    ends[0] = lowest; ends[1] = highest;
+  }
+  cluster_sync_all();
+  for (int r = 0; r < a.cluster; ++r) {
+    lowest = min(lowest, ld_dsmem_u32(&ends[0], r));
+    highest = max(highest, ld_dsmem_u32(&ends[1], r));
+  }
+  // `need` of the keys in [base, base + 2^bits) are to be found, all above are taken
+  uint32_t base = lowest, need = a.k - a.keep_first - a.keep_last;
+  int bits = highest > lowest ? 32 - __clz(highest - lowest) : 0;
+  bool all = need == 0 || bits == 0;                                  // nothing to narrow
+  for (int turn = 0; bits > 0 && need > 0; ++turn) {
+    uint32_t* mine = hist[turn & 1];
+    const int shift = max(bits - 8, 0);
+    const uint32_t top = bits >= 32 ? 0xffffffffu : (1u << bits) - 1;
+    for (int i = tid; i < cnt; i += kSelThreads) {
+      const uint32_t off = keys[i] - base;
+      if (keys[i] != kKept && keys[i] >= base && off <= top) atomicAdd(&mine[off >> shift], 1u);
+    }
+    cluster_sync_all();
+    uint32_t n = 0;
+    for (int r = 0; r < a.cluster; ++r) n += ld_dsmem_u32(&mine[tid], r);
+    hist[(turn + 1) & 1][tid] = 0;                                    // read by all before this turn's barrier
+    sum[tid] = n;
+    __syncthreads();
+    if (warp == 0) {                                                  // counts from the highest bin down
+      uint32_t c[kBins / 32], t = 0;
+#pragma unroll
+      for (int i = 0; i < kBins / 32; ++i) { c[i] = sum[kBins - 1 - (lane * (kBins / 32) + i)]; t += c[i]; }
+      uint32_t before = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += u;
+      }
+      before -= t;
+#pragma unroll
+      for (int i = 0; i < kBins / 32; ++i) {
+        if (before < need && need <= before + c[i]) { found[0] = kBins - 1 - (lane * (kBins / 32) + i); found[1] = before; }
+        before += c[i];
+      }
+    }
+    __syncthreads();
+    const uint32_t bin = found[0], in_bin = sum[bin];
+    need -= found[1];
+    base += bin << shift;
+    bits = shift;
+    all = need == in_bin;
+    __syncthreads();
+    if (all) break;
+  }
+  // taken: kept ones, keys above the last range, and of those in it all or (one
+  // value is left) the first `need`
+  const uint32_t span = bits >= 32 ? 0xffffffffu : (1u << bits) - 1;
+  const bool none = a.k == a.keep_first + a.keep_last;
+  auto kind = [&](uint32_t key) {                                     // 2 taken, 1 in the last range, 0 not
+    if (key == kKept) return 2;
+    if (none || key < base) return 0;
+    return key - base > span ? 2 : 1;
+  };
+  const int seg = (cnt + kSelThreads - 1) / kSelThreads * 32;         // a warp's run of keys
+  const int s0 = min(warp * seg, cnt), s1 = min(s0 + seg, cnt);
+  uint32_t sure = 0, tied = 0;
+  for (int i = s0; i < s1; i += 32) {
+    const int t = i + lane < s1 ? kind(keys[i + lane]) : 0;
+    sure += __popc(__ballot_sync(0xffffffffu, t == 2));
+    tied += __popc(__ballot_sync(0xffffffffu, t == 1));
+  }
+  if (lane == 0) { per_warp[warp][0] = sure; per_warp[warp][1] = tied; }
+  __syncthreads();
+  if (tid == 0) {
+    counts[0] = counts[1] = 0;
+    for (int w = 0; w < kSelWarps; ++w) { counts[0] += per_warp[w][0]; counts[1] += per_warp[w][1]; }
+  }
+  cluster_sync_all();
+  uint32_t sure_before = 0, tied_before = 0;
+  for (int r = 0; r < rank; ++r) { sure_before += ld_dsmem_u32(&counts[0], r); tied_before += ld_dsmem_u32(&counts[1], r); }
+  for (int w = 0; w < warp; ++w) { sure_before += per_warp[w][0]; tied_before += per_warp[w][1]; }
+  for (int i = s0; i < s1; i += 32) {
+    const int t = i + lane < s1 ? kind(keys[i + lane]) : 0;
+    const uint32_t m2 = __ballot_sync(0xffffffffu, t == 2), m1 = __ballot_sync(0xffffffffu, t == 1), below = (1u << lane) - 1;
+    const uint32_t ahead = tied_before + __popc(m1 & below);
+    if (t == 2 || (t == 1 && ahead < need)) sel[sure_before + __popc(m2 & below) + min(ahead, need)] = j0 + i + lane;
+    sure_before += __popc(m2);
+    tied_before += __popc(m1);
+  }
+  cluster_sync_all();                                                 // stay resident until the others have read
+}
+
+}  // namespace
+
+cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t s) {
+  auto go = [&](auto kernel) {
+    kernel<<<(unsigned)a.n, 32 * kBoundsWarps, 0, s>>>(a);
+    return cudaGetLastError();
+  };
+  if (a.d == 64)
+    return a.kv == KV_BF16 ? go(key_bounds_kernel<64, KV_BF16>) : a.kv == KV_E4M3 ? go(key_bounds_kernel<64, KV_E4M3>)
+                                                                                  : go(key_bounds_kernel<64, KV_FP4>);
+  return a.kv == KV_BF16 ? go(key_bounds_kernel<128, KV_BF16>) : a.kv == KV_E4M3 ? go(key_bounds_kernel<128, KV_E4M3>)
+                                                                                 : go(key_bounds_kernel<128, KV_FP4>);
+}
+
+cudaError_t block_select_init() {
+  for (const void* f : {(const void*)block_select_kernel<64>, (const void*)block_select_kernel<128>}) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               MBT_SELECT_MAX_BLOCKS / kSelCluster * 4);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_block_select(const BlockSelectArgs& a, cudaStream_t s) {
+  BlockSelectArgs args = a;
+  args.cluster = kSelCluster;
+  const long long grid = (long long)a.n * a.nkv * args.cluster;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  void* p[] = {&args};
+  const size_t smem = (size_t)((a.bt_stride + args.cluster - 1) / args.cluster) * 4;
+  return launch_ex(a.d == 64 ? (const void*)block_select_kernel<64> : (const void*)block_select_kernel<128>,
+                   dim3((unsigned)grid), dim3(kSelThreads), smem, s, p, false, -1, args.cluster);
+}
+
+}  // namespace mbt

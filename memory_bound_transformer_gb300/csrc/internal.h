@@ -303,4 +303,41 @@ cudaError_t attn_fp4_plan(AttnFp4Args* a, int num_sms);     // sets hblocks, clu
 cudaError_t launch_attention_fp4(const AttnFp4Args& a, cudaStream_t s);
 cudaError_t attn_fp4_init();
 
+// ---------------------------------------------------------------------------
+// attention over selected blocks of the paged cache
+
+// Table entries for new tokens from the free list, and the packed rows' layout.
+// held may be ctx_lens, free_next may be free_at.
+struct KvExtendArgs {
+  int nseq; const int* ctx_lens; const int* new_lens; int* bt; int bt_stride; int num_blocks;
+  const int* free_blocks; int nfree; const int* free_at; int n;
+  int* held; int* cu; int* positions; int* row_seq; int64_t* slots; int* free_next; uint32_t* err;
+};
+cudaError_t launch_kv_extend(const KvExtendArgs& a, cudaStream_t s);
+
+// Per-channel ranges of the keys in the blocks that the rows are in.
+struct KeyBoundsArgs {
+  int n; const int* positions; const int* row_seq; int nseq; const int* bt; int bt_stride; int nkv, d;
+  const void* kpool; int kv; int num_blocks; int8_t* bounds; float* scales; uint32_t* err;
+};
+cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t s);
+
+// The k blocks of each (row, KV head) whose ranges allow the largest scores.
+struct BlockSelectArgs {
+  int n; const float* q; int nq, nkv, d; const int8_t* bounds; const float* scales;
+  const int* positions; const int* row_seq; int nseq; const int* bt; int bt_stride; int num_blocks;
+  int keep_first, keep_last, k; int* sel; uint32_t* err;
+  int cluster;
+};
+cudaError_t launch_block_select(const BlockSelectArgs& a, cudaStream_t s);
+cudaError_t block_select_init();
+
+// Attention of n rows over the blocks sel[n][nkv][k] of their contexts.
+struct BlockAttnArgs {
+  int n; const float* q; int nq, nkv, d; int kv; const void* kpool; const void* vpool; float k_scale, v_scale;
+  const int* positions; const int* row_seq; int nseq; const int* bt; int bt_stride;
+  const int* sel; int k; int num_blocks; float* out; uint32_t* err;
+};
+cudaError_t launch_block_attention(const BlockAttnArgs& a, cudaStream_t s);
+
 }  // namespace mbt

@@ -9,21 +9,10 @@
 #include "common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
+#include "ops_checks.h"
 #include "../../include/mbt_ops.h"
 
-using namespace mbt;
-
-namespace {
-bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
-// A tensor's scale. Beyond these its products with block scales, queries and
-// their reciprocals could leave fp32's range.
-bool scale_ok(float s) { return s >= 0x1p-64f && s <= 0x1p64f; }
-// A row of a block table: its token count, rounded up to tiles, stays an int.
-bool table_ok(const int32_t* bt, int bt_stride) { return bt && bt_stride >= 1 && bt_stride <= (1 << 26); }
-// Heads and head size that the cache's kernels take.
-bool heads_ok(int nq, int nkv, int d) {
-  return nq >= 1 && nkv >= 1 && nq % nkv == 0 && nq / nkv <= 16 && (d == 64 || d == 128);
-}
+namespace mbt {
 // SM count of the current device; the kernels' shared-memory limits are raised
 // once per device.
 int device_setup(int* sms) {
@@ -36,17 +25,16 @@ int device_setup(int* sms) {
   if (!known[dev]) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MBT_ERR_NO_DEVICE;
-    if (attn_fp4_init() != cudaSuccess || prompt_attention_init() != cudaSuccess) return MBT_ERR_CUDA;
+    if (attn_fp4_init() != cudaSuccess || prompt_attention_init() != cudaSuccess || block_select_init() != cudaSuccess)
+      return MBT_ERR_CUDA;
     known[dev] = n;
   }
   *sms = known[dev];
   return MBT_OK;
 }
-int status(cudaError_t e) {
-  if (e == cudaSuccess) return MBT_OK;
-  return e == cudaErrorInvalidValue ? MBT_ERR_BAD_ARG : MBT_ERR_CUDA;
-}
-}  // namespace
+}  // namespace mbt
+
+using namespace mbt;
 
 extern "C" {
 
@@ -138,14 +126,14 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
   if (n < 1 || !q || !heads_ok(nq, nkv, d) || nseq < 1 || !cu_seqlens || !ctx_lens || !kpool || !vpool ||
       !scale_ok(k_scale) || !scale_ok(v_scale) || !table_ok(bt, bt_stride) || num_blocks < 1 || !out)
     return MBT_ERR_BAD_ARG;
-  if (kv_dtype != MBT_DTYPE_BF16 && kv_dtype != MBT_DTYPE_E4M3 && kv_dtype != MBT_DTYPE_E2M1) return MBT_ERR_BAD_ARG;
+  if (!cache_ok(kv_dtype)) return MBT_ERR_BAD_ARG;
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out)) return MBT_ERR_BAD_ARG;
   int sms = 0;
   const int rc = device_setup(&sms);
   if (rc != MBT_OK) return rc;
   PromptArgs a = {};
   a.n = n; a.q = q; a.nq = nq; a.nkv = nkv; a.d = d; a.kpool = kpool; a.vpool = vpool;
-  a.kv = kv_dtype == MBT_DTYPE_BF16 ? KV_BF16 : kv_dtype == MBT_DTYPE_E4M3 ? KV_E4M3 : KV_FP4;
+  a.kv = kv_type(kv_dtype);
   a.k_scale = k_scale; a.v_scale = v_scale; a.nseq = nseq; a.cu = cu_seqlens; a.lens = ctx_lens; a.bt = bt;
   a.bt_stride = bt_stride; a.num_blocks = num_blocks; a.out = out; a.err = err;
   return status(launch_prompt_attention(a, (cudaStream_t)stream));

@@ -43,7 +43,13 @@ pins live in tests/test_oracle_*.py):
   zero, NaN, infinite, tiny and saturating groups; pack_pool / unpack_pool: a
   round trip and single bytes at hand-computed offsets; rows_attention /
   prompt_positions: softmax sums written out over a gathered context.
+* blocks.extend: hand-written tables, lists that run out, padding rows;
+  blocks.key_range: every key inside its channel's range, ranges no wider than a
+  step each way, the exponent minimal; blocks.scores: an upper bound of every
+  key's rounded score and equal to it for a block of one grid key; blocks.select:
+  brute force over all subsets of a few blocks; blocks.attention: kv_fp4's
+  rows_attention where all blocks are selected.
 
 No function is "parity unpinned".
 """
-from . import numerics, decode, sampling, kv_fp4  # noqa: F401
+from . import numerics, decode, sampling, kv_fp4, blocks  # noqa: F401
