@@ -1,7 +1,29 @@
 // Softmax attention over selected blocks of the paged KV cache:
 //   o_h = sum_t softmax_t(q_h . K_t / sqrt(d)) V_t   over the tokens t <= p of the
 // blocks chosen for the row and the KV head of h, one pass with the running
-// maximum and sum of the softmax.
+// maximum and sum of the softmax ("GPU Inference Internals", "The KV-Cache
+// Ledger": the bytes of the cache are what a decode step reads).
+//
+// What bounds it: every chosen block is read once, 2 x 16 tokens of d values, so
+// the work per value has to stay below what the SM issues meanwhile. A warp
+// takes whole blocks from the list, straight from memory into registers: no
+// shared memory, no barrier in the loop.
+// * Queries and probabilities enter mma.sync.m16n8k16 as parts stacked on M: rows
+//   0..7 the high parts of the group's heads, rows 8..15 the next. Over a BF16
+//   cache they are three BF16 parts (24 bits; the third in a second MMA whose rows
+//   8..15 are zeros), over the narrow caches, whose values FP16 holds exactly, two
+//   FP16 parts (2^-22), probabilities relative to 2^-14 of the largest so that
+//   FP16's smallest steps lie at 2^-39 of it.
+// * The contraction may run over channels in any order: thread (g, t) of a warp
+//   takes 16-byte pieces of token g's key, and the queries are laid out the same
+//   way. V's pairs are two tokens of one channel, interleaved from two tokens'
+//   words. The score accumulators are the A fragments of P V as they stand.
+// * The tensor core's fp32 accumulation truncates, so chains are short (d / 16
+//   steps for scores, a step's blocks for P V) and sums over steps are IEEE fp32.
+// * The loads of the next step's keys are under way while the softmax and P V of
+//   this one are done, its values' from there on.
+#include <algorithm>
+
 #include "fp4.cuh"
 #include "internal.h"
 
@@ -9,100 +31,564 @@ namespace mbt {
 
 namespace {
 
-constexpr int kBaThreads = 128;
+constexpr int kBaWarps = 4;                 // most warps of a CTA
+constexpr int kBaPerSm = 12;                // warps per SM (168 registers a thread)
+constexpr int kBaHeads = 8;                 // query heads per CTA (MMA rows)
+constexpr int kBaCluster = 8;               // most CTAs of a cluster
 
-// Values of D / 32 neighbouring channels of a token, before the tensor's scale.
-template <int D, int KV>
-__device__ __forceinline__ void values(const unsigned char* unit, int token, int lane, float (&x)[D / 32]) {
-  constexpr int N = D / 32;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int c = lane * N + i;
-    if constexpr (KV == KV_BF16) {
-      x[i] = __bfloat162float(reinterpret_cast<const bf16*>(unit)[token * D + c]);
-    } else if constexpr (KV == KV_E4M3) {
-      x[i] = e4m3_to_f32(unit[token * D + c]);
-    } else {
-      const uint32_t code = unit[token * (D / 2) + c / 2] >> (4 * (c & 1)) & 15u;
-      uint32_t p[2];
-      e2m1x4_to_h2(code, p);
-      x[i] = h2_to_float2(p[0]).x * e4m3_to_f32(unit[kBlockTokens * (D / 2) + token * (D / kFp4Group) + c / kFp4Group]);
-    }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Parts of two values as 16-bit pairs: FP16 high and low, or BF16 high, middle and low.
+template <bool BF>
+__device__ __forceinline__ void split(float x0, float x1, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+  if constexpr (BF) {
+    p0 = pack_b2(x0, x1);
+    x0 -= bf16_lo(p0); x1 -= bf16_hi(p0);
+    p1 = pack_b2(x0, x1);
+    p2 = pack_b2(x0 - bf16_lo(p1), x1 - bf16_hi(p1));
+  } else {
+    p0 = pack_h2(x0, x1);
+    const float2 h = h2_to_float2(p0);
+    p1 = pack_h2(x0 - h.x, x1 - h.y);
+    p2 = 0;
   }
 }
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (BF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-// A CTA per (row, KV head), a warp per query head in turn, a lane per D / 32 channels.
+// Words of a lane, read once, past L1.
+template <int N>
+__device__ __forceinline__ void ld_words(uint32_t (&w)[N], const unsigned char* p, int at) {
+  if constexpr (N == 4)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p + at));
+  else if constexpr (N == 2)
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p + at));
+  else
+    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p + at));
+}
+
+// How a block's K and V lie over a warp. Thread (g, t) = (lane / 4, lane % 4)
+// holds a quarter of the channels of keys g and g + 8 and an eighth of those of
+// the values 2t, 2t + 1, 2t + 8 and 2t + 9.
 template <int D, int KV>
-__global__ void __launch_bounds__(kBaThreads) block_attention_kernel(const BlockAttnArgs a) {
-  constexpr int N = D / 32;
-  constexpr size_t UNIT = KV == KV_BF16 ? kBlockTokens * D * 2 : KV == KV_E4M3 ? kBlockTokens * D : fp4_unit_bytes(D);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = (int)(blockIdx.x % (unsigned)a.nkv), row = (int)(blockIdx.x / (unsigned)a.nkv), G = a.nq / a.nkv;
-  const int pos = a.positions[row], seq = a.row_seq ? a.row_seq[row] : row;
-  const bool ok = pos >= 0 && pos / kBlockTokens < a.bt_stride && seq >= 0 && seq < a.nseq;
-  if (!ok && h == 0 && threadIdx.x == 0) set_err(a.err, MBT_DEV_POS_RANGE);
-  const int* sel = a.sel + (size_t)blockIdx.x * a.k;
-  for (int g = warp; g < G; g += kBaThreads / 32) {
-    const size_t at = ((size_t)row * a.nq + (size_t)h * G + g) * D + lane * N;
-    float q[N], o[N], m = -INFINITY, l = 0.f;
+struct Lay {
+  static constexpr bool BF = KV == KV_BF16;
+  static constexpr int ROW = KV == KV_BF16 ? 2 * D : KV == KV_E4M3 ? D : D / 2;   // bytes of a token
+  static constexpr int UNIT = KV == KV_FP4 ? fp4_unit_bytes(D) : kBlockTokens * ROW;
+  static constexpr int KB = ROW / 4 < 16 ? ROW / 4 : 16, KP = ROW / 4 / KB;       // bytes of a key's piece, pieces
+  static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16, VP = ROW / 8 / VB;       // of a value's
+  static constexpr int KC = D / 4 / KP, VC = D / 8 / VP;                          // channels of a piece
+  static constexpr int TB = KV == KV_BF16 ? 128 / D : KV == KV_E4M3 ? 256 / D : 256 / D;   // blocks of a step
+  static constexpr int KS = D / 16, NT = D / 8;                                   // MMA steps of a score, n-tiles of the output
+  static constexpr int SC = KV == KV_FP4 ? TB : 1;                                // scale registers
+  // channel of a lane's i-th query value; of the c-th value of column g of the output's n-tiles
+  static __device__ __forceinline__ int q_channel(int t, int i) { return i / KC * 4 * KC + KC * t + i % KC; }
+  static __device__ __forceinline__ int v_channel(int g, int c) { return c / VC * 8 * VC + VC * g + c % VC; }
+};
+
+// The chosen blocks of a warp: entries first, first + stride, .. of the row's
+// list, 32 at a time, a lane per entry.
+struct Picks {
+  const int* sel; const int* table;
+  int k, stride, at, last, num_blocks;      // at: this lane's next entry; last: the context's last block
+  uint32_t* err;
+  uint32_t mask;                            // entries of this turn still to do
+  int e, id, e2;                            // this turn's entry and block id, the next turn's entry
+
+  __device__ __forceinline__ int entry() {
+    const int x = at < k ? __ldg(sel + at) : -1;
+    at = at < k ? at + 32 * stride : k;     // below k + 32 * stride: the caller sees to its range
+    return x;
+  }
+  __device__ __forceinline__ void turn() {
+    e = e2;
+    if (e > last) {
+      set_err(err, MBT_DEV_BLOCK_RANGE);
+      e = -1;
+    }
+    mask = __ballot_sync(0xffffffffu, e >= 0);
+    id = e >= 0 ? __ldg(table + e) : 0;
+    if ((uint32_t)id > (uint32_t)num_blocks) {
+      set_err(err, MBT_DEV_BLOCK_RANGE);
+      id = num_blocks;
+    }
+    e2 = entry();
+  }
+  __device__ __forceinline__ bool any() {                             // warp-uniform
+    while (!mask) {
+      if (!__any_sync(0xffffffffu, at < k || e2 >= 0)) return false;
+      turn();
+    }
+    return true;
+  }
+  // The next block: its id, and its first token relative to the row's position
+  // (0 or less: live), or an id with no live token.
+  __device__ __forceinline__ void take(int& blk, int& live, int pos) {
+    if (mask) {
+      const int src = __ffs(mask) - 1;
+      mask &= mask - 1;
+      blk = __shfl_sync(0xffffffffu, id, src);
+      live = min(kBlockTokens, pos - __shfl_sync(0xffffffffu, e, src) * kBlockTokens + 1);
+    } else {
+      blk = num_blocks;
+      live = 0;
+    }
+  }
+};
+
+template <int D, int KV>
+struct BlockWarp {
+  using L = Lay<D, KV>;
+  static constexpr bool BF = L::BF;
+  uint32_t k[L::TB][2][L::KP][L::KB / 4], v[L::TB][4][L::VP][L::VB / 4];
+  uint32_t ks[L::SC][2], vs[L::SC][2];                                // 4-bit: scale bytes of the keys and values
+  float m, l, o[L::NT][2];
+
+  __device__ __forceinline__ void start() {
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) { q[i] = a.q[at + i]; o[i] = 0.f; }
-    for (int j = 0; ok && j < a.k; ++j) {
-      const int e = sel[j];
-      if (e < 0) continue;
-      if (e > pos / kBlockTokens) { set_err(a.err, MBT_DEV_BLOCK_RANGE); continue; }
-      int id = a.bt[(size_t)seq * a.bt_stride + e];
-      if (id < 0 || id > a.num_blocks) { set_err(a.err, MBT_DEV_BLOCK_RANGE); id = a.num_blocks; }
-      const size_t off = ((size_t)id * a.nkv + h) * UNIT;
-      const int live = min(kBlockTokens, pos - e * kBlockTokens + 1);
-      float s[kBlockTokens], mn = m, x[N];
+    for (int i = 0; i < L::NT; ++i) o[i][0] = o[i][1] = 0.f;
+  }
+  __device__ __forceinline__ void load_k(const unsigned char* pool, const int (&blk)[L::TB], int nkv, int h, int lane) {
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-      for (int t = 0; t < kBlockTokens; ++t) {
-        s[t] = 0.f;
-        values<D, KV>(reinterpret_cast<const unsigned char*>(a.kpool) + off, min(t, live - 1), lane, x);
+    for (int b = 0; b < L::TB; ++b) {
+      const unsigned char* unit = pool + ((size_t)blk[b] * nkv + h) * L::UNIT;
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[t] = fmaf(q[i], x[i], s[t]);
-        s[t] = warp_sum(s[t]) * (a.k_scale / sqrtf((float)D));
-        s[t] += s[t] - s[t];                                         // an infinite score is no score: NaN
-        if (t >= live) s[t] = -INFINITY;
-        mn = fmaxf(mn, s[t]);
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int p = 0; p < L::KP; ++p) ld_words(k[b][n][p], unit, (8 * n + g) * L::ROW + (4 * p + t) * L::KB);
+        if constexpr (KV == KV_FP4) {
+          const unsigned char* s = unit + kBlockTokens * L::ROW + (8 * n + g) * (D / 16) + t * (D / 64);
+          ks[b][n] = D == 128 ? *reinterpret_cast<const uint16_t*>(s) : *s;
+        }
       }
-      // a block's sums on their own first: long sums of equal shares would round one way
-      const float f = expf(m - mn);
-      float lb = 0.f, ob[N] = {};
+    }
+  }
+  __device__ __forceinline__ void load_v(const unsigned char* pool, const int (&blk)[L::TB], int nkv, int h, int lane) {
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-      for (int t = 0; t < kBlockTokens; ++t) {
-        if (t >= live) continue;
-        const float p = expf(s[t] - mn);
-        lb += p;
-        values<D, KV>(reinterpret_cast<const unsigned char*>(a.vpool) + off, t, lane, x);
+    for (int b = 0; b < L::TB; ++b) {
+      const unsigned char* unit = pool + ((size_t)blk[b] * nkv + h) * L::UNIT;
 #pragma unroll
-        for (int i = 0; i < N; ++i) ob[i] += p * x[i];
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < L::VP; ++p)
+          ld_words(v[b][i][p], unit, (2 * t + (i & 1) + 8 * (i >> 1)) * L::ROW + (8 * p + g) * L::VB);
+      if constexpr (KV == KV_FP4) {
+        const unsigned char* s = unit + kBlockTokens * L::ROW + 2 * t * (D / 16) + g * (D / 8) / 16;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) vs[b][n] = s[8 * n * (D / 16)] | (uint32_t)s[(8 * n + 1) * (D / 16)] << 8;
       }
-      m = mn;
-      l = l * f + lb;
+    }
+  }
+
+  // Scores of a step: s[2 b + n][e] of head g and token 2 t + e + 8 n of block b.
+  // frag: the queries' fragments, [KS][32 lanes] x 4 words; frag_lo: the third parts', x 2.
+  __device__ __forceinline__ void scores(float (&s)[2 * L::TB][2], const uint4* frag, const uint2* frag_lo, int lane) {
+    float acc[2 * L::TB][4];
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = o[i] * f + ob[i];
+    for (int i = 0; i < 2 * L::TB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    uint32_t sc[2 * L::TB];
+#pragma unroll
+    for (int st = 0; st < L::KS; ++st) {
+      const uint4 a = frag[st * 32 + lane];
+      uint2 z = make_uint2(0, 0);
+      if constexpr (BF) z = frag_lo[st * 32 + lane];
+#pragma unroll
+      for (int i = 0; i < 2 * L::TB; ++i) {
+        uint32_t b0, b1;
+        if constexpr (KV == KV_BF16) {
+          b0 = k[i / 2][i & 1][st / 2][2 * (st & 1)];
+          b1 = k[i / 2][i & 1][st / 2][2 * (st & 1) + 1];
+        } else if constexpr (KV == KV_E4M3) {
+          const uint32_t w = k[i / 2][i & 1][st / 4][st % 4];
+          b0 = e4m3x2_to_h2bits(w);
+          b1 = e4m3x2_to_h2bits(w >> 16);
+        } else {
+          if (st % 4 == 0) {                                          // a scale per 16 channels
+            const uint32_t byte = ks[i / 2][i & 1] >> (8 * (st / 4)) & 0xffu;
+            sc[i] = e4m3x2_to_h2bits(byte | byte << 8);
+          }
+          uint32_t h[2];
+          e2m1x4_to_h2(k[i / 2][i & 1][0][st / 2] >> (16 * (st & 1)) & 0xffffu, h);
+          b0 = hmul2(h[0], sc[i]);
+          b1 = hmul2(h[1], sc[i]);
+        }
+        mma<BF>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
+        if constexpr (BF) mma<BF>(acc[i], z.x, 0u, z.y, 0u, b0, b1);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) a.out[at + i] = l == 0.f ? 0.f : o[i] * (a.v_scale / l);
+    for (int i = 0; i < 2 * L::TB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        s[i][e] = acc[i][e] + acc[i][e + 2];
+        if constexpr (BF) s[i][e] += s[i][e] - s[i][e];               // of a key that is not finite: NaN
+      }
   }
+
+  // Softmax of head g over the lane's tokens, then O = O * al + P V. live: tokens
+  // of each block that the row sees. spec: where values that are not finite go
+  // (null: they are not looked for).
+  __device__ __forceinline__ void rest(float (&s)[2 * L::TB][2], const int (&live)[L::TB], float fac, float* spec, int lane) {
+    constexpr float UP = BF ? 0.f : 14.f;
+    const int g = lane >> 2, t = lane & 3;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2 * L::TB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (8 * (i & 1) + 2 * t + e >= live[i / 2]) s[i][e] = -INFINITY;
+        mx = fmaxf(mx, s[i][e]);
+      }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // differences of scores first: equal ones stay equal however large they are
+    const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn, al = ex2((m - mu) * fac);
+    m = mn;
+    float sum = 0.f;
+    uint32_t pa[2 * L::TB][3];
+#pragma unroll
+    for (int i = 0; i < 2 * L::TB; ++i) {
+      const float p0 = ex2(fmaf(s[i][0] - mu, fac, UP)), p1 = ex2(fmaf(s[i][1] - mu, fac, UP));
+      sum += p0 + p1;
+      split<BF>(p0, p1, pa[i][0], pa[i][1], pa[i][2]);
+    }
+    l = fmaf(l, al, sum);
+#pragma unroll
+    for (int b = 0; b < L::TB; ++b) {
+      if (live[b] < kBlockTokens) {                                   // the same for the whole warp
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (2 * t + (i & 1) + 8 * (i >> 1) < live[b]) continue;
+          if constexpr (KV == KV_FP4) {
+            vs[b][i >> 1] &= (i & 1) ? 0x00ffu : 0xff00u;
+          } else {
+#pragma unroll
+            for (int p = 0; p < L::VP; ++p)
+#pragma unroll
+              for (int w = 0; w < L::VB / 4; ++w) v[b][i][p][w] = 0;
+          }
+        }
+      }
+      if constexpr (BF) {
+        if (spec) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < L::VP; ++p)
+#pragma unroll
+              for (int w = 0; w < L::VB / 4; ++w) {
+                uint32_t& x = v[b][i][p][w];
+                if ((x & 0x7f80u) == 0x7f80u) { atomicAdd(spec + L::v_channel(g, p * L::VC + 2 * w), bf16_lo(x)); x &= 0xffff0000u; }
+                if ((x & 0x7f800000u) == 0x7f800000u) { atomicAdd(spec + L::v_channel(g, p * L::VC + 2 * w + 1), bf16_hi(x)); x &= 0xffffu; }
+              }
+        }
+      }
+    }
+    auto add = [&](int c, const uint32_t (&f0)[L::TB], const uint32_t (&f1)[L::TB]) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int b = 0; b < L::TB; ++b) {
+        mma<BF>(acc, pa[2 * b][0], pa[2 * b][1], pa[2 * b + 1][0], pa[2 * b + 1][1], f0[b], f1[b]);
+        if constexpr (BF) mma<BF>(acc, pa[2 * b][2], 0u, pa[2 * b + 1][2], 0u, f0[b], f1[b]);
+      }
+      o[c][0] = fmaf(o[c][0], al, acc[0] + acc[2]);
+      o[c][1] = fmaf(o[c][1], al, acc[1] + acc[3]);
+    };
+    uint32_t f[4][L::TB], f2[4][L::TB];
+    if constexpr (KV == KV_BF16) {
+#pragma unroll
+      for (int p = 0; p < L::VP; ++p)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+#pragma unroll
+            for (int b = 0; b < L::TB; ++b) {
+              f[0][b] = __byte_perm(v[b][0][p][w], v[b][1][p][w], odd ? 0x7632 : 0x5410);
+              f2[0][b] = __byte_perm(v[b][2][p][w], v[b][3][p][w], odd ? 0x7632 : 0x5410);
+            }
+            add(8 * p + 2 * w + odd, f[0], f2[0]);
+          }
+    } else if constexpr (KV == KV_E4M3) {
+#pragma unroll
+      for (int w = 0; w < L::VB / 4; ++w)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int b = 0; b < L::TB; ++b) {
+            const uint32_t x = __byte_perm(v[b][0][0][w], v[b][1][0][w], half ? 0x7362 : 0x5140);
+            const uint32_t y = __byte_perm(v[b][2][0][w], v[b][3][0][w], half ? 0x7362 : 0x5140);
+            f[0][b] = e4m3x2_to_h2bits(x); f[1][b] = e4m3x2_to_h2bits(x >> 16);
+            f2[0][b] = e4m3x2_to_h2bits(y); f2[1][b] = e4m3x2_to_h2bits(y >> 16);
+          }
+          add(4 * w + 2 * half, f[0], f2[0]);
+          add(4 * w + 2 * half + 1, f[1], f2[1]);
+        }
+    } else {
+      uint32_t sc[L::TB][2];
+#pragma unroll
+      for (int b = 0; b < L::TB; ++b) { sc[b][0] = e4m3x2_to_h2bits(vs[b][0]); sc[b][1] = e4m3x2_to_h2bits(vs[b][1]); }
+#pragma unroll
+      for (int w = 0; w < L::VB / 4; ++w)
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+#pragma unroll
+          for (int b = 0; b < L::TB; ++b) {
+            uint32_t x[4], y[4];
+            auto pairs = [&](uint32_t p, uint32_t q) {
+              return odd ? ((p >> 4) & 0x0f0f0f0fu) | (q & 0xf0f0f0f0u) : (p & 0x0f0f0f0fu) | ((q << 4) & 0xf0f0f0f0u);
+            };
+            e2m1x8_to_h2(pairs(v[b][0][0][w], v[b][1][0][w]), x);
+            e2m1x8_to_h2(pairs(v[b][2][0][w], v[b][3][0][w]), y);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) { f[c][b] = hmul2(x[c], sc[b][0]); f2[c][b] = hmul2(y[c], sc[b][1]); }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) add(8 * w + 2 * c + odd, f[c], f2[c]);
+        }
+    }
+  }
+
+  // The warp's state to shared memory: so [head][D], sm_m and sm_l [head].
+  __device__ __forceinline__ void leave(float* so, float* sm_m, float* sm_l, const float* spec, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    if (t == 0) { sm_m[g] = m; sm_l[g] = l; }
+#pragma unroll
+    for (int c = 0; c < L::NT; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int ch = L::v_channel(2 * t + e, c);
+        so[g * D + ch] = spec ? o[c][e] + spec[ch] : o[c][e];
+      }
+  }
+};
+
+// One cluster of 1..8 CTAs per (row, KV head, group of eight query heads); its
+// warps take the row's blocks in turn and the CTAs' parts merge through
+// distributed shared memory. One launch, no scratch.
+template <int D, int KV>
+__global__ void __launch_bounds__(32 * kBaWarps, kBaPerSm / kBaWarps) block_attention_kernel(const BlockAttnArgs a) {
+  using L = Lay<D, KV>;
+  constexpr bool BF = L::BF;
+  __shared__ __align__(16) uint4 frag[L::KS * 32];
+  __shared__ __align__(16) uint2 frag_lo[BF ? L::KS * 32 : 1];
+  __shared__ __align__(16) float so[kBaWarps * kBaHeads * D];         // [warp][head][D]
+  __shared__ float sm_m[kBaWarps][kBaHeads], sm_l[kBaWarps][kBaHeads], cta_m[kBaHeads], cta_l[kBaHeads], sm_fac[kBaHeads];
+  __shared__ float sm_spec[BF ? kBaWarps : 1][BF ? D : 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int sp = (int)(blockIdx.x % (unsigned)a.cluster), pair = (int)(blockIdx.x / (unsigned)a.cluster);
+  const int hb = pair % a.hblocks, h = pair / a.hblocks % a.nkv, row = pair / a.hblocks / a.nkv;
+  const int G = a.nq / a.nkv, gn = min(kBaHeads, G - hb * kBaHeads);
+  const size_t head0 = (size_t)row * a.nq + (size_t)h * G + hb * kBaHeads;
+  const int g = lane >> 2, t = lane & 3;
+
+  Picks pk;
+  const int pos = a.positions[row], seq = a.row_seq ? a.row_seq[row] : row;
+  pk.sel = a.sel + ((size_t)row * a.nkv + h) * a.k;
+  pk.k = a.k;
+  pk.stride = a.cluster * warps;
+  const int first = sp * warps + warp + lane * pk.stride;
+  pk.at = first;
+  pk.e2 = pk.entry();
+  float x[D / 4];                                                     // head g's channels of this lane
+#pragma unroll
+  for (int i = 0; i < D / 4; i += 4) {
+    const float4 q = g < gn ? __ldg(reinterpret_cast<const float4*>(a.q + (head0 + g) * D + L::q_channel(t, i)))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[i] = q.x; x[i + 1] = q.y; x[i + 2] = q.z; x[i + 3] = q.w;
+  }
+  const bool ok = pos >= 0 && pos / kBlockTokens < a.bt_stride && seq >= 0 && seq < a.nseq;
+  if (!ok && tid == 0 && sp == 0 && h == 0 && hb == 0) set_err(a.err, MBT_DEV_POS_RANGE);
+  pk.last = ok ? pos / kBlockTokens : -1;
+  if (!ok) { pk.at = pk.k; pk.e2 = -1; }                              // no entry counts
+  pk.table = a.bt + (size_t)(ok ? seq : 0) * a.bt_stride;
+  pk.num_blocks = a.num_blocks;
+  pk.err = a.err;
+  pk.mask = 0;
+  const unsigned char* kpool = reinterpret_cast<const unsigned char*>(a.kpool);
+  const unsigned char* vpool = reinterpret_cast<const unsigned char*>(a.vpool);
+  BlockWarp<D, KV> w;
+  int blk[L::TB], live[L::TB];
+  bool more = pk.any();
+  auto take = [&]() {
+#pragma unroll
+    for (int b = 0; b < L::TB; ++b) pk.take(blk[b], live[b], pos);
+  };
+  if (more) {
+    take();
+    w.load_k(kpool, blk, a.nkv, h, lane);
+    w.load_v(vpool, blk, a.nkv, h, lane);
+  }
+
+  // The queries' fragments, while the first blocks are under way. A power of two
+  // per head brings the largest into FP16's range, or (BF16) a tiny one away from
+  // the smallest numbers; `fac` takes scores back to the log2 domain.
+  uint32_t big = 0;                                                   // largest magnitude's bits; a NaN's are larger than inf's
+#pragma unroll
+  for (int i = 0; i < D / 4; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
+  big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+  const int ex = (int)(big >> 23), e = BF ? (ex < 87 ? min(120, 127 - ex) : 0) : min(120, 140 - ex);
+  const float up = __int_as_float((e + 127) << 23);
+  float fac = 1.4426950408889634f / sqrtf((float)D) * a.k_scale * __int_as_float((127 - e) << 23);
+  fac = fmaxf(fac, 1.2e-38f);                                         // masked scores (-inf) stay -inf
+  if (big >= 0x7f800000u) fac = __int_as_float(0x7fc00000);           // a non-finite query: its row is NaN
+  if (t == 0) sm_fac[g] = fac;                                        // every warp the same
+#pragma unroll
+  for (int st = 0; st < L::KS; ++st) {
+    uint32_t h0, h1, m0, m1, l0, l1;
+    split<BF>(x[4 * st] * up, x[4 * st + 1] * up, h0, m0, l0);
+    split<BF>(x[4 * st + 2] * up, x[4 * st + 3] * up, h1, m1, l1);
+    if (st % warps == warp) {
+      frag[st * 32 + lane] = make_uint4(h0, m0, h1, m1);
+      if constexpr (BF) frag_lo[st * 32 + lane] = make_uint2(l0, l1);
+    }
+  }
+  __syncthreads();
+
+  float* spec = nullptr;
+  w.start();
+#pragma unroll 1
+  while (true) {
+#pragma unroll 1
+    while (more) {
+      float s[2 * L::TB][2];
+      int now[L::TB];
+      w.scores(s, frag, frag_lo, lane);
+#pragma unroll
+      for (int b = 0; b < L::TB; ++b) now[b] = live[b];
+      more = pk.any();
+      if (more) {
+        take();
+        w.load_k(kpool, blk, a.nkv, h, lane);
+      }
+      w.rest(s, now, fac, spec, lane);
+      if (more) w.load_v(vpool, blk, a.nkv, h, lane);
+    }
+    w.l += __shfl_xor_sync(0xffffffffu, w.l, 1);
+    w.l += __shfl_xor_sync(0xffffffffu, w.l, 2);
+    if constexpr (!BF) break;
+    // BF16 values may be infinite or NaN, and a product with a part that is 0 is
+    // then NaN: such a warp goes through its blocks again and adds them apart.
+    bool odd = false;
+    if (!spec) {
+#pragma unroll
+      for (int c = 0; c < L::NT; ++c) odd |= !(fabsf(w.o[c][0]) <= 3.4e38f) || !(fabsf(w.o[c][1]) <= 3.4e38f);
+      odd = odd && w.l <= 3.4e38f;
+    }
+    if (!__any_sync(0xffffffffu, odd)) break;
+    spec = sm_spec[warp];
+    for (int i = lane; i < D; i += 32) spec[i] = 0.f;
+    __syncwarp();
+    pk.at = first;
+    pk.e2 = pk.entry();
+    pk.mask = 0;
+    w.start();
+    more = pk.any();
+    if (more) {
+      take();
+      w.load_k(kpool, blk, a.nkv, h, lane);
+      w.load_v(vpool, blk, a.nkv, h, lane);
+    }
+  }
+  __syncwarp();
+  w.leave(so + warp * kBaHeads * D, sm_m[warp], sm_l[warp], spec, lane);
+  __syncthreads();
+  // an infinity counts whatever its share
+  auto share = [](float x, float f) { return x * (fabsf(x) > 3.4e38f ? 1.f : f); };
+  for (int i = tid; i < gn * D; i += blockDim.x) {
+    const int hr = i / D;
+    float M = -INFINITY, Ls = 0.f, acc = 0.f;
+    for (int v = 0; v < warps; ++v) M = fmaxf(M, sm_m[v][hr]);
+    const float mu = M == -INFINITY ? 0.f : M;
+    for (int v = 0; v < warps; ++v) {
+      const float f = ex2((sm_m[v][hr] - mu) * sm_fac[hr]);
+      Ls = fmaf(sm_l[v][hr], f, Ls);
+      acc += share(so[v * kBaHeads * D + i], f);
+    }
+    if (a.cluster == 1) {
+      a.out[head0 * D + i] = Ls == 0.f ? 0.f : acc * (a.v_scale / Ls);
+    } else {
+      so[i] = acc;                                                    // of warp 0's part: read by this thread only
+      if (i % D == 0) { cta_m[hr] = M; cta_l[hr] = Ls; }
+    }
+  }
+  if (a.cluster == 1) return;
+  cluster_sync_all();
+  for (int i = sp * blockDim.x + tid; i < gn * D; i += a.cluster * blockDim.x) {
+    float pm[kBaCluster], pl[kBaCluster], po[kBaCluster], M = -INFINITY, Ls = 0.f, acc = 0.f;
+#pragma unroll
+    for (int r = 0; r < kBaCluster; ++r) {
+      const bool in = r < a.cluster;
+      pm[r] = in ? ld_dsmem_f32(&cta_m[i / D], r) : -INFINITY;
+      pl[r] = in ? ld_dsmem_f32(&cta_l[i / D], r) : 0.f;
+      po[r] = in ? ld_dsmem_f32(&so[i], r) : 0.f;
+      M = fmaxf(M, pm[r]);
+    }
+    const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int r = 0; r < kBaCluster; ++r) {
+      const float f = ex2((pm[r] - mu) * sm_fac[i / D]);
+      Ls = fmaf(pl[r], f, Ls);
+      acc += share(po[r], f);
+    }
+    a.out[head0 * D + i] = Ls == 0.f ? 0.f : acc * (a.v_scale / Ls);
+  }
+  cluster_sync_all();                                                 // stay resident until the others have read
+}
+
+template <int D, int KV>
+cudaError_t ba_launch(const BlockAttnArgs& a, cudaStream_t s) {
+  BlockAttnArgs args = a;
+  void* p[] = {&args};
+  const long long grid = (long long)a.n * a.nkv * a.hblocks * a.cluster;
+  return launch_ex((const void*)block_attention_kernel<D, KV>, dim3((unsigned)grid), dim3(32 * a.warps), 0, s, p, false, -1,
+                   a.cluster > 1 ? a.cluster : 0);
 }
 
 }  // namespace
 
-cudaError_t launch_block_attention(const BlockAttnArgs& a, cudaStream_t s) {
-  const long long grid = (long long)a.n * a.nkv;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  auto go = [&](auto kernel) {
-    kernel<<<(unsigned)grid, kBaThreads, 0, s>>>(a);
-    return cudaGetLastError();
-  };
-  if (a.d == 64)
-    return a.kv == KV_BF16 ? go(block_attention_kernel<64, KV_BF16>) : a.kv == KV_E4M3 ? go(block_attention_kernel<64, KV_E4M3>)
-                                                                                       : go(block_attention_kernel<64, KV_FP4>);
-  return a.kv == KV_BF16 ? go(block_attention_kernel<128, KV_BF16>) : a.kv == KV_E4M3 ? go(block_attention_kernel<128, KV_E4M3>)
-                                                                                      : go(block_attention_kernel<128, KV_FP4>);
+cudaError_t launch_block_attention(const BlockAttnArgs& in, int num_sms, cudaStream_t s) {
+  BlockAttnArgs a = in;
+  a.hblocks = (a.nq / a.nkv + kBaHeads - 1) / kBaHeads;
+  const long long pairs = (long long)a.n * a.nkv * a.hblocks;
+  if (pairs * kBaCluster > 0x7fffffffLL || a.k > 0x7fffffff - 32 * kBaWarps * kBaCluster) return cudaErrorInvalidValue;
+  const long long want = std::min<long long>((a.k + 2 * kBaWarps - 1) / (2 * kBaWarps), (long long)kBaPerSm * num_sms / kBaWarps / pairs);
+  a.cluster = (int)std::max<long long>(1, std::min<long long>(kBaCluster, want));
+  a.warps = kBaWarps;
+  const bool wide = a.d == 128;
+  if (a.kv == KV_BF16) return wide ? ba_launch<128, KV_BF16>(a, s) : ba_launch<64, KV_BF16>(a, s);
+  if (a.kv == KV_E4M3) return wide ? ba_launch<128, KV_E4M3>(a, s) : ba_launch<64, KV_E4M3>(a, s);
+  return wide ? ba_launch<128, KV_FP4>(a, s) : ba_launch<64, KV_FP4>(a, s);
 }
 
 }  // namespace mbt

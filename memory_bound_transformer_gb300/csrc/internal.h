@@ -337,7 +337,8 @@ struct BlockAttnArgs {
   int n; const float* q; int nq, nkv, d; int kv; const void* kpool; const void* vpool; float k_scale, v_scale;
   const int* positions; const int* row_seq; int nseq; const int* bt; int bt_stride;
   const int* sel; int k; int num_blocks; float* out; uint32_t* err;
+  int hblocks, cluster, warps;      // set by the launch: groups of eight heads per KV head, CTAs per cluster, warps per CTA
 };
-cudaError_t launch_block_attention(const BlockAttnArgs& a, cudaStream_t s);
+cudaError_t launch_block_attention(const BlockAttnArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace mbt

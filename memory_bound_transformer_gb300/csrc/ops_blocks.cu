@@ -74,7 +74,7 @@ int op_block_attention(int n, const float* q, int nq, int nkv, int d, const void
   a.n = n; a.q = q; a.nq = nq; a.nkv = nkv; a.d = d; a.kv = kv_type(kv_dtype); a.kpool = kpool; a.vpool = vpool;
   a.k_scale = k_scale; a.v_scale = v_scale; a.positions = positions; a.row_seq = row_seq; a.nseq = nseq; a.bt = bt;
   a.bt_stride = bt_stride; a.sel = sel; a.k = k; a.num_blocks = num_blocks; a.out = out; a.err = err;
-  return status(launch_block_attention(a, (cudaStream_t)stream));
+  return status(launch_block_attention(a, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"
