@@ -9,6 +9,8 @@
 // for every key of the block; the right side with the 8-bit codes is an exact
 // integer (|.| < 2^29: P - N <= 2^14, codes <= 127, 128 channels), so that no
 // order of summation can move a block over the border of the chosen ones.
+#include <algorithm>
+
 #include "fp4.cuh"
 #include "internal.h"
 #include "../../include/mbt_ops.h"
@@ -147,9 +149,10 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Key
 // ---------------------------------------------------------------------------
 // choice
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelCluster = 8;
+constexpr int kSelWarps = 16;                // most warps of a CTA
+constexpr int kSelCluster = 8;               // most CTAs of a cluster
+constexpr int kSelShare = MBT_SELECT_MAX_BLOCKS / kSelCluster;   // most blocks of a CTA
+constexpr int kSelLoads = 8;                 // 16-byte loads that a lane has under way
 constexpr int kBins = 256;
 constexpr uint32_t kKept = 0xffffffffu;      // key of a block that is taken in any case; scores' are lower
 
@@ -168,16 +171,35 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// v[0 .. 7] of each lane, to the sums over groups of LANES neighbouring lanes: a
+// lane is left with the sum of the v that its place in the group names (from the
+// highest bit down; with 16 lanes, neighbours have the same). Half of the values
+// change hands in each step.
+template <int LANES>
+__device__ __forceinline__ int group_sums(int (&v)[kSelLoads], int lane) {
+#pragma unroll
+  for (int o = LANES / 2, n = kSelLoads / 2; n >= 1; o >>= 1, n >>= 1) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int mine = lane & o ? v[n + i] : v[i], other = lane & o ? v[i] : v[n + i];
+      v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+    }
+  }
+  if (LANES == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+  return v[0];
+}
+
 // A cluster per (row, KV head); its CTAs take equal runs of the context's blocks
 // and leave their keys in shared memory. The k-th largest key is found by
 // histograms of 256 bins over the range that is left, summed over the cluster.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSelectArgs a) {
+__global__ void __launch_bounds__(32 * kSelWarps) block_select_kernel(const BlockSelectArgs a) {
   constexpr int REC = 2 * D, LANES = REC / 16, PER = 32 / LANES;      // bytes of a range, lanes on one, ranges per load
+  constexpr int BATCH = kSelLoads * PER;                              // ranges per round of loads (32 or 16)
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) uint8_t digit[2][REC];                     // weights' low and high bytes
   __shared__ uint32_t red[kSelWarps][2], hist[2][kBins], sum[kBins + 1], ends[2], found[2], counts[2], per_warp[kSelWarps][2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   const int rank = (int)(blockIdx.x % (unsigned)a.cluster), pair = (int)(blockIdx.x / (unsigned)a.cluster);
   const int h = pair % a.nkv, row = pair / a.nkv, G = a.nq / a.nkv;
   int* sel = a.sel + (size_t)pair * a.k;
@@ -187,23 +209,25 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSe
   const int* table = a.bt + (size_t)max(seq, 0) * a.bt_stride;
   if (seq < 0 && tid == 0 && rank == 0 && h == 0) set_err(a.err, MBT_DEV_POS_RANGE);
   if (held <= a.k) {                                                  // all of them; the cluster's CTAs agree
-    for (int j = rank * kSelThreads + tid; j < a.k; j += a.cluster * kSelThreads) {
+    for (int j = rank * threads + tid; j < a.k; j += a.cluster * threads) {
       if (j < held && (uint32_t)table[j] > (uint32_t)a.num_blocks) set_err(a.err, MBT_DEV_BLOCK_RANGE);
       sel[j] = j < held ? j : -1;
     }
     return;
   }
+  // this CTA's blocks are [j0, j0 + cnt), a warp's 32 at a time
+  const int share = (held + a.cluster - 1) / a.cluster, j0 = min(rank * share, held), cnt = min(share, held - j0);
+  int next = 32 * warp + lane < cnt ? __ldg(table + j0 + 32 * warp + lane) : 0;
 
   // weights: the group's rounded queries
   const float* q = a.q + ((size_t)row * a.nq + (size_t)h * G) * D;
   uint32_t big = 0;
-  for (int i = tid; i < G * D; i += kSelThreads) big = max(big, __float_as_uint(__ldg(q + i)) & 0x7fffffffu);
+  for (int i = tid; i < G * D; i += threads) big = max(big, __float_as_uint(__ldg(q + i)) & 0x7fffffffu);
   big = __reduce_max_sync(0xffffffffu, big);
   if (lane == 0) red[warp][0] = big;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) big = max(big, red[w][0]);
-  for (int i = tid; i < D; i += kSelThreads) {
+  for (int w = 0; w < warps; ++w) big = max(big, red[w][0]);
+  for (int i = tid; i < D; i += threads) {
     int up = 0, down = 0;
     if (big != 0 && big < 0x7f800000u) {
       int x;
@@ -222,30 +246,44 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSe
   const uint4 w0 = *reinterpret_cast<const uint4*>(digit[0] + 16 * l), w1 = *reinterpret_cast<const uint4*>(digit[1] + 16 * l);
   const int side = l < LANES / 2 ? -1 : 1;
 
-  // keys of this CTA's blocks [j0, j0 + cnt)
-  const int share = (held + a.cluster - 1) / a.cluster, j0 = min(rank * share, held), cnt = min(share, held - j0);
   uint32_t lowest = 0xffffffffu, highest = 0;
-  for (int i0 = warp * PER; i0 < cnt; i0 += kSelWarps * PER) {
-    const int i = i0 + lane / LANES, j = j0 + i;
-    int id = i < cnt ? __ldg(table + j) : 0;
+  const unsigned char* ranges = reinterpret_cast<const unsigned char*>(a.bounds) + 16 * l;
+#pragma unroll 1
+  for (int i0 = 32 * warp; i0 < cnt; i0 += 32 * warps) {
+    int id = next;
+    const int ahead = i0 + 32 * warps + lane;
+    next = ahead < cnt ? __ldg(table + j0 + ahead) : 0;
     if ((uint32_t)id > (uint32_t)a.num_blocks) {
       set_err(a.err, MBT_DEV_BLOCK_RANGE);
       id = a.num_blocks;
     }
-    const size_t at = (size_t)id * a.nkv + h;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.bounds + at * REC) + l);
-    const float scale = __ldg(a.scales + at);
-    int lo = dp4a_us(w0.w, v.w, dp4a_us(w0.z, v.z, dp4a_us(w0.y, v.y, dp4a_us(w0.x, v.x, 0))));
-    int hi = dp4a_us(w1.w, v.w, dp4a_us(w1.z, v.z, dp4a_us(w1.y, v.y, dp4a_us(w1.x, v.x, 0))));
-    int dot = side * (hi * 256 + lo);
+    const float scale = __ldg(a.scales + (size_t)id * a.nkv + h);
 #pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (l == 0 && i < cnt) {
-      const float inf = __int_as_float(0x7f800000);
-      uint32_t key = key_of(scale < inf ? (float)dot * scale : inf);
-      if (j < a.keep_first || j >= held - a.keep_last) key = kKept;
-      else { lowest = min(lowest, key); highest = max(highest, key); }
-      keys[i] = key;
+    for (int b = 0; b < 32; b += BATCH) {
+      if (i0 + b >= cnt) break;
+      uint4 v[kSelLoads];
+#pragma unroll
+      for (int u = 0; u < kSelLoads; ++u) {                           // blocks past the share: block 0, not used
+        const int from = __shfl_sync(0xffffffffu, id, b + u * PER + lane / LANES);
+        v[u] = ld_stream(ranges + ((size_t)from * a.nkv + h) * REC);
+      }
+      int dot[kSelLoads];
+#pragma unroll
+      for (int u = 0; u < kSelLoads; ++u) {
+        const int lo = dp4a_us(w0.w, v[u].w, dp4a_us(w0.z, v[u].z, dp4a_us(w0.y, v[u].y, dp4a_us(w0.x, v[u].x, 0))));
+        const int hi = dp4a_us(w1.w, v[u].w, dp4a_us(w1.z, v[u].z, dp4a_us(w1.y, v[u].y, dp4a_us(w1.x, v[u].x, 0))));
+        dot[u] = side * (hi * 256 + lo);
+      }
+      const int total = group_sums<LANES>(dot, lane);
+      const int r = b + (LANES == 16 ? l >> 1 : l) * PER + lane / LANES, i = i0 + r, j = j0 + i;
+      const float sc = __shfl_sync(0xffffffffu, scale, r);
+      if (i < cnt && (LANES == 8 || !(lane & 1))) {
+        const float inf = __int_as_float(0x7f800000);
+        uint32_t key = key_of(sc < inf ? (float)total * sc : inf);
+        if (j < a.keep_first || j >= held - a.keep_last) key = kKept;
+        else { lowest = min(lowest, key); highest = max(highest, key); }
+        keys[i] = key;
+      }
     }
   }
 
@@ -253,10 +291,10 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSe
   lowest = __reduce_min_sync(0xffffffffu, lowest);
   highest = __reduce_max_sync(0xffffffffu, highest);
   if (lane == 0) { red[warp][0] = lowest; red[warp][1] = highest; }
-  for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = hist[1][i] = 0;
+  for (int i = tid; i < kBins; i += threads) hist[0][i] = hist[1][i] = 0;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 0; w < kSelWarps; ++w) { lowest = min(lowest, red[w][0]); highest = max(highest, red[w][1]); }
+    for (int w = 0; w < warps; ++w) { lowest = min(lowest, red[w][0]); highest = max(highest, red[w][1]); }
     ends[0] = lowest; ends[1] = highest;
   }
   cluster_sync_all();
@@ -272,15 +310,17 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSe
     uint32_t* mine = hist[turn & 1];
     const int shift = max(bits - 8, 0);
     const uint32_t top = bits >= 32 ? 0xffffffffu : (1u << bits) - 1;
-    for (int i = tid; i < cnt; i += kSelThreads) {
+    for (int i = tid; i < cnt; i += threads) {
       const uint32_t off = keys[i] - base;
       if (keys[i] != kKept && keys[i] >= base && off <= top) atomicAdd(&mine[off >> shift], 1u);
     }
     cluster_sync_all();
     uint32_t n = 0;
-    for (int r = 0; r < a.cluster; ++r) n += ld_dsmem_u32(&mine[tid], r);
-    hist[(turn + 1) & 1][tid] = 0;                                    // read by all before this turn's barrier
-    sum[tid] = n;
+    if (tid < kBins) {
+      for (int r = 0; r < a.cluster; ++r) n += ld_dsmem_u32(&mine[tid], r);
+      hist[(turn + 1) & 1][tid] = 0;                                  // read by all before this turn's barrier
+      sum[tid] = n;
+    }
     __syncthreads();
     if (warp == 0) {                                                  // counts from the highest bin down
       uint32_t c[kBins / 32], t = 0;
@@ -317,7 +357,7 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSe
     if (none || key < base) return 0;
     return key - base > span ? 2 : 1;
   };
-  const int seg = (cnt + kSelThreads - 1) / kSelThreads * 32;         // a warp's run of keys
+  const int seg = (cnt + threads - 1) / threads * 32;         // a warp's run of keys
   const int s0 = min(warp * seg, cnt), s1 = min(s0 + seg, cnt);
   uint32_t sure = 0, tied = 0;
   for (int i = s0; i < s1; i += 32) {
@@ -329,7 +369,7 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSe
   __syncthreads();
   if (tid == 0) {
     counts[0] = counts[1] = 0;
-    for (int w = 0; w < kSelWarps; ++w) { counts[0] += per_warp[w][0]; counts[1] += per_warp[w][1]; }
+    for (int w = 0; w < warps; ++w) { counts[0] += per_warp[w][0]; counts[1] += per_warp[w][1]; }
   }
   cluster_sync_all();
   uint32_t sure_before = 0, tied_before = 0;
@@ -363,21 +403,26 @@ cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t s) {
 cudaError_t block_select_init() {
   for (const void* f : {(const void*)block_select_kernel<64>, (const void*)block_select_kernel<128>}) {
     const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               MBT_SELECT_MAX_BLOCKS / kSelCluster * 4);
+                                               kSelShare * 4);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-cudaError_t launch_block_select(const BlockSelectArgs& a, cudaStream_t s) {
+cudaError_t launch_block_select(const BlockSelectArgs& a, int num_sms, cudaStream_t s) {
   BlockSelectArgs args = a;
-  args.cluster = kSelCluster;
-  const long long grid = (long long)a.n * a.nkv * args.cluster;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long pairs = (long long)a.n * a.nkv;
+  if (pairs * kSelCluster > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // four CTAs of eight warps per SM; no CTA with less than 32 blocks of a full table per warp
+  const long long want = std::min<long long>((a.bt_stride + 255) / 256, 4LL * num_sms / pairs);
+  args.cluster = (int)std::max<long long>(want, (a.bt_stride + kSelShare - 1) / kSelShare);
+  args.cluster = std::max(1, std::min(args.cluster, kSelCluster));
+  const int share = (a.bt_stride + args.cluster - 1) / args.cluster;
+  const int warps = share > 2048 ? kSelWarps : 8;
   void* p[] = {&args};
-  const size_t smem = (size_t)((a.bt_stride + args.cluster - 1) / args.cluster) * 4;
   return launch_ex(a.d == 64 ? (const void*)block_select_kernel<64> : (const void*)block_select_kernel<128>,
-                   dim3((unsigned)grid), dim3(kSelThreads), smem, s, p, false, -1, args.cluster);
+                   dim3((unsigned)(pairs * args.cluster)), dim3(32 * warps), (size_t)share * 4, s, p, false, -1,
+                   args.cluster > 1 ? args.cluster : 0);
 }
 
 }  // namespace mbt

@@ -56,7 +56,7 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
   a.n = n; a.q = q; a.nq = nq; a.nkv = nkv; a.d = d; a.bounds = bounds; a.scales = scales; a.positions = positions;
   a.row_seq = row_seq; a.nseq = nseq; a.bt = bt; a.bt_stride = bt_stride; a.num_blocks = num_blocks;
   a.keep_first = keep_first; a.keep_last = keep_last; a.k = k; a.sel = sel; a.err = err;
-  return status(launch_block_select(a, (cudaStream_t)stream));
+  return status(launch_block_select(a, sms, (cudaStream_t)stream));
 }
 
 int op_block_attention(int n, const float* q, int nq, int nkv, int d, const void* kpool, const void* vpool, int kv_dtype,
