@@ -282,7 +282,7 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
  * of sequence row_seq[i] (NULL: sequence i, nseq >= n) of bt [nseq][bt_stride].
  * A row whose position or sequence is outside the table sets MBT_DEV_POS_RANGE;
  * an out-of-range block id sets MBT_DEV_BLOCK_RANGE. They keep nothing between
- * calls and use no scratch memory. */
+ * calls, and but for op_block_select's long tables use no scratch memory. */
 
 /* op_kv_extend: block tables and row layout for a step's new tokens, from the
  * sequences' lengths ("Kernels, Fusion & CUDA Graphs", "The serving engine's
@@ -327,8 +327,9 @@ int op_key_bounds(int n, const int32_t* positions, const int32_t* row_seq, int n
                   int nkv, int d, const void* kpool, int kv_dtype, int num_blocks, int8_t* bounds, float* scales,
                   uint32_t* err, void* stream);
 
-/* Widest table (blocks per sequence) that op_block_select takes. */
-#define MBT_SELECT_MAX_BLOCKS (1 << 18)
+/* op_block_select_scratch: bytes of scratch that op_block_select works in for
+ * these sizes on the current device; 0 up to tables of 4096 blocks. */
+size_t op_block_select_scratch(int n, int nkv, int bt_stride, int k);
 
 /* op_block_select: per row and KV head the k blocks of the row's context (tokens
  * 0 .. positions[i]) that can hold the largest scores. Over the group's query
@@ -345,11 +346,13 @@ int op_key_bounds(int n, const int32_t* positions, const int32_t* row_seq, int n
  * earlier block. sel [n][nkv][k] int32: the taken blocks' places in the table,
  * ascending, then -1 where the context has fewer than k blocks. q [n][nq][d]
  * fp32. An out-of-range id counts with the null block's range; a row outside
- * its table gets -1 throughout. MBT_ERR_UNSUPPORTED for bt_stride above
- * MBT_SELECT_MAX_BLOCKS. */
+ * its table gets -1 throughout. scratch (device, 16-byte aligned) has at least
+ * op_block_select_scratch(..) bytes, or the call returns MBT_ERR_SCRATCH; calls
+ * that may overlap need one each. NULL: taken from the stream-ordered allocator. */
 int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t* bounds, const float* scales,
                     const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
-                    int num_blocks, int keep_first, int keep_last, int k, int32_t* sel, uint32_t* err, void* stream);
+                    int num_blocks, int keep_first, int keep_last, int k, int32_t* sel, void* scratch, size_t scratch_bytes,
+                    uint32_t* err, void* stream);
 
 /* op_block_attention: softmax attention of n rows over selected blocks of the
  * cache: out[i][h] = sum_t softmax_t(q[i][h] . K_t / sqrt(d)) V_t over the tokens

@@ -67,7 +67,8 @@ SIGNATURES = {
     "op_prompt_attention": (_I, [_I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _F, _F, _P, _I, _I, _P, _P, _P]),
     "op_kv_extend": (_I, [_I, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
     "op_key_bounds": (_I, [_I, _P, _P, _I, _P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P]),
-    "op_block_select": (_I, [_I, _P, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "op_block_select_scratch": (_Z, [_I, _I, _I, _I]),
+    "op_block_select": (_I, [_I, _P, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _Z, _P, _P]),
     "op_block_attention": (_I, [_I, _P, _I, _I, _I, _P, _P, _I, _F, _F, _P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P]),
 }
 
@@ -560,10 +561,19 @@ def op_key_bounds(positions, bt, kpool, nkv, d, kv_dtype, num_blocks, bounds, sc
         _tensor(fn, "scales", scales, dev, torch.float32, (num_blocks + 1, nkv)), _err(fn, err, dev), _stream_of(stream, dev)))
 
 
+SELECT_PLAIN = 4096                                        # tables up to this width need no scratch
+
+
+def op_block_select_scratch(n: int, nkv: int, width: int, k: int) -> int:
+    """Bytes of scratch op_block_select works in for n rows, tables of this width and k blocks; 0 for none."""
+    return load().op_block_select_scratch(n, nkv, width, k)
+
+
 def op_block_select(q, nkv, bounds, scales, positions, bt, num_blocks, keep_first, keep_last, sel, row_seq=None, err=None,
-                    stream=None) -> None:
+                    stream=None, scratch=None) -> None:
     """The blocks with the largest possible scores per row and KV head: q [n][nq][d] fp32, bounds and scales as
-    op_key_bounds leaves them, sel [n][nkv][k] int32 (ascending places in the table, then -1)."""
+    op_key_bounds leaves them, sel [n][nkv][k] int32 (ascending places in the table, then -1). scratch: uint8 device
+    tensor of op_block_select_scratch(n, nkv, width, k) bytes; None takes it from torch's allocator, on the call's stream."""
     fn = "op_block_select"
     n, nq, d = _shape(fn, "q", q, 3)
     dev = _device(fn, "q", q)
@@ -571,13 +581,22 @@ def op_block_select(q, nkv, bounds, scales, positions, bt, num_blocks, keep_firs
     k = _shape(fn, "sel", sel, 3)[2]
     if num_blocks < 1 or keep_first < 0 or keep_last < 1 or keep_first + keep_last > k:   # before ctypes takes 32 bits of them
         raise MbtError(fn, -1)
+    if scratch is None and width > SELECT_PLAIN:
+        on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(on):                        # the allocator's stream order is then the call's
+            scratch = torch.empty(op_block_select_scratch(n, nkv, width, k), dtype=torch.uint8, device=q.device)
+    size = 0
+    if scratch is not None:
+        size, = _shape(fn, "scratch", scratch, 1)
+        _tensor(fn, "scratch", scratch, dev, torch.uint8, (size,))
     _check(fn, load().op_block_select(
         n, _tensor(fn, "q", q, dev, torch.float32, (n, nq, d)), nq, nkv, d,
         _tensor(fn, "bounds", bounds, dev, torch.int8, (num_blocks + 1, nkv, 2, d)),
         _tensor(fn, "scales", scales, dev, torch.float32, (num_blocks + 1, nkv)),
         _tensor(fn, "positions", positions, dev, torch.int32, (n,)), _rows_of(fn, n, row_seq, nseq, dev), nseq,
         _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, num_blocks, keep_first, keep_last, k,
-        _tensor(fn, "sel", sel, dev, torch.int32, (n, nkv, k)), _err(fn, err, dev), _stream_of(stream, dev)))
+        _tensor(fn, "sel", sel, dev, torch.int32, (n, nkv, k)), _ptr(scratch), size, _err(fn, err, dev),
+        _stream_of(stream, dev)))
 
 
 def op_block_attention(q, nkv, kpool, vpool, kv_dtype, k_scale, v_scale, positions, bt, sel, num_blocks, out, row_seq=None,

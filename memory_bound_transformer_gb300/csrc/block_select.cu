@@ -149,24 +149,28 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Key
 // ---------------------------------------------------------------------------
 // choice
 
-constexpr int kSelWarps = 16;                // most warps of a CTA
-constexpr int kSelFew = 8;                   // of one with up to 2048 blocks
-constexpr int kSelLoads = 8;                 // 16-byte loads that a lane has under way
-constexpr int kSelPerSm = 4;                 // such CTAs per SM
+constexpr int kSelWarps = 8;                 // warps of a CTA that chooses from one context
+constexpr int kSelPerSm = 4;                 // such CTAs per SM (64 registers a thread)
 constexpr int kSelCluster = 8;               // most CTAs of a cluster
-constexpr int kSelShare = MBT_SELECT_MAX_BLOCKS / kSelCluster;   // most blocks of a CTA
-constexpr int kSelCollect = 2048;            // blocks up to which one CTA of a cluster chooses
-constexpr int kBins = 256;
-constexpr uint32_t kKept = 0xffffffffu;      // key of a block that is taken in any case; scores' are lower
+constexpr int kSelOne = 4096;                // widest table for which one CTA has all keys
+constexpr int kPartWarps = 16;               // warps of a CTA that scores a part of a long context, two per SM
+constexpr int kPartMost = 8192;              // most blocks of a part
+constexpr int kMergeSmem = 192 << 10;        // shared memory for the candidates of all parts
+constexpr int kSelLoads = 8;                 // 16-byte loads that a lane has under way
+constexpr int kBins = 1024;
+constexpr uint32_t kKept = 0xffffffffu;      // key of a block that is taken in any case; scores' are lower, and not 0
 
+// 16 bytes read once, past L1. Volatile: such loads are issued in a row.
+__device__ __forceinline__ uint4 ld_range(const unsigned char* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
 // Dot product of four unsigned with four signed bytes, added to c.
 __device__ __forceinline__ int dp4a_us(uint32_t u, uint32_t s, int c) {
   int r;
   asm("dp4a.u32.s32 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(s), "r"(c));
   return r;
-}
-__device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
-  return __float_as_uint(ld_dsmem_f32(p, rank));
 }
 __device__ __forceinline__ void st_dsmem_u32(const void* p, uint32_t rank, uint32_t x) {
   uint32_t r;
@@ -201,303 +205,281 @@ __device__ __forceinline__ int group_sums(int (&v)[N], int lane) {
   return v[0];
 }
 
-// A cluster per (row, KV head); its CTAs take equal runs of the context's blocks
-// and leave their keys in shared memory. Histograms of 256 bins over the range
-// that is left, summed over the cluster, narrow down the k-th largest key until at
-// most 32 candidates are left, which are ranked, or a single value, of which the
-// first are taken.
-template <int D, int WARPS, int LOADS>
-__global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) block_select_kernel(const BlockSelectArgs a) {
-  constexpr int REC = 2 * D, LANES = REC / 16, PER = 32 / LANES;      // bytes of a range, lanes on one, ranges per load
-  constexpr int BATCH = LOADS * PER, SAME = LANES / LOADS;            // ranges per round of loads, lanes left with one's sum
-  extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ __align__(16) uint8_t digit[2][REC];                     // weights' low and high bytes
-  __shared__ __align__(16) uint32_t hist[2][kBins], sum[kBins];
-  __shared__ float group[16 * D];                                     // the group's queries
-  __shared__ uint32_t red[kSelWarps][2], per_warp[kSelWarps][2];
-  __shared__ uint32_t ends[2], counts[3], list[2][32];                // read by the cluster
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int warps = WARPS, threads = 32 * WARPS;
-  const int rank = (int)(blockIdx.x % (unsigned)a.cluster), pair = (int)(blockIdx.x / (unsigned)a.cluster);
-  const int h = pair % a.nkv, row = pair / a.nkv, G = a.nq / a.nkv;
-  int* sel = a.sel + (size_t)pair * a.k;
+// A (row, KV head) and its context.
+struct SelRow {
+  int row, h, held;                          // held: blocks of the context, 0 for a row outside its table
+  const int* table;
+  bool bad;
+};
+__device__ __forceinline__ SelRow sel_row(const BlockSelectArgs& a, int pair) {
+  SelRow r;
+  r.h = pair % a.nkv;
+  r.row = pair / a.nkv;
   int pos;
-  const int seq = row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, row, pos);
-  const int held = seq < 0 ? 0 : pos / kBlockTokens + 1;
-  const int* table = a.bt + (size_t)max(seq, 0) * a.bt_stride;
-  if (seq < 0 && tid == 0 && rank == 0 && h == 0) set_err(a.err, MBT_DEV_POS_RANGE);
-  if (held <= a.k) {                                                  // all of them; the cluster's CTAs agree
-    for (int j = rank * threads + tid; j < a.k; j += a.cluster * threads) {
-      if (j < held && (uint32_t)table[j] > (uint32_t)a.num_blocks) set_err(a.err, MBT_DEV_BLOCK_RANGE);
-      sel[j] = j < held ? j : -1;
-    }
-    return;
-  }
-  // Few blocks: all keys go to the first CTA, which does the rest alone.
-  const bool collect = a.cluster > 1 && held <= kSelCollect;
-  if (collect) cluster_arrive();
-  // this CTA's blocks are [j0, j0 + cnt), a warp's 32 at a time
-  const int share = (held + a.cluster - 1) / a.cluster, j0 = min(rank * share, held), cnt = min(share, held - j0);
-  const int l = lane % LANES;
-  const unsigned char* ranges = reinterpret_cast<const unsigned char*>(a.bounds) + 16 * l;
-  auto entry = [&](int i) { return i + lane < cnt ? __ldg(table + j0 + i + lane) : 0; };   // past the share: block 0, not used
-  auto checked = [&](int id) {
-    if ((uint32_t)id <= (uint32_t)a.num_blocks) return id;
-    set_err(a.err, MBT_DEV_BLOCK_RANGE);
-    return a.num_blocks;
-  };
-  uint4 v[LOADS];
-  int i0 = 32 * warp, id = entry(i0), next = entry(i0 + 32 * warps);
-  auto request = [&](int b) {
-#pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-      const int from = __shfl_sync(0xffffffffu, id, b + u * PER + lane / LANES);
-      v[u] = ld_stream(ranges + ((size_t)from * a.nkv + h) * REC);
-    }
-  };
-  id = checked(id);
-  float scale = 0.f;
-  if (i0 < cnt) {
-    scale = __ldg(a.scales + (size_t)id * a.nkv + h);
-  }
+  const int seq = row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, r.row, pos);
+  r.bad = seq < 0;
+  r.held = r.bad ? 0 : pos / kBlockTokens + 1;
+  r.table = a.bt + (size_t)max(seq, 0) * a.bt_stride;
+  return r;
+}
 
-  // weights: the group's rounded queries
+// Shared memory of the scores: the group's queries, then the two bytes of the
+// weights, of -N for the low codes and of P for the high ones.
+template <int D>
+struct SelQuery {
+  float q[16 * D];
+  __align__(16) uint8_t digit[2][2 * D];
+  uint32_t red[kPartWarps];
+};
+
+// Requests the group's queries (nothing depends on where the row is).
+template <int D, int WARPS>
+__device__ __forceinline__ uint32_t load_group(SelQuery<D>& m, const BlockSelectArgs& a, int row, int h) {
+  const int G = a.nq / a.nkv;
   const float* q = a.q + ((size_t)row * a.nq + (size_t)h * G) * D;
   uint32_t big = 0;
-  for (int i = tid; i < G * D; i += threads) {
+  for (int i = threadIdx.x; i < G * D; i += 32 * WARPS) {
     const float x = __ldg(q + i);
-    group[i] = x;
+    m.q[i] = x;
     big = max(big, __float_as_uint(x) & 0x7fffffffu);
   }
+  return big;
+}
+// The weights from them; all threads call it, `big` from load_group.
+template <int D, int WARPS>
+__device__ __forceinline__ void weigh(SelQuery<D>& m, uint32_t big, int G) {
+  const int tid = threadIdx.x, lane = tid & 31;
   big = __reduce_max_sync(0xffffffffu, big);
-  if (lane == 0) red[warp][0] = big;
-  for (int i = tid; i < kBins; i += threads) hist[0][i] = hist[1][i] = 0;
-  if (tid == 0) counts[2] = 0;
+  if (lane == 0) m.red[tid >> 5] = big;
   __syncthreads();
-  big = __reduce_max_sync(0xffffffffu, lane < warps ? red[lane][0] : 0);
+  big = __reduce_max_sync(0xffffffffu, lane < WARPS ? m.red[lane] : 0);
   int e;
   frexpf(__uint_as_float(big), &e);
   // 2^(10 - e) in two factors that fp32 holds; rint takes care of what is too small for it
   const float m1 = ldexpf(1.f, (10 - e) / 2), m2 = ldexpf(1.f, (10 - e) - (10 - e) / 2);
-  for (int i = tid; i < D; i += threads) {
+  for (int i = tid; i < D; i += 32 * WARPS) {
     int up = 0, down = 0;
     if (big != 0 && big < 0x7f800000u) {
       for (int g = 0; g < G; ++g) {
-        const int u = (int)rintf(group[g * D + i] * m1 * m2);
+        const int u = (int)rintf(m.q[g * D + i] * m1 * m2);
         up += max(u, 0);
         down += max(-u, 0);
       }
     }
-    digit[0][i] = (uint8_t)down; digit[1][i] = (uint8_t)(down >> 8);
-    digit[0][D + i] = (uint8_t)up; digit[1][D + i] = (uint8_t)(up >> 8);
+    m.digit[0][i] = (uint8_t)down; m.digit[1][i] = (uint8_t)(down >> 8);
+    m.digit[0][D + i] = (uint8_t)up; m.digit[1][D + i] = (uint8_t)(up >> 8);
   }
   __syncthreads();
-  const uint4 w0 = *reinterpret_cast<const uint4*>(digit[0] + 16 * l), w1 = *reinterpret_cast<const uint4*>(digit[1] + 16 * l);
-  const int side = l < LANES / 2 ? -1 : 1;
+}
 
-  if (collect) cluster_wait();
+// Keys of the context's blocks [j0, j0 + cnt), 32 at a time per warp: a range is
+// read by 16 or 8 neighbouring lanes. put(place, key).
+template <int D, int WARPS, class Put>
+__device__ __forceinline__ void score_blocks(const SelQuery<D>& m, const BlockSelectArgs& a, const SelRow& w, int j0, int cnt, Put put) {
+  constexpr int REC = 2 * D, LANES = REC / 16, PER = 32 / LANES;      // bytes of a range, lanes on one, ranges per load
+  constexpr int BATCH = kSelLoads * PER, SAME = LANES / kSelLoads;    // ranges per round of loads, lanes left with one's sum
+  const int lane = threadIdx.x & 31, l = lane % LANES, side = l < LANES / 2 ? -1 : 1;
+  const unsigned char* ranges = reinterpret_cast<const unsigned char*>(a.bounds) + 16 * l;
+  const uint4 w0 = *reinterpret_cast<const uint4*>(m.digit[0] + 16 * l), w1 = *reinterpret_cast<const uint4*>(m.digit[1] + 16 * l);
+  int i0 = 32 * (threadIdx.x >> 5);
+  auto entry = [&](int i) { return i + lane < cnt ? __ldg(w.table + j0 + i + lane) : 0; };   // past the end: block 0, not used
+  int next = entry(i0);
 #pragma unroll 1
-  while (i0 < cnt) {
-    const float scale_now = scale;
-    const int ahead = i0 + 32 * warps;
+  for (; i0 < cnt; i0 += 32 * WARPS) {
+    int id = next;
+    next = entry(i0 + 32 * WARPS);
+    if ((uint32_t)id > (uint32_t)a.num_blocks) {
+      set_err(a.err, MBT_DEV_BLOCK_RANGE);
+      id = a.num_blocks;
+    }
+    const float scale = __ldg(a.scales + (size_t)id * a.nkv + w.h);
 #pragma unroll
     for (int b = 0; b < 32; b += BATCH) {
       if (i0 + b >= cnt) break;
-      request(b);
-      int dot[LOADS];
+      uint4 v[kSelLoads];
 #pragma unroll
-      for (int u = 0; u < LOADS; ++u) {
+      for (int u = 0; u < kSelLoads; ++u) {
+        const int from = __shfl_sync(0xffffffffu, id, b + u * PER + lane / LANES);
+        v[u] = ld_range(ranges + ((size_t)from * a.nkv + w.h) * REC);
+      }
+      int dot[kSelLoads];
+#pragma unroll
+      for (int u = 0; u < kSelLoads; ++u) {
         const int lo = dp4a_us(w0.w, v[u].w, dp4a_us(w0.z, v[u].z, dp4a_us(w0.y, v[u].y, dp4a_us(w0.x, v[u].x, 0))));
         const int hi = dp4a_us(w1.w, v[u].w, dp4a_us(w1.z, v[u].z, dp4a_us(w1.y, v[u].y, dp4a_us(w1.x, v[u].x, 0))));
         dot[u] = side * (hi * 256 + lo);
       }
-      const int total = group_sums<LANES, LOADS>(dot, lane);
+      const int total = group_sums<LANES, kSelLoads>(dot, lane);
       const int r = b + l / SAME * PER + lane / LANES, i = i0 + r, j = j0 + i;
-      const float sc = __shfl_sync(0xffffffffu, scale_now, r);
+      const float sc = __shfl_sync(0xffffffffu, scale, r);
       if (i < cnt && l % SAME == 0) {
         const float inf = __int_as_float(0x7f800000);
-        const bool kept = j < a.keep_first || j >= held - a.keep_last;
-        const uint32_t key = kept ? kKept : key_of(sc < inf ? (float)total * sc : inf);
-        if (collect) st_dsmem_u32(keys + j, 0, key);
-        else keys[i] = key;
+        put(i, j < a.keep_first || j >= w.held - a.keep_last ? kKept : key_of(sc < inf ? (float)total * sc : inf));
       }
     }
-    i0 = ahead;
-    if (ahead < cnt) {
-      id = checked(next);
-      next = entry(ahead + 32 * warps);
-      scale = __ldg(a.scales + (size_t)id * a.nkv + h);
-    }
   }
+}
 
-  // From here on: the CTA's keys [0, n) of the blocks from `origin` on.
-  int n = cnt, origin = j0;
-  bool solo = a.cluster == 1;
-  if (collect) {
-    cluster_sync_all();
-    if (rank) return;
-    n = held;
-    origin = 0;
-    solo = true;
-  } else {
-    __syncthreads();
+// Adds one to bin off >> shift where off <= span.
+__device__ __forceinline__ void count_in(uint32_t* bins, uint32_t off, uint32_t span, int shift) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(bins + (off >> shift));
+  asm volatile("{\n .reg .pred p;\n setp.le.u32 p, %1, %2;\n @p red.shared.add.u32 [%0], 1;\n}\n" ::"r"(at), "r"(off), "r"(span) : "memory");
+}
+
+// The bin that holds the need-th of all counted ones from the highest bin down,
+// its count, and the count above it. Every warp calls it for itself.
+__device__ __forceinline__ void find_bin(const uint32_t* bins, uint32_t need, int lane, uint32_t& bin, uint32_t& in_bin, uint32_t& above) {
+  constexpr int N = kBins / 128;                                      // groups of 128 bins, four to a lane
+  uint4 c[N];
+  uint32_t total[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) c[i] = *reinterpret_cast<const uint4*>(bins + 128 * i + 4 * lane);
+#pragma unroll
+  for (int i = 0; i < N; ++i) total[i] = __reduce_add_sync(0xffffffffu, c[i].x + c[i].y + c[i].z + c[i].w);
+  uint4 v = c[0];
+  uint32_t before = 0;
+  int group = 0;
+  bool done = false;
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) {
+    if (!done && before + total[i] >= need) {
+      done = true;
+      group = i;
+      v = c[i];
+    }
+    if (!done) before += total[i];
   }
+  const uint32_t s = v.x + v.y + v.z + v.w;
+  uint32_t upto = s;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_down_sync(0xffffffffu, upto, o);
+    if (lane + o < 32) upto += u;
+  }
+  before += upto - s;
+  const int owner = __ffs(__ballot_sync(0xffffffffu, before < need && need <= before + s)) - 1;
+  const uint32_t q[4] = {v.w, v.z, v.y, v.x};
+  uint32_t b = 0, n = 0, up = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (before < need && need <= before + q[i]) { b = 128 * group + 4 * lane + 3 - i; n = q[i]; up = before; }
+    before += q[i];
+  }
+  bin = __shfl_sync(0xffffffffu, b, owner);
+  in_bin = __shfl_sync(0xffffffffu, n, owner);
+  above = __shfl_sync(0xffffffffu, up, owner);
+}
+
+// Shared memory of the choice.
+struct Chooser {
+  __align__(16) uint32_t hist[2][kBins];
+  uint32_t red[kPartWarps][3], list[2][32], listed;
+};
+__device__ __forceinline__ void clear(Chooser& m, int threads) {      // before the first barrier ahead of choose()
+  for (int i = threadIdx.x; i < kBins / 2; i += threads) reinterpret_cast<uint4*>(m.hist)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) m.listed = 0;
+}
+
+// The k largest of n > k keys get(i), of equal ones the first; keys kKept are
+// among them, and at most k. put(place among the taken, i), in order. Histograms
+// over the range that is left narrow down the k-th largest until at most 32
+// candidates are left, which are ranked, or a single value, of which the first are
+// taken. All threads call it.
+template <int WARPS, class Get, class Put>
+__device__ __forceinline__ void choose(Chooser& m, int n, int k, Get get, Put put) {
+  constexpr int threads = 32 * WARPS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seg = (n + threads - 1) / threads * 32;                   // a warp's run of keys, eight times 32 at a time
   const int s0 = min(warp * seg, n), s1 = min(s0 + seg, n);
-  auto eight = [&](int i, uint32_t (&k8)[8]) {                        // keys past the run read as 0, below all scores'
+  auto eight = [&](int i, uint32_t (&k8)[8]) {                        // keys past the run read as 0
 #pragma unroll
-    for (int u = 0; u < 8; ++u) k8[u] = i + 32 * u + lane < s1 ? keys[i + 32 * u + lane] : 0;
+    for (int u = 0; u < 8; ++u) k8[u] = i + 32 * u + lane < s1 ? get(i + 32 * u + lane) : 0;
   };
-
-  // the range of keys
-  uint32_t lowest = 0xffffffffu, highest = 0;
-  for (int i = s0; i < s1; i += 256) {
-    uint32_t k8[8];
-    eight(i, k8);
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (k8[u] != kKept && k8[u]) { lowest = min(lowest, k8[u]); highest = max(highest, k8[u]); }
-  }
-  lowest = __reduce_min_sync(0xffffffffu, lowest);
-  highest = __reduce_max_sync(0xffffffffu, highest);
-  if (lane == 0) { red[warp][0] = lowest; red[warp][1] = highest; }
-  __syncthreads();
-  lowest = __reduce_min_sync(0xffffffffu, lane < warps ? red[lane][0] : 0xffffffffu);
-  highest = __reduce_max_sync(0xffffffffu, lane < warps ? red[lane][1] : 0);
-  if (!solo) {
-    if (tid == 0) { ends[0] = lowest; ends[1] = highest; }
-    cluster_sync_all();
-    lowest = __reduce_min_sync(0xffffffffu, lane < a.cluster ? ld_dsmem_u32(&ends[0], lane) : 0xffffffffu);
-    highest = __reduce_max_sync(0xffffffffu, lane < a.cluster ? ld_dsmem_u32(&ends[1], lane) : 0);
-  }
-  // The last `need` are to be found among the `left` keys in [base, base + 2^bits);
-  // all above are taken.
-  uint32_t base = lowest, need = a.k - a.keep_first - a.keep_last, left = held - a.keep_first - a.keep_last;
-  int bits = highest > lowest ? 32 - __clz(highest - lowest) : 0;
-  auto below_top = [&](uint32_t key) { return key - base <= (bits >= 32 ? 0xffffffffu : (1u << bits) - 1); };
-#pragma unroll 1
-  for (int turn = 0; bits > 0 && need > 0 && left > 32; ++turn) {
-    uint32_t* mine = hist[turn & 1];
-    const int shift = max(bits - 8, 0);
-    for (int i = s0; i < s1; i += 256) {
-      uint32_t k8[8];
-      eight(i, k8);
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (k8[u] != kKept && k8[u] >= base && below_top(k8[u])) atomicAdd(&mine[(k8[u] - base) >> shift], 1u);
-    }
-    if (solo) __syncthreads();
-    else cluster_sync_all();
-    if (tid < kBins) {
-      if (!solo) {
-        uint32_t c[kSelCluster], t = 0;
-#pragma unroll
-        for (int r = 0; r < kSelCluster; ++r) c[r] = r < a.cluster ? ld_dsmem_u32(&mine[tid], r) : 0;
-#pragma unroll
-        for (int r = 0; r < kSelCluster; ++r) t += c[r];
-        sum[tid] = t;
-      }
-      hist[(turn + 1) & 1][tid] = 0;                                  // read by all before this turn's barrier
-    }
-    if (!solo) __syncthreads();
-    // every warp: counts from the highest bin down
-    const uint4* bins = reinterpret_cast<const uint4*>(solo ? mine : sum) + (31 - lane) * (kBins / 128);
-    const uint4 c1 = bins[0], c0 = bins[1];
-    const uint32_t c[8] = {c0.w, c0.z, c0.y, c0.x, c1.w, c1.z, c1.y, c1.x};
-    uint32_t t = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += c[i];
-    uint32_t before = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += u;
-    }
-    before -= t;
-    const int owner = __ffs(__ballot_sync(0xffffffffu, before < need && need <= before + t)) - 1;
-    uint32_t bin = 0, in_bin = 0, above = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (before < need && need <= before + c[i]) { bin = kBins - 1 - (lane * 8 + i); in_bin = c[i]; above = before; }
-      before += c[i];
-    }
-    need -= __shfl_sync(0xffffffffu, above, owner);
-    base += __shfl_sync(0xffffffffu, bin, owner) << shift;
-    left = __shfl_sync(0xffffffffu, in_bin, owner);
-    bits = shift;
-    if (need == left) break;                                          // all of them
-    __syncthreads();                                                  // the other histogram is clear
-  }
-  // Count the keys above the range (or kept), and list the candidates in it.
-  const bool ranked = left <= 32 && need > 0;
-  auto kind = [&](uint32_t key) {                                     // 2 taken, 1 in the last range, 0 not
-    if (key == kKept) return 2;
-    if (need == 0 || key < base) return 0;
-    return below_top(key) ? 1 : 2;
-  };
-  uint32_t sure = 0, tied = 0;                                        // of this lane, then of the warp
+  // The last `need` are to be found among the `left` keys in [base, top]; all above
+  // are taken. First the range of all keys but 0 and kKept.
+  uint32_t base = 0xffffffffu, top = 0, kept = 0;
   for (int i = s0; i < s1; i += 256) {
     uint32_t k8[8];
     eight(i, k8);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int t = kind(k8[u]);
-      sure += t == 2;
-      tied += t == 1;
-      if (ranked && t == 1) {
-        const uint32_t at = atomicAdd(&counts[2], 1u);
-        list[0][at] = k8[u];
-        list[1][at] = origin + i + 32 * u + lane;
+      base = min(base, k8[u] - 1);
+      top = max(top, k8[u] + 1);
+      kept += k8[u] == kKept;
+    }
+  }
+  base = __reduce_min_sync(0xffffffffu, base);
+  top = __reduce_max_sync(0xffffffffu, top);
+  kept = __reduce_add_sync(0xffffffffu, kept);
+  if (lane == 0) { m.red[warp][0] = base; m.red[warp][1] = top; m.red[warp][2] = kept; }
+  __syncthreads();
+  base = __reduce_min_sync(0xffffffffu, lane < WARPS ? m.red[lane][0] : 0xffffffffu) + 1;
+  top = __reduce_max_sync(0xffffffffu, lane < WARPS ? m.red[lane][1] : 0) - 1;
+  kept = __reduce_add_sync(0xffffffffu, lane < WARPS ? m.red[lane][2] : 0);
+  uint32_t need = k - kept, left = n - kept;
+  if (need == 0) base = top = kKept - 1;                              // no key; only kept ones are above
+#pragma unroll 1
+  for (int turn = 0; need > 0 && left > 32 && base < top; ++turn) {
+    uint32_t* mine = m.hist[turn & 1];
+    const uint32_t span = top - base;
+    const int shift = max(22 - __clz(span), 0);
+    for (int i = s0; i < s1; i += 256) {
+      uint32_t k8[8];
+      eight(i, k8);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) count_in(mine, k8[u] - base, span, shift);
+    }
+    __syncthreads();
+    for (int i = tid; i < kBins; i += threads) m.hist[(turn + 1) & 1][i] = 0;   // read before this turn's barrier
+    uint32_t bin, above;
+    find_bin(mine, need, lane, bin, left, above);
+    need -= above;
+    base += bin << shift;
+    top = min(top, base + ((1u << shift) - 1));
+    if (need == left) break;                                          // all of them
+    __syncthreads();                                                  // the other histogram is clear
+  }
+  __syncthreads();                                                    // `red` has been read by all
+  // Count the keys above the range, and list the candidates in it.
+  const bool ranked = left <= 32 && need > 0;
+  uint32_t sure = 0, tied = 0;
+  for (int i = s0; i < s1; i += 256) {
+    uint32_t k8[8];
+    eight(i, k8);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      sure += k8[u] > top;
+      if (k8[u] - base <= top - base) {
+        ++tied;
+        if (ranked) {
+          const uint32_t at = atomicAdd(&m.listed, 1u);
+          m.list[0][at] = k8[u];
+          m.list[1][at] = i + 32 * u + lane;
+        }
       }
     }
   }
   sure = __reduce_add_sync(0xffffffffu, sure);
   tied = __reduce_add_sync(0xffffffffu, tied);
-  if (lane == 0) { per_warp[warp][0] = sure; per_warp[warp][1] = tied; }
+  if (lane == 0) { m.red[warp][0] = sure; m.red[warp][1] = tied; }
   __syncthreads();
-  const uint32_t ps = lane < warps ? per_warp[lane][0] : 0, pt = lane < warps ? per_warp[lane][1] : 0;
-  uint32_t sure_before = __reduce_add_sync(0xffffffffu, lane < warp ? ps : 0);
-  uint32_t tied_before = __reduce_add_sync(0xffffffffu, lane < warp ? pt : 0);
-  if (!solo) {
-    const uint32_t cs = __reduce_add_sync(0xffffffffu, ps), ct = __reduce_add_sync(0xffffffffu, pt);
-    if (tid == 0) { counts[0] = cs; counts[1] = ct; }
-    cluster_sync_all();
-    sure_before += __reduce_add_sync(0xffffffffu, lane < rank ? ld_dsmem_u32(&counts[0], lane) : 0);
-    tied_before += __reduce_add_sync(0xffffffffu, lane < rank ? ld_dsmem_u32(&counts[1], lane) : 0);
-  }
-  // The last one taken: candidate (key, place), ranked by key, then by place.
-  uint32_t last_key = base, last_j = 0xffffffffu, at = sure_before;
+  uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? m.red[lane][0] : 0);   // taken before this warp's run
+  uint32_t tied_before = __reduce_add_sync(0xffffffffu, lane < warp ? m.red[lane][1] : 0);
+  // Taken are keys above last_key, and those equal to it up to place last_i.
+  const bool cut = !ranked && need < left;                            // equal keys: the first `need`
+  uint32_t last_key = base, last_i = 0xffffffffu;
   if (ranked) {
-    uint32_t first = 0;                                               // of CTA r's candidates
-    int r = 0;
-    if (!solo) {
-      uint32_t upto = lane < a.cluster ? ld_dsmem_u32(&counts[2], lane) : 0;
-#pragma unroll
-      for (int o = 1; o < kSelCluster; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += u;
-      }
-#pragma unroll
-      for (int i = 0; i < kSelCluster - 1; ++i) {
-        const uint32_t u = __shfl_sync(0xffffffffu, upto, i);
-        if (i + 1 < a.cluster && lane >= u) { r = i + 1; first = u; }
-      }
-    }
     const bool in = lane < left;
-    uint32_t key = 0, j = 0;
-    if (in) {
-      key = solo ? list[0][lane] : ld_dsmem_u32(&list[0][lane - first], r);
-      j = solo ? list[1][lane] : ld_dsmem_u32(&list[1][lane - first], r);
-    }
+    const uint32_t key = in ? m.list[0][lane] : 0, i = in ? m.list[1][lane] : 0;
     uint32_t ahead = 0;
-    for (int i = 0; i < (int)left; ++i) {
-      const uint32_t ki = __shfl_sync(0xffffffffu, key, i), ji = __shfl_sync(0xffffffffu, j, i);
-      ahead += ki > key || (ki == key && ji < j);
+    for (int c = 0; c < (int)left; ++c) {
+      const uint32_t kc = m.list[0][c], ic = m.list[1][c];
+      ahead += kc > key || (kc == key && ic < i);
     }
     const int it = __ffs(__ballot_sync(0xffffffffu, in && ahead == need - 1)) - 1;
     last_key = __shfl_sync(0xffffffffu, key, it);
-    last_j = __shfl_sync(0xffffffffu, j, it);
-    at += __popc(__ballot_sync(0xffffffffu, in && ahead < need && j < (uint32_t)(origin + s0)));
+    last_i = __shfl_sync(0xffffffffu, i, it);
+    at += __popc(__ballot_sync(0xffffffffu, in && ahead < need && i < (uint32_t)s0));
   } else {
     at += min(tied_before, need);
   }
@@ -507,21 +489,127 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) block_select_kernel(co
     eight(i, k8);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const uint32_t j = origin + i + 32 * u + lane;
-      const int t = kind(k8[u]);
-      bool one = ranked && (k8[u] > last_key || (k8[u] == last_key && j <= last_j));
-      if (!ranked) {                                                  // equal keys: the first ones
-        const uint32_t m1 = __ballot_sync(0xffffffffu, t == 1);
-        one = tied_before + __popc(m1 & below) < need;
+      const uint32_t j = i + 32 * u + lane;
+      bool same = k8[u] == last_key && j <= last_i;
+      if (cut) {
+        const uint32_t m1 = __ballot_sync(0xffffffffu, same);
+        same = same && tied_before + __popc(m1 & below) < need;
         tied_before += __popc(m1);
       }
-      const bool taken = t == 2 || (t == 1 && one);
-      const uint32_t m = __ballot_sync(0xffffffffu, taken);
-      if (taken) sel[at + __popc(m & below)] = (int)j;
-      at += __popc(m);
+      const bool taken = k8[u] > last_key || same;
+      const uint32_t t = __ballot_sync(0xffffffffu, taken);
+      if (taken) put(at + __popc(t & below), j);
+      at += __popc(t);
     }
   }
-  if (!solo) cluster_sync_all();                                      // stay resident until the others have read
+}
+
+// Contexts of at most kSelOne blocks: a CTA per (row, KV head), or where those are
+// few a cluster that shares the scores and leaves the choice to its first CTA, to
+// whose shared memory the others write their keys.
+template <int D>
+__global__ void __launch_bounds__(32 * kSelWarps, kSelPerSm) block_select_kernel(const BlockSelectArgs a) {
+  constexpr int threads = 32 * kSelWarps;
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ SelQuery<D> mem;
+  __shared__ Chooser chooser;
+  const int tid = threadIdx.x;
+  const int rank = (int)(blockIdx.x % (unsigned)a.cluster), pair = (int)(blockIdx.x / (unsigned)a.cluster);
+  const uint32_t big = load_group<D, kSelWarps>(mem, a, pair / a.nkv, pair % a.nkv);
+  const SelRow w = sel_row(a, pair);
+  int* sel = a.sel + (size_t)pair * a.k;
+  if (w.bad && tid == 0 && rank == 0 && w.h == 0) set_err(a.err, MBT_DEV_POS_RANGE);
+  if (w.held <= a.k) {                                                // all of them; the cluster's CTAs agree
+    for (int j = rank * threads + tid; j < a.k; j += a.cluster * threads) {
+      if (j < w.held && (uint32_t)w.table[j] > (uint32_t)a.num_blocks) set_err(a.err, MBT_DEV_BLOCK_RANGE);
+      sel[j] = j < w.held ? j : -1;
+    }
+    return;
+  }
+  const bool shared = a.cluster > 1;
+  if (shared) cluster_arrive();
+  const int share = (w.held + a.cluster - 1) / a.cluster, j0 = min(rank * share, w.held), cnt = min(share, w.held - j0);
+  clear(chooser, threads);
+  weigh<D, kSelWarps>(mem, big, a.nq / a.nkv);
+  if (shared) cluster_wait();
+  score_blocks<D, kSelWarps>(mem, a, w, j0, cnt, [&](int i, uint32_t key) {
+    if (shared) st_dsmem_u32(keys + j0 + i, 0, key);
+    else keys[i] = key;
+  });
+  if (shared) {
+    cluster_sync_all();
+    if (rank) return;
+  } else {
+    __syncthreads();
+  }
+  choose<kSelWarps>(chooser, w.held, a.k, [&](int i) { return keys[i]; }, [&](uint32_t at, uint32_t j) { sel[at] = (int)j; });
+}
+
+// Longer ones, in two launches: each CTA scores a part of a context and leaves the
+// k best of it, in order, in memory; then a CTA per (row, KV head) chooses among
+// those. (A context's k best are among its parts' k best, and in the same order.)
+__device__ __forceinline__ int part_blocks(const BlockSelectArgs& a, int held) { return (held + a.parts - 1) / a.parts; }
+
+template <int D>
+__global__ void __launch_bounds__(32 * kPartWarps, 2) block_candidates_kernel(const BlockSelectArgs a) {
+  constexpr int threads = 32 * kPartWarps;
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ SelQuery<D> mem;
+  __shared__ Chooser chooser;
+  const int part = (int)(blockIdx.x % (unsigned)a.parts), pair = (int)(blockIdx.x / (unsigned)a.parts);
+  const uint32_t big = load_group<D, kPartWarps>(mem, a, pair / a.nkv, pair % a.nkv);
+  const SelRow w = sel_row(a, pair);
+  if (w.held <= a.k) return;
+  const int share = part_blocks(a, w.held), j0 = min(part * share, w.held), cnt = min(share, w.held - j0);
+  const int take = min(a.k, share);
+  uint32_t* ck = a.keys + (size_t)pair * a.cand + (size_t)part * take;
+  int* cj = a.places + (size_t)pair * a.cand + (size_t)part * take;
+  clear(chooser, threads);
+  weigh<D, kPartWarps>(mem, big, a.nq / a.nkv);
+  score_blocks<D, kPartWarps>(mem, a, w, j0, cnt, [&](int i, uint32_t key) { keys[i] = key; });
+  __syncthreads();
+  if (cnt <= take) {
+    for (int i = threadIdx.x; i < cnt; i += threads) { ck[i] = keys[i]; cj[i] = j0 + i; }
+    return;
+  }
+  choose<kPartWarps>(chooser, cnt, take, [&](int i) { return keys[i]; },
+                     [&](uint32_t at, uint32_t i) { ck[at] = keys[i]; cj[at] = j0 + (int)i; });
+}
+
+__global__ void __launch_bounds__(32 * kPartWarps) block_merge_kernel(const BlockSelectArgs a) {
+  constexpr int threads = 32 * kPartWarps;
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ Chooser chooser;
+  const int pair = (int)blockIdx.x;
+  const SelRow w = sel_row(a, pair);
+  int* sel = a.sel + (size_t)pair * a.k;
+  if (w.bad && threadIdx.x == 0 && w.h == 0) set_err(a.err, MBT_DEV_POS_RANGE);
+  if (w.held <= a.k) {
+    for (int j = threadIdx.x; j < a.k; j += threads) {
+      if (j < w.held && (uint32_t)w.table[j] > (uint32_t)a.num_blocks) set_err(a.err, MBT_DEV_BLOCK_RANGE);
+      sel[j] = j < w.held ? j : -1;
+    }
+    return;
+  }
+  // every part but the last ones is full, so the candidates are one run
+  const int share = part_blocks(a, w.held), take = min(a.k, share), full = w.held / share;
+  const int n = full * take + min(take, w.held - full * share);
+  const uint32_t* ck = a.keys + (size_t)pair * a.cand;
+  const int* cj = a.places + (size_t)pair * a.cand;
+  clear(chooser, threads);
+  auto put = [&](uint32_t at, uint32_t i) { sel[at] = cj[i]; };
+  if (n * 4LL <= kMergeSmem) {
+    for (int i = threadIdx.x; i < n; i += threads) keys[i] = ck[i];
+    __syncthreads();
+    if (n == a.k) {                                                   // cannot be fewer: the k best are among them
+      for (int i = threadIdx.x; i < n; i += threads) put(i, i);
+      return;
+    }
+    choose<kPartWarps>(chooser, n, a.k, [&](int i) { return keys[i]; }, put);
+  } else {
+    __syncthreads();
+    choose<kPartWarps>(chooser, n, a.k, [&](int i) { return __ldg(ck + i); }, put);
+  }
 }
 
 }  // namespace
@@ -539,28 +627,53 @@ cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t s) {
 }
 
 cudaError_t block_select_init() {
-  for (const void* f : {(const void*)block_select_kernel<64, kSelWarps, kSelLoads>, (const void*)block_select_kernel<128, kSelWarps, kSelLoads>}) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelShare * 4);
+  for (const void* f : {(const void*)block_candidates_kernel<64>, (const void*)block_candidates_kernel<128>}) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kPartMost * 4);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  return cudaFuncSetAttribute((const void*)block_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem);
 }
 
-cudaError_t launch_block_select(const BlockSelectArgs& a, int num_sms, cudaStream_t s) {
-  BlockSelectArgs args = a;
+cudaError_t block_select_plan(BlockSelectArgs* a, int num_sms) {
+  const long long pairs = (long long)a->n * a->nkv, blocks = a->bt_stride;
+  a->cluster = 1;
+  a->parts = 0;
+  a->cand = 0;
+  if (blocks <= kSelOne) {
+    // one wave of CTAs, none with less than 32 blocks of a full table per warp
+    const long long want = std::min((blocks + 32 * kSelWarps - 1) / (32 * kSelWarps), (long long)kSelPerSm * num_sms / pairs);
+    a->cluster = (int)std::max<long long>(1, std::min<long long>(want, kSelCluster));
+    return pairs * a->cluster > 0x7fffffffLL ? cudaErrorInvalidValue : cudaSuccess;
+  }
+  const long long least = (blocks + kPartMost - 1) / kPartMost, most = (blocks + 32 * kPartWarps - 1) / (32 * kPartWarps);
+  a->parts = (int)std::max(least, std::min(most, 2LL * num_sms / pairs));
+  const long long share = (blocks + a->parts - 1) / a->parts;
+  a->cand = a->parts * std::min<long long>(a->k, share);
+  return pairs * a->parts > 0x7fffffffLL ? cudaErrorInvalidValue : cudaSuccess;
+}
+
+size_t block_select_scratch(const BlockSelectArgs& a) {
+  return (size_t)a.n * a.nkv * a.cand * (sizeof(uint32_t) + sizeof(int));
+}
+
+cudaError_t launch_block_select(const BlockSelectArgs& in, void* scratch, cudaStream_t s) {
+  BlockSelectArgs a = in;
+  void* p[] = {&a};
   const long long pairs = (long long)a.n * a.nkv;
-  if (pairs * kSelCluster > 0x7fffffffLL) return cudaErrorInvalidValue;
-  // four CTAs of eight warps per SM; no CTA with less than 32 blocks of a full table per warp
-  const long long want = std::min<long long>((a.bt_stride + 255) / 256, (long long)kSelPerSm * num_sms / pairs);
-  args.cluster = (int)std::max<long long>(want, (a.bt_stride + kSelShare - 1) / kSelShare);
-  args.cluster = std::max(1, std::min(args.cluster, kSelCluster));
-  const int share = (a.bt_stride + args.cluster - 1) / args.cluster;
-  const bool few = share <= 2048;
-  const void* f = a.d == 64 ? few ? (const void*)block_select_kernel<64, kSelFew, kSelLoads> : (const void*)block_select_kernel<64, kSelWarps, kSelLoads>
-                            : few ? (const void*)block_select_kernel<128, kSelFew, kSelLoads> : (const void*)block_select_kernel<128, kSelWarps, kSelLoads>;
-  void* p[] = {&args};
-  return launch_ex(f, dim3((unsigned)(pairs * args.cluster)), dim3(32 * (few ? kSelFew : kSelWarps)),
-                   (size_t)std::max(share, std::min(a.bt_stride, kSelCollect)) * 4, s, p, false, -1, args.cluster > 1 ? args.cluster : 0);
+  if (!a.parts) {
+    const size_t smem = (size_t)a.bt_stride * sizeof(uint32_t);
+    return launch_ex(a.d == 64 ? (const void*)block_select_kernel<64> : (const void*)block_select_kernel<128>,
+                     dim3((unsigned)(pairs * a.cluster)), dim3(32 * kSelWarps), smem, s, p, false, -1, a.cluster > 1 ? a.cluster : 0);
+  }
+  a.keys = (uint32_t*)scratch;
+  a.places = (int*)(a.keys + (size_t)pairs * a.cand);
+  const size_t share = (a.bt_stride + a.parts - 1) / a.parts;
+  const cudaError_t e =
+      launch_ex(a.d == 64 ? (const void*)block_candidates_kernel<64> : (const void*)block_candidates_kernel<128>,
+                dim3((unsigned)(pairs * a.parts)), dim3(32 * kPartWarps), share * sizeof(uint32_t), s, p, false, -1);
+  if (e != cudaSuccess) return e;
+  return launch_ex((const void*)block_merge_kernel, dim3((unsigned)pairs), dim3(32 * kPartWarps),
+                   (size_t)std::min<long long>(a.cand * 4LL, kMergeSmem), s, p, false, -1);
 }
 
 }  // namespace mbt

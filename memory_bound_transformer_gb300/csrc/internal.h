@@ -327,9 +327,13 @@ struct BlockSelectArgs {
   int n; const float* q; int nq, nkv, d; const int8_t* bounds; const float* scales;
   const int* positions; const int* row_seq; int nseq; const int* bt; int bt_stride; int num_blocks;
   int keep_first, keep_last, k; int* sel; uint32_t* err;
-  int cluster;                      // set by the launch: CTAs per (row, KV head)
+  int cluster;                      // CTAs per (row, KV head)
+  int parts; long long cand;        // parts > 0: CTAs per (row, KV head) of a long context, and the candidates they leave
+  uint32_t* keys; int* places;      // those, [n][nkv][cand]
 };
-cudaError_t launch_block_select(const BlockSelectArgs& a, int num_sms, cudaStream_t s);
+cudaError_t block_select_plan(BlockSelectArgs* a, int num_sms);     // sets cluster, parts and cand
+size_t block_select_scratch(const BlockSelectArgs& a);
+cudaError_t launch_block_select(const BlockSelectArgs& a, void* scratch, cudaStream_t s);
 cudaError_t block_select_init();
 
 // Attention of n rows over the blocks sel[n][nkv][k] of their contexts.

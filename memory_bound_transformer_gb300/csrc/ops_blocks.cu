@@ -41,14 +41,23 @@ int op_key_bounds(int n, const int32_t* positions, const int32_t* row_seq, int n
   return status(launch_key_bounds(a, (cudaStream_t)stream));
 }
 
+size_t op_block_select_scratch(int n, int nkv, int bt_stride, int k) {
+  int sms = 0;
+  BlockSelectArgs a = {};
+  a.n = n; a.nkv = nkv; a.bt_stride = bt_stride; a.k = k;
+  if (n < 1 || nkv < 1 || bt_stride < 1 || k < 1 || device_setup(&sms) != MBT_OK || block_select_plan(&a, sms) != cudaSuccess)
+    return 0;
+  return block_select_scratch(a);
+}
+
 int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t* bounds, const float* scales,
                     const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
-                    int num_blocks, int keep_first, int keep_last, int k, int32_t* sel, uint32_t* err, void* stream) {
+                    int num_blocks, int keep_first, int keep_last, int k, int32_t* sel, void* scratch, size_t scratch_bytes,
+                    uint32_t* err, void* stream) {
   if (!rows_ok(n, positions, row_seq, nseq) || !q || !heads_ok(nq, nkv, d) || !bounds || !scales ||
       !table_ok(bt, bt_stride) || num_blocks < 1 || keep_first < 0 || keep_last < 1 ||
-      (long long)keep_first + keep_last > k || !sel || !aligned16(q) || !aligned16(bounds))
+      (long long)keep_first + keep_last > k || !sel || !aligned16(q) || !aligned16(bounds) || !aligned16(scratch))
     return MBT_ERR_BAD_ARG;
-  if (bt_stride > MBT_SELECT_MAX_BLOCKS) return MBT_ERR_UNSUPPORTED;
   int sms = 0;
   const int rc = device_setup(&sms);
   if (rc != MBT_OK) return rc;
@@ -56,7 +65,15 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
   a.n = n; a.q = q; a.nq = nq; a.nkv = nkv; a.d = d; a.bounds = bounds; a.scales = scales; a.positions = positions;
   a.row_seq = row_seq; a.nseq = nseq; a.bt = bt; a.bt_stride = bt_stride; a.num_blocks = num_blocks;
   a.keep_first = keep_first; a.keep_last = keep_last; a.k = k; a.sel = sel; a.err = err;
-  return status(launch_block_select(a, sms, (cudaStream_t)stream));
+  if (block_select_plan(&a, sms) != cudaSuccess) return MBT_ERR_BAD_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  const size_t bytes = block_select_scratch(a);
+  if (!bytes || scratch)
+    return scratch_bytes < bytes ? MBT_ERR_SCRATCH : status(launch_block_select(a, scratch, s));
+  if (cudaMallocAsync(&scratch, bytes, s) != cudaSuccess) return MBT_ERR_OOM;
+  const int done = status(launch_block_select(a, scratch, s));
+  const cudaError_t freed = cudaFreeAsync(scratch, s);
+  return done != MBT_OK ? done : status(freed);
 }
 
 int op_block_attention(int n, const float* q, int nq, int nkv, int d, const void* kpool, const void* vpool, int kv_dtype,

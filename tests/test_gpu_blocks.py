@@ -308,8 +308,43 @@ def test_select_ties(cuda_lib, kinds):
         c.check()
 
 
+@pytest.mark.parametrize("held,k", [(4096, 7), (4097, 4090), (5000, 1), (9000, 700), (40000, 33), (40000, 39999)])
+def test_select_tables_of_two_launches(cuda_lib, held, k):
+    """Contexts shorter than their wide tables, scratch of the caller's and of the allocator's, in a graph too; scratch that is
+    too small is refused."""
+    c = Select(8, 2, 64, [16 * held - 3, 16 * (held // 3) + 1, 40, 1], k, 0, 1, seed=held + k)
+    want, (got, err) = c.want(), c.run()
+    assert err == 0 and np.array_equal(got, want)
+    t = (dev(c.q, torch.float32), dev(c.codes, torch.int8), dev(c.scales, torch.float32), dev(c.pos), dev(c.bt))
+    size = capi.op_block_select_scratch(4, 2, c.bt.shape[1], k)
+    assert (size > 0) == (c.bt.shape[1] > capi.SELECT_PLAIN)
+    own, sel = torch.zeros(max(size, 1), dtype=torch.uint8, device=DEV), dev(np.zeros(want.shape))
+    call = lambda scratch: capi.op_block_select(*t[:1], 2, *t[1:], c.nb, 0, 1, sel, scratch=scratch)
+    call(own)
+    assert np.array_equal(sel.cpu().numpy(), want)
+    if size:
+        with pytest.raises(capi.MbtError) as e:
+            call(own[:size - 1])
+        assert e.value.code == -8
+    args = (4, *(capi._ptr(x) for x in t[:1]), 8, 2, 64, *(capi._ptr(x) for x in t[1:4]), None, 4, capi._ptr(t[4]), c.bt.shape[1],
+            c.nb, 0, 1, k, capi._ptr(sel), None, 0, None, None)
+    sel.zero_()
+    torch.cuda.synchronize()
+    assert cuda_lib.op_block_select(*args) == 0                      # the stream-ordered allocator's, on the default stream
+    torch.cuda.synchronize()
+    assert np.array_equal(sel.cpu().numpy(), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(None)
+    for _ in range(3):
+        sel.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(sel.cpu().numpy(), want)
+
+
 def test_select_widest_table(cuda_lib):
-    """As many blocks as a table may name, few different ones, so most scores are equal."""
+    """A quarter of a million blocks, few different ones, so most scores are equal."""
     c = Select(2, 1, 64, [16 * 40], 5000, 2, 3, seed=3)
     ids = np.random.default_rng(4).integers(0, 40, 1 << 18)
     c.bt, c.pos = ids[None].astype(np.int32), np.array([(16 << 18) - 1])

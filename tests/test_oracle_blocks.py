@@ -115,7 +115,7 @@ EXTEND = dict(nseq=4, ctx=P, new=P, bt=P, bt_stride=3, num_blocks=5, free=P, nfr
 BOUNDS = dict(n=4, positions=P, row_seq=None, nseq=4, bt=P, bt_stride=3, nkv=2, d=64, kpool=P, kv_dtype=0, num_blocks=5,
               bounds=P, scales=P, err=None, stream=None)
 SELECT = dict(n=4, q=P, nq=8, nkv=2, d=64, bounds=P, scales=P, positions=P, row_seq=None, nseq=4, bt=P, bt_stride=3,
-              num_blocks=5, keep_first=1, keep_last=1, k=2, sel=P, err=None, stream=None)
+              num_blocks=5, keep_first=1, keep_last=1, k=2, sel=P, scratch=None, scratch_bytes=0, err=None, stream=None)
 ATTEND = dict(n=4, q=P, nq=8, nkv=2, d=64, kpool=P, vpool=P, kv_dtype=0, k_scale=1.0, v_scale=1.0, positions=P,
               row_seq=None, nseq=4, bt=P, bt_stride=3, sel=P, k=2, num_blocks=5, out=P, err=None, stream=None)
 BAD = {
@@ -131,7 +131,7 @@ BAD = {
         ("n", 0), ("q", None), ("q", ODD), ("nq", 0), ("nq", 7), ("nq", 34), ("nkv", 0), ("d", 80), ("bounds", None),
         ("bounds", ODD), ("scales", None), ("positions", None), ("nseq", 0), ("nseq", 3), ("bt", None), ("bt_stride", 0),
         ("num_blocks", 0), ("keep_first", -1), ("keep_last", 0), ("k", 1), ("k", 0), ("keep_first", 2 ** 31 - 1),
-        ("sel", None)]),
+        ("sel", None), ("scratch", ODD), ("bt_stride", (1 << 26) + 1)]),
     "op_block_attention": (ATTEND, [
         ("n", 0), ("q", None), ("q", ODD), ("nq", 0), ("nq", 7), ("nq", 34), ("nkv", 0), ("d", 256), ("kpool", None),
         ("kpool", ODD), ("vpool", None), ("vpool", ODD), ("kv_dtype", 2), ("kv_dtype", 4), ("k_scale", 0.0),
@@ -148,10 +148,6 @@ def test_refused_arguments(lib, fn, name, value):
     assert name in args
     args[name] = value
     assert getattr(lib, fn)(*args.values()) == -1
-
-
-def test_widest_table(lib):
-    assert lib.op_block_select(*dict(SELECT, bt_stride=(1 << 18) + 1).values()) == -6
 
 
 def test_binding_refuses_host_tensors_and_wide_numbers(lib):
