@@ -64,33 +64,43 @@ __device__ __forceinline__ void key_pairs(const unsigned char* unit, int token, 
 }
 
 constexpr int kBoundsWarps = 8;
+constexpr int kBoundsRows = 64;              // most rows of a CTA
 
-// One row per CTA, its KV heads over the warps. A lane holds eight channels; the
-// lanes of a warp cover 256 / D tokens at a time. Tokens past the row's are
-// replaced by its own.
+// A CTA looks through `rows` neighbouring rows for those that their block is left
+// to, then a warp takes a (block, KV head) at a time: a lane holds eight channels,
+// the lanes cover 256 / D tokens. Tokens past the row's are replaced by its own.
 template <int D, int KV>
 __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const KeyBoundsArgs a) {
   constexpr int LANES = D / 8, TOK = 32 / LANES;
   constexpr bool BF = KV == KV_BF16;
-  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int pos, next;
-  const int seq = row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, row, pos);
-  if (seq < 0) {
-    if (threadIdx.x == 0) set_err(a.err, MBT_DEV_POS_RANGE);
-    return;
+  __shared__ int sm_blk[kBoundsRows], sm_upto[kBoundsRows], sm_count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x * a.rows + tid;
+  if (tid == 0) sm_count = 0;
+  __syncthreads();
+  if (tid < a.rows && row < a.n) {
+    int pos, next;
+    const int seq = row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, row, pos);
+    const bool left = row + 1 < a.n && row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, row + 1, next) == seq &&
+                      next / kBlockTokens == pos / kBlockTokens;      // to the next row
+    if (seq < 0) {
+      set_err(a.err, MBT_DEV_POS_RANGE);
+    } else if (!left) {
+      const int blk = a.bt[(size_t)seq * a.bt_stride + pos / kBlockTokens];
+      if (blk < 0 || blk > a.num_blocks) {
+        set_err(a.err, MBT_DEV_BLOCK_RANGE);
+      } else {
+        const int at = atomicAdd(&sm_count, 1);
+        sm_blk[at] = blk;
+        sm_upto[at] = pos % kBlockTokens;
+      }
+    }
   }
-  if (row + 1 < a.n && row_in_table(a.positions, a.row_seq, a.nseq, a.bt_stride, row + 1, next) == seq &&
-      next / kBlockTokens == pos / kBlockTokens)
-    return;                                                          // the next row's work
-  const int blk = a.bt[(size_t)seq * a.bt_stride + pos / kBlockTokens];
-  if (blk < 0 || blk > a.num_blocks) {
-    if (threadIdx.x == 0) set_err(a.err, MBT_DEV_BLOCK_RANGE);
-    return;
-  }
+  __syncthreads();
   constexpr size_t UNIT = KV == KV_BF16 ? kBlockTokens * D * 2 : KV == KV_E4M3 ? kBlockTokens * D : fp4_unit_bytes(D);
-  const int c = lane % LANES, upto = pos % kBlockTokens;
-  for (int h = warp; h < a.nkv; h += kBoundsWarps) {
-    const size_t at = (size_t)blk * a.nkv + h;
+  const int c = lane % LANES, tasks = sm_count * a.nkv;
+  for (int i = warp; i < tasks; i += kBoundsWarps) {
+    const int upto = sm_upto[i / a.nkv];
+    const size_t at = (size_t)sm_blk[i / a.nkv] * a.nkv + i % a.nkv;
     const unsigned char* unit = reinterpret_cast<const unsigned char*>(a.kpool) + at * UNIT;
     uint32_t lo[4], hi[4];
 #pragma unroll
@@ -614,9 +624,12 @@ __global__ void __launch_bounds__(32 * kPartWarps) block_merge_kernel(const Bloc
 
 }  // namespace
 
-cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t s) {
+cudaError_t launch_key_bounds(const KeyBoundsArgs& in, int num_sms, cudaStream_t s) {
+  KeyBoundsArgs a = in;
+  // all CTAs resident at once, eight per SM: most of a prompt's rows leave their block to the next
+  a.rows = (int)std::min<long long>(kBoundsRows, (a.n + 8LL * num_sms - 1) / (8LL * num_sms));
   auto go = [&](auto kernel) {
-    kernel<<<(unsigned)a.n, 32 * kBoundsWarps, 0, s>>>(a);
+    kernel<<<(unsigned)((a.n + (long long)a.rows - 1) / a.rows), 32 * kBoundsWarps, 0, s>>>(a);
     return cudaGetLastError();
   };
   if (a.d == 64)

@@ -312,6 +312,7 @@ struct KvExtendArgs {
   int nseq; const int* ctx_lens; const int* new_lens; int* bt; int bt_stride; int num_blocks;
   const int* free_blocks; int nfree; const int* free_at; int n;
   int* held; int* cu; int* positions; int* row_seq; int64_t* slots; int* free_next; uint32_t* err;
+  int here;                         // set by the launch: the tables' CTA lays out the rows too
 };
 cudaError_t launch_kv_extend(const KvExtendArgs& a, cudaStream_t s);
 
@@ -319,8 +320,9 @@ cudaError_t launch_kv_extend(const KvExtendArgs& a, cudaStream_t s);
 struct KeyBoundsArgs {
   int n; const int* positions; const int* row_seq; int nseq; const int* bt; int bt_stride; int nkv, d;
   const void* kpool; int kv; int num_blocks; int8_t* bounds; float* scales; uint32_t* err;
+  int rows;                         // set by the launch: rows per CTA
 };
-cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t s);
+cudaError_t launch_key_bounds(const KeyBoundsArgs& a, int num_sms, cudaStream_t s);
 
 // The k blocks of each (row, KV head) whose ranges allow the largest scores.
 struct BlockSelectArgs {

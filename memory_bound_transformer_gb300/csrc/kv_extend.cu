@@ -12,34 +12,35 @@ namespace mbt {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;           // most threads of the tables' CTA, a sequence each
+constexpr int kPlanRows = 4096;              // rows up to which it lays them out itself
 constexpr int kRowThreads = 256;
+constexpr int kRowSeqs = 4096;               // row edges that the rows' CTAs keep in shared memory
 
 __device__ __forceinline__ int blocks_for(long long tokens) { return (int)((tokens + kBlockTokens - 1) / kBlockTokens); }
 
-// Inclusive sum over the CTA's threads; `total` is the last one's. scratch: 33 entries.
-__device__ __forceinline__ long long block_scan(long long v, long long* scratch, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+struct Pair { long long x, y; };
+// Inclusive sums over the CTA's threads; `total` are the last one's. scratch: 32 entries.
+__device__ __forceinline__ Pair block_scan(Pair v, Pair* scratch, Pair& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  auto scan = [&](Pair p) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, p.x, o), y = __shfl_up_sync(0xffffffffu, p.y, o);
+      if (lane >= o) { p.x += x; p.y += y; }
+    }
+    return p;
+  };
+  v = scan(v);
   __syncthreads();
   if (lane == 31) scratch[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    long long w = scratch[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    scratch[lane] = w;
-  }
-  __syncthreads();
-  total = scratch[31];
-  return v + (warp ? scratch[warp - 1] : 0);
+  const Pair w = scan(lane < warps ? scratch[lane] : Pair{0, 0});     // every warp for itself
+  total.x = __shfl_sync(0xffffffffu, w.x, 31);
+  total.y = __shfl_sync(0xffffffffu, w.y, 31);
+  const long long x = __shfl_sync(0xffffffffu, w.x, max(warp - 1, 0)), y = __shfl_sync(0xffffffffu, w.y, max(warp - 1, 0));
+  if (warp) { v.x += x; v.y += y; }
+  return v;
 }
 
 // Last entry of the non-decreasing edge[0 .. n] that is <= x, for edge[0] <= x < edge[n].
@@ -53,71 +54,10 @@ __device__ __forceinline__ int segment_of(const int* edge, int n, int x) {
   return lo;
 }
 
-// One CTA: tables, lengths and row edges, 1024 sequences at a time. What a
-// sequence reads of arrays that may be written in place it reads before.
-__global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvExtendArgs a) {
-  __shared__ long long scratch[33];
-  __shared__ int took_edge[kPlanThreads + 1], sm_seq[kPlanThreads];
-  const int tid = threadIdx.x;
-  const int at0 = *a.free_at;
-  const bool at_ok = at0 >= 0 && at0 <= a.nfree;
-  if (!at_ok && tid == 0) set_err(a.err, MBT_DEV_BLOCK_RANGE);
-  long long needed = 0, asked = 0, rows = 0, taken = 0;
-  if (tid == 0) a.cu[0] = 0;
-  for (int s0 = 0; s0 < a.nseq; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    const bool in = s < a.nseq;
-    const int ctx = in ? a.ctx_lens[s] : 0;
-    int add = in ? a.new_lens[s] : 0;
-    if (ctx < 0 || add < 0 || (long long)ctx + add > (long long)a.bt_stride * kBlockTokens) {
-      set_err(a.err, MBT_DEV_SEQLEN_RANGE);
-      add = 0;
-    }
-    const int have = blocks_for(ctx);
-    int need = add ? blocks_for((long long)ctx + add) - have : 0;
-    long long t0, t1, t2;
-    const long long need_end = needed + block_scan(need, scratch, t0);
-    const long long ask_end = asked + block_scan(add, scratch, t1);
-    needed += t0;
-    asked += t1;
-    if (add && ask_end > a.n) {
-      set_err(a.err, MBT_DEV_POS_RANGE);
-      add = need = 0;
-    } else if (need && (!at_ok || at0 + need_end > a.nfree)) {
-      set_err(a.err, MBT_DEV_BLOCK_RANGE);
-      add = need = 0;
-    }
-    // those that fit need the first blocks of the list: what others ask lies behind
-    const long long row_end = rows + block_scan(add, scratch, t1), took_end = block_scan(need, scratch, t2);
-    if (in) {
-      a.held[s] = ctx + add;
-      a.cu[s + 1] = (int)row_end;
-    }
-    rows += t1;
-    took_edge[tid + 1] = (int)took_end;
-    sm_seq[tid] = have;
-    if (tid == 0) took_edge[0] = 0;
-    __syncthreads();
-    for (int i = tid; i < (int)t2; i += kPlanThreads) {
-      const int q = segment_of(took_edge, kPlanThreads, i), id = a.free_blocks[at0 + taken + i];
-      if (id < 0 || id > a.num_blocks) set_err(a.err, MBT_DEV_BLOCK_RANGE);
-      a.bt[(size_t)(s0 + q) * a.bt_stride + sm_seq[q] + i - took_edge[q]] = id;
-    }
-    taken += t2;
-    __syncthreads();
-  }
-  if (tid == 0) *a.free_next = at0 + (int)taken;
-}
-
-// The packed rows, one per thread.
-__global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const KvExtendArgs a) {
-  const int i = blockIdx.x * kRowThreads + threadIdx.x;
-  if (i >= a.n) return;
-  int seq = a.nseq, pos = 0;
+// Row i of sequence seq (nseq: padding) at position pos.
+__device__ __forceinline__ void lay_row(const KvExtendArgs& a, int i, int seq, int pos) {
   long long slot = (long long)a.num_blocks * kBlockTokens;
-  if (i < a.cu[a.nseq]) {
-    seq = segment_of(a.cu, a.nseq, i);
-    pos = a.held[seq] - a.cu[seq + 1] + i;
+  if (seq < a.nseq) {
     const int blk = a.bt[(size_t)seq * a.bt_stride + pos / kBlockTokens];
     const bool ok = blk >= 0 && blk <= a.num_blocks;
     if (!ok) set_err(a.err, MBT_DEV_BLOCK_RANGE);
@@ -128,14 +68,107 @@ __global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const KvExtendArgs
   a.slots[i] = slot;
 }
 
+// One CTA: tables, lengths and row edges, a sequence per thread at a time, and the
+// rows where they are few. What a sequence reads of arrays that may be written in
+// place it reads before. Bound by latency: the lengths, the free list's entries
+// and the rows' table entries are three round trips, a launch the rest.
+__global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvExtendArgs a) {
+  __shared__ Pair scratch[32];
+  __shared__ int took_edge[kPlanThreads + 1], row_edge[kPlanThreads + 1], sm_have[kPlanThreads], sm_ctx[kPlanThreads];
+  const int tid = threadIdx.x, threads = blockDim.x;
+  pdl_launch_dependents();
+  const int at0 = *a.free_at;
+  const bool at_ok = at0 >= 0 && at0 <= a.nfree;
+  if (!at_ok && tid == 0) set_err(a.err, MBT_DEV_BLOCK_RANGE);
+  long long needed = 0, asked = 0, rows = 0, taken = 0;
+  if (tid == 0) a.cu[0] = took_edge[0] = row_edge[0] = 0;
+  for (int s0 = 0; s0 < a.nseq; s0 += threads) {
+    const int s = s0 + tid;
+    const bool in = s < a.nseq;
+    const int ctx = in ? a.ctx_lens[s] : 0;
+    int add = in ? a.new_lens[s] : 0;
+    if (ctx < 0 || add < 0 || (long long)ctx + add > (long long)a.bt_stride * kBlockTokens) {
+      set_err(a.err, MBT_DEV_SEQLEN_RANGE);
+      add = 0;
+    }
+    const int have = blocks_for(ctx);
+    int need = add ? blocks_for((long long)ctx + add) - have : 0;
+    Pair total;
+    const Pair end = block_scan(Pair{need, add}, scratch, total);     // blocks and rows up to this sequence
+    // those that fit get the first blocks of the list: what others ask lies behind
+    Pair got = end, got_total = total;
+    if (asked + total.y > a.n || !at_ok || at0 + needed + total.x > a.nfree) {
+      if (add && asked + end.y > a.n) {
+        set_err(a.err, MBT_DEV_POS_RANGE);
+        add = need = 0;
+      } else if (need && (!at_ok || at0 + needed + end.x > a.nfree)) {
+        set_err(a.err, MBT_DEV_BLOCK_RANGE);
+        add = need = 0;
+      }
+      got = block_scan(Pair{need, add}, scratch, got_total);
+    }
+    if (in) {
+      a.held[s] = ctx + add;
+      a.cu[s + 1] = (int)(rows + got.y);
+    }
+    took_edge[tid + 1] = (int)got.x;
+    row_edge[tid + 1] = (int)(rows + got.y);
+    sm_have[tid] = have;
+    sm_ctx[tid] = ctx;
+    __syncthreads();
+    for (int i = tid; i < (int)got_total.x; i += threads) {
+      const int q = segment_of(took_edge, threads, i), id = a.free_blocks[at0 + taken + i];
+      if (id < 0 || id > a.num_blocks) set_err(a.err, MBT_DEV_BLOCK_RANGE);
+      a.bt[(size_t)(s0 + q) * a.bt_stride + sm_have[q] + i - took_edge[q]] = id;
+    }
+    __syncthreads();
+    if (a.here) {
+      for (int i = (int)rows + tid; i < (int)(rows + got_total.y); i += threads) {
+        const int q = segment_of(row_edge, threads, i);
+        lay_row(a, i, s0 + q, sm_ctx[q] + i - row_edge[q]);
+      }
+      __syncthreads();
+    }
+    needed += total.x;
+    asked += total.y;
+    rows += got_total.y;
+    taken += got_total.x;
+    if (tid == 0) row_edge[0] = (int)rows;
+  }
+  if (a.here)
+    for (int i = (int)rows + tid; i < a.n; i += threads) lay_row(a, i, a.nseq, 0);
+  if (tid == 0) *a.free_next = at0 + (int)taken;
+}
+
+// The packed rows of a large step, one per thread.
+__global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const KvExtendArgs a) {
+  __shared__ int edge[kRowSeqs + 1];
+  pdl_wait();
+  const bool small = a.nseq <= kRowSeqs;
+  if (small) {
+    for (int s = threadIdx.x; s <= a.nseq; s += kRowThreads) edge[s] = a.cu[s];
+    __syncthreads();
+  }
+  const int* cu = small ? edge : a.cu;
+  const int i = blockIdx.x * kRowThreads + threadIdx.x;
+  if (i >= a.n) return;
+  if (i >= cu[a.nseq]) return lay_row(a, i, a.nseq, 0);
+  const int seq = segment_of(cu, a.nseq, i);
+  lay_row(a, i, seq, a.held[seq] - cu[seq + 1] + i);
+}
+
 }  // namespace
 
-cudaError_t launch_kv_extend(const KvExtendArgs& a, cudaStream_t s) {
-  kv_extend_kernel<<<1, kPlanThreads, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  kv_rows_kernel<<<(unsigned)((a.n + (long long)kRowThreads - 1) / kRowThreads), kRowThreads, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_kv_extend(const KvExtendArgs& in, cudaStream_t s) {
+  KvExtendArgs a = in;
+  void* p[] = {&a};
+  // few sequences or rows: a barrier of few warps. Rows beyond a few per thread go to a grid of their own.
+  const int most = a.nseq > a.n ? a.nseq : a.n, threads = most <= 128 ? 128 : most <= 512 ? 512 : kPlanThreads;
+  a.here = a.n <= kPlanRows;
+  const cudaError_t e = launch_ex((const void*)kv_extend_kernel, dim3(1), dim3(threads), 0, s, p, false, -1);
+  if (e != cudaSuccess || a.here) return e;
+  return launch_pdl((const void*)kv_rows_kernel, dim3((unsigned)((a.n + (long long)kRowThreads - 1) / kRowThreads)),
+                    dim3(kRowThreads), 0, s, p);
 }
 
 }  // namespace mbt

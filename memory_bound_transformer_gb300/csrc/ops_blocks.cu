@@ -34,11 +34,14 @@ int op_key_bounds(int n, const int32_t* positions, const int32_t* row_seq, int n
   if (!rows_ok(n, positions, row_seq, nseq) || !table_ok(bt, bt_stride) || nkv < 1 || (d != 64 && d != 128) || !kpool ||
       !cache_ok(kv_dtype) || num_blocks < 1 || !bounds || !scales || !aligned16(kpool) || !aligned16(bounds))
     return MBT_ERR_BAD_ARG;
+  int sms = 0;
+  const int rc = device_setup(&sms);
+  if (rc != MBT_OK) return rc;
   KeyBoundsArgs a = {};
   a.n = n; a.positions = positions; a.row_seq = row_seq; a.nseq = nseq; a.bt = bt; a.bt_stride = bt_stride; a.nkv = nkv;
   a.d = d; a.kpool = kpool; a.kv = kv_type(kv_dtype); a.num_blocks = num_blocks; a.bounds = bounds; a.scales = scales;
   a.err = err;
-  return status(launch_key_bounds(a, (cudaStream_t)stream));
+  return status(launch_key_bounds(a, sms, (cudaStream_t)stream));
 }
 
 size_t op_block_select_scratch(int n, int nkv, int bt_stride, int k) {
