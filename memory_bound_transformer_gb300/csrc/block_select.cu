@@ -42,33 +42,47 @@ __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b, bool bf) {
   return r;
 }
 
-// Channels 8 c .. 8 c + 7 of a token's key as four 16-bit pairs, exactly: BF16
-// values as they are, e4m3 and 4-bit ones as FP16 (e2m1 * e4m3 has at most six
-// significant bits and lies in FP16's range).
+// Channels 8 c .. 8 c + 7 of a token's key as they lie in the cache, and as four
+// 16-bit pairs, exactly: BF16 values as they are, e4m3 and 4-bit ones as FP16
+// (e2m1 * e4m3 has at most six significant bits and lies in FP16's range).
 template <int D, int KV>
-__device__ __forceinline__ void key_pairs(const unsigned char* unit, int token, int c, uint32_t (&p)[4]) {
-  if constexpr (KV == KV_BF16) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(unit + token * 2 * D + 16 * c));
-    p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
-  } else if constexpr (KV == KV_E4M3) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(unit + token * D + 8 * c));
-    p[0] = e4m3x2_to_h2bits(v.x); p[1] = e4m3x2_to_h2bits(v.x >> 16);
-    p[2] = e4m3x2_to_h2bits(v.y); p[3] = e4m3x2_to_h2bits(v.y >> 16);
-  } else {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(unit + token * (D / 2) + 4 * c));
-    const uint32_t s = __ldg(unit + kBlockTokens * (D / 2) + token * (D / kFp4Group) + c / 2), g = e4m3x2_to_h2bits(s | s << 8);
-    e2m1x8_to_h2(w, p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(p[i]) : "r"(g));
+struct Key8 {
+  uint32_t w[KV == KV_BF16 ? 4 : KV == KV_E4M3 ? 2 : 1], scale;
+  __device__ __forceinline__ void load(const unsigned char* unit, int token, int c) {
+    if constexpr (KV == KV_BF16) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(unit + token * 2 * D + 16 * c));
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (KV == KV_E4M3) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(unit + token * D + 8 * c));
+      w[0] = v.x; w[1] = v.y;
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(unit + token * (D / 2) + 4 * c));
+      scale = __ldg(unit + kBlockTokens * (D / 2) + token * (D / kFp4Group) + c / 2);
+    }
   }
-}
+  __device__ __forceinline__ void pairs(uint32_t (&p)[4]) const {
+    if constexpr (KV == KV_BF16) {
+      p[0] = w[0]; p[1] = w[1]; p[2] = w[2]; p[3] = w[3];
+    } else if constexpr (KV == KV_E4M3) {
+      p[0] = e4m3x2_to_h2bits(w[0]); p[1] = e4m3x2_to_h2bits(w[0] >> 16);
+      p[2] = e4m3x2_to_h2bits(w[1]); p[3] = e4m3x2_to_h2bits(w[1] >> 16);
+    } else {
+      e2m1x8_to_h2(w[0], p);
+      const uint32_t g = e4m3x2_to_h2bits(scale | scale << 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(p[i]) : "r"(g));
+    }
+  }
+};
 
 constexpr int kBoundsWarps = 8;
-constexpr int kBoundsRows = 64;              // most rows of a CTA
+constexpr int kBoundsRows = 256;             // most rows of a CTA
 
 // A CTA looks through `rows` neighbouring rows for those that their block is left
-// to, then a warp takes a (block, KV head) at a time: a lane holds eight channels,
-// the lanes cover 256 / D tokens. Tokens past the row's are replaced by its own.
+// to, then a warp takes a (block, KV head) at a time, the next one's keys under
+// way: a lane holds eight channels, the lanes cover 256 / D tokens (those past the
+// row's are replaced by its own). Smallest and largest stay 16-bit pairs; lanes of
+// the same channels halve them among each other, so that each encodes its own.
 template <int D, int KV>
 __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const KeyBoundsArgs a) {
   constexpr int LANES = D / 8, TOK = 32 / LANES;
@@ -97,60 +111,76 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Key
   }
   __syncthreads();
   constexpr size_t UNIT = KV == KV_BF16 ? kBlockTokens * D * 2 : KV == KV_E4M3 ? kBlockTokens * D : fp4_unit_bytes(D);
+  constexpr int LOADS = kBlockTokens / TOK, OWN = 4 / TOK;            // pairs that a lane encodes
   const int c = lane % LANES, tasks = sm_count * a.nkv;
+  Key8<D, KV> key[LOADS];
+  auto load = [&](int i) {
+    const unsigned char* unit = reinterpret_cast<const unsigned char*>(a.kpool) + ((size_t)sm_blk[i / a.nkv] * a.nkv + i % a.nkv) * UNIT;
+#pragma unroll
+    for (int t = 0; t < LOADS; ++t) key[t].load(unit, min(t * TOK + lane / LANES, sm_upto[i / a.nkv]), c);
+  };
+  if (warp < tasks) load(warp);
   for (int i = warp; i < tasks; i += kBoundsWarps) {
-    const int upto = sm_upto[i / a.nkv];
     const size_t at = (size_t)sm_blk[i / a.nkv] * a.nkv + i % a.nkv;
-    const unsigned char* unit = reinterpret_cast<const unsigned char*>(a.kpool) + at * UNIT;
     uint32_t lo[4], hi[4];
 #pragma unroll
-    for (int t = 0; t < kBlockTokens / TOK; ++t) {
+    for (int t = 0; t < LOADS; ++t) {
       uint32_t p[4];
-      key_pairs<D, KV>(unit, min(t * TOK + lane / LANES, upto), c, p);
+      key[t].pairs(p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = t ? min_nan(lo[i], p[i], BF) : p[i];
-        hi[i] = t ? max_nan(hi[i], p[i], BF) : p[i];
+      for (int k = 0; k < 4; ++k) {
+        lo[k] = t ? min_nan(lo[k], p[k], BF) : p[k];
+        hi[k] = t ? max_nan(hi[k], p[k], BF) : p[k];
       }
     }
+    if (i + kBoundsWarps < tasks) load(i + kBoundsWarps);
+    int ch = 8 * c;                                                   // the lane's first channel
 #pragma unroll
-    for (int o = LANES; o < 32; o <<= 1)
+    for (int o = 16, n = 2; o >= LANES; o >>= 1, n >>= 1) {
+      const bool up = lane & o;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = min_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o), BF);
-        hi[i] = max_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o), BF);
+      for (int k = 0; k < n; ++k) {
+        const uint32_t l = __shfl_xor_sync(0xffffffffu, up ? lo[k] : lo[n + k], o);
+        const uint32_t h = __shfl_xor_sync(0xffffffffu, up ? hi[k] : hi[n + k], o);
+        lo[k] = min_nan(up ? lo[n + k] : lo[k], l, BF);
+        hi[k] = max_nan(up ? hi[n + k] : hi[k], h, BF);
       }
-    float l[8], u[8];
-    uint32_t big = 0;                                                // a NaN's bits are larger than an infinity's
+      ch += up ? 2 * n : 0;
+    }
+    float l[2 * OWN], u[2 * OWN];
+    uint32_t big = 0;                                                 // a NaN's bits are larger than an infinity's
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = BF ? make_float2(bf16_lo(lo[i]), bf16_hi(lo[i])) : h2_to_float2(lo[i]);
-      const float2 y = BF ? make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])) : h2_to_float2(hi[i]);
-      l[2 * i] = x.x; l[2 * i + 1] = x.y;
-      u[2 * i] = y.x; u[2 * i + 1] = y.y;
+    for (int k = 0; k < OWN; ++k) {
+      const float2 x = BF ? make_float2(bf16_lo(lo[k]), bf16_hi(lo[k])) : h2_to_float2(lo[k]);
+      const float2 y = BF ? make_float2(bf16_lo(hi[k]), bf16_hi(hi[k])) : h2_to_float2(hi[k]);
+      l[2 * k] = x.x; l[2 * k + 1] = x.y;
+      u[2 * k] = y.x; u[2 * k + 1] = y.y;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) big = max(big, max(__float_as_uint(l[i]) & 0x7fffffffu, __float_as_uint(u[i]) & 0x7fffffffu));
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+    for (int k = 0; k < 2 * OWN; ++k)
+      big = max(big, max(__float_as_uint(l[k]) & 0x7fffffffu, __float_as_uint(u[k]) & 0x7fffffffu));
+    big = __reduce_max_sync(0xffffffffu, big);
     const bool bad = big >= 0x7f800000u;
     // big = f 2^x with f in [1/2, 1): 127 * 2^(x - 7) holds it up to f = 127 / 128
     const int e = max((int)(big >> 23) - 126 - ((big & 0x7fffffu) <= 0x7e0000u ? 7 : 6), -100);
     const float down = bad || big == 0 ? 0.f : __int_as_float((127 - e) << 23);
-    uint32_t w[2][2] = {{0, 0}, {0, 0}};
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int k = 0; k < 2 * OWN; ++k) {
       // a product too small for fp32 is still on its side of 0
-      float x = bad ? 0.f : floorf(l[i] * down), y = bad ? 0.f : ceilf(u[i] * down);
-      if (down != 0.f && l[i] < 0.f) x = fminf(x, -1.f);
-      if (down != 0.f && u[i] > 0.f) y = fmaxf(y, 1.f);
-      w[0][i / 4] |= ((uint32_t)(int)x & 0xffu) << (8 * (i % 4));
-      w[1][i / 4] |= ((uint32_t)(int)y & 0xffu) << (8 * (i % 4));
+      float x = bad ? 0.f : floorf(l[k] * down), y = bad ? 0.f : ceilf(u[k] * down);
+      if (down != 0.f && l[k] < 0.f) x = fminf(x, -1.f);
+      if (down != 0.f && u[k] > 0.f) y = fmaxf(y, 1.f);
+      w[0] |= ((uint32_t)(int)x & 0xffu) << (8 * k);
+      w[1] |= ((uint32_t)(int)y & 0xffu) << (8 * k);
     }
-    if (lane < LANES) {
-      uint2* dst = reinterpret_cast<uint2*>(a.bounds + at * 2 * D) + c;
-      dst[0] = make_uint2(w[0][0], w[0][1]);
-      dst[LANES] = make_uint2(w[1][0], w[1][1]);
+    int8_t* dst = a.bounds + at * 2 * D + ch;
+    if constexpr (OWN == 2) {
+      *reinterpret_cast<uint32_t*>(dst) = w[0];
+      *reinterpret_cast<uint32_t*>(dst + D) = w[1];
+    } else {
+      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
+      *reinterpret_cast<uint16_t*>(dst + D) = (uint16_t)w[1];
     }
     if (lane == 0) a.scales[at] = bad ? __int_as_float(0x7f800000) : big == 0 ? 0.f : __int_as_float((e + 127) << 23);
   }
@@ -626,8 +656,8 @@ __global__ void __launch_bounds__(32 * kPartWarps) block_merge_kernel(const Bloc
 
 cudaError_t launch_key_bounds(const KeyBoundsArgs& in, int num_sms, cudaStream_t s) {
   KeyBoundsArgs a = in;
-  // all CTAs resident at once, eight per SM: most of a prompt's rows leave their block to the next
-  a.rows = (int)std::min<long long>(kBoundsRows, (a.n + 8LL * num_sms - 1) / (8LL * num_sms));
+  // all CTAs resident at once, four per SM: most of a prompt's rows leave their block to the next
+  a.rows = (int)std::min<long long>(kBoundsRows, (a.n + 4LL * num_sms - 1) / (4LL * num_sms));
   auto go = [&](auto kernel) {
     kernel<<<(unsigned)((a.n + (long long)a.rows - 1) / a.rows), 32 * kBoundsWarps, 0, s>>>(a);
     return cudaGetLastError();
