@@ -35,6 +35,7 @@ constexpr int kBaWarps = 4;                 // most warps of a CTA
 constexpr int kBaPerSm = 12;                // warps per SM (168 registers a thread)
 constexpr int kBaHeads = 8;                 // query heads per CTA (MMA rows)
 constexpr int kBaCluster = 8;               // most CTAs of a cluster
+constexpr int kBaStages = 2;                // steps of a warp's rings of K and V
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -81,20 +82,24 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Words of a lane, read once, past L1.
+// A lane's N words of shared memory.
 template <int N>
-__device__ __forceinline__ void ld_words(uint32_t (&w)[N], const unsigned char* p, int at) {
-  if constexpr (N == 4)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p + at));
-  else if constexpr (N == 2)
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p + at));
-  else
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p + at));
+__device__ __forceinline__ void lds(uint32_t (&w)[N], const unsigned char* p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 // How a block's K and V lie over a warp. Thread (g, t) = (lane / 4, lane % 4)
-// holds a quarter of the channels of keys g and g + 8 and an eighth of those of
-// the values 2t, 2t + 1, 2t + 8 and 2t + 9.
+// holds a quarter of the channels of the keys of columns g, token (g >> 1) + 4
+// (g & 1) and that + 8, and an eighth of those of the values t, t + 4, t + 8 and
+// t + 12.
 template <int D, int KV>
 struct Lay {
   static constexpr bool BF = KV == KV_BF16;
@@ -103,12 +108,22 @@ struct Lay {
   static constexpr int KB = ROW / 4 < 16 ? ROW / 4 : 16, KP = ROW / 4 / KB;       // bytes of a key's piece, pieces
   static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16, VP = ROW / 8 / VB;       // of a value's
   static constexpr int KC = D / 4 / KP, VC = D / 8 / VP;                          // channels of a piece
-  static constexpr int TB = KV == KV_BF16 ? 128 / D : KV == KV_E4M3 ? 256 / D : 256 / D;   // blocks of a step
+  static constexpr int TB = KV == KV_BF16 ? 128 / D : KV == KV_E4M3 ? 256 / D : 4;   // blocks of a step
   static constexpr int KS = D / 16, NT = D / 8;                                   // MMA steps of a score, n-tiles of the output
-  static constexpr int SC = KV == KV_FP4 ? TB : 1;                                // scale registers
+  static constexpr int STAGE = TB * UNIT, RING = 2 * kBaStages * STAGE;           // K or V of a step; a warp's ring
+  static constexpr int WARP = RING + (BF ? D * 4 : 0);                            // with the sums of values that are not finite
+  static_assert(RING >= kBaHeads * D * 4, "the warp's output takes the drained ring's place");
   // channel of a lane's i-th query value; of the c-th value of column g of the output's n-tiles
   static __device__ __forceinline__ int q_channel(int t, int i) { return i / KC * 4 * KC + KC * t + i % KC; }
   static __device__ __forceinline__ int v_channel(int g, int c) { return c / VC * 8 * VC + VC * g + c % VC; }
+  // What a token's 16-byte pieces are exchanged by within 128 bytes of shared
+  // memory, so that eight lanes meet eight different ones, of two keys or of four
+  // values.
+  static __device__ __forceinline__ int swap(int tok) {
+    return (tok & 4) ^ (ROW >= 128 ? (tok & 3) << 1 : ROW == 64 ? tok & 2 : 0);
+  }
+  // Place of byte `b` of a token in a unit in shared memory.
+  static __device__ __forceinline__ int place(int tok, int b) { return (((tok * ROW + b) >> 4) ^ swap(tok)) << 4 | (b & 15); }
 };
 
 // The chosen blocks of a warp: entries first, first + stride, .. of the row's
@@ -165,8 +180,6 @@ template <int D, int KV>
 struct BlockWarp {
   using L = Lay<D, KV>;
   static constexpr bool BF = L::BF;
-  uint32_t k[L::TB][2][L::KP][L::KB / 4], v[L::TB][4][L::VP][L::VB / 4];
-  uint32_t ks[L::SC][2], vs[L::SC][2];                                // 4-bit: scale bytes of the keys and values
   float m, l, o[L::NT][2];
 
   __device__ __forceinline__ void start() {
@@ -175,74 +188,71 @@ struct BlockWarp {
 #pragma unroll
     for (int i = 0; i < L::NT; ++i) o[i][0] = o[i][1] = 0.f;
   }
-  __device__ __forceinline__ void load_k(const unsigned char* pool, const int (&blk)[L::TB], int nkv, int h, int lane) {
-    const int g = lane >> 2, t = lane & 3;
+  // Requests the K or V units of a step's blocks into a stage (a shared address).
+  static __device__ __forceinline__ void request(uint32_t stage, const unsigned char* pool, const int (&blk)[L::TB], int nkv, int h, int lane) {
+    constexpr int N = L::UNIT / 16, ROWS = kBlockTokens * L::ROW / 16;
 #pragma unroll
     for (int b = 0; b < L::TB; ++b) {
-      const unsigned char* unit = pool + ((size_t)blk[b] * nkv + h) * L::UNIT;
+      const unsigned char* unit = pool + ((size_t)blk[b] * nkv + h) * L::UNIT + lane * 16;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-#pragma unroll
-        for (int p = 0; p < L::KP; ++p) ld_words(k[b][n][p], unit, (8 * n + g) * L::ROW + (4 * p + t) * L::KB);
-        if constexpr (KV == KV_FP4) {
-          const unsigned char* s = unit + kBlockTokens * L::ROW + (8 * n + g) * (D / 16) + t * (D / 64);
-          ks[b][n] = D == 128 ? *reinterpret_cast<const uint16_t*>(s) : *s;
-        }
+      for (int i = 0; i < N; i += 32) {
+        const int c = i + lane, to = c < ROWS ? c ^ L::swap(c * 16 / L::ROW) : c;
+        if (i + 32 <= N || c < N)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(stage + b * L::UNIT + to * 16), "l"(unit + i * 16) : "memory");
       }
     }
-  }
-  __device__ __forceinline__ void load_v(const unsigned char* pool, const int (&blk)[L::TB], int nkv, int h, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int b = 0; b < L::TB; ++b) {
-      const unsigned char* unit = pool + ((size_t)blk[b] * nkv + h) * L::UNIT;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int p = 0; p < L::VP; ++p)
-          ld_words(v[b][i][p], unit, (2 * t + (i & 1) + 8 * (i >> 1)) * L::ROW + (8 * p + g) * L::VB);
-      if constexpr (KV == KV_FP4) {
-        const unsigned char* s = unit + kBlockTokens * L::ROW + 2 * t * (D / 16) + g * (D / 8) / 16;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) vs[b][n] = s[8 * n * (D / 16)] | (uint32_t)s[(8 * n + 1) * (D / 16)] << 8;
-      }
-    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
 
-  // Scores of a step: s[2 b + n][e] of head g and token 2 t + e + 8 n of block b.
-  // frag: the queries' fragments, [KS][32 lanes] x 4 words; frag_lo: the third parts', x 2.
-  __device__ __forceinline__ void scores(float (&s)[2 * L::TB][2], const uint4* frag, const uint2* frag_lo, int lane) {
+  // Scores of a step: s[2 b + n][e] of head g and token t + 4 e + 8 n of block b.
+  // stage: its keys; frag: the queries' fragments, [KS][32 lanes] x 4 words;
+  // frag_lo: the third parts', x 2.
+  __device__ __forceinline__ void scores(float (&s)[2 * L::TB][2], const unsigned char* stage, const uint4* frag, const uint2* frag_lo, int lane) {
+    const int g = lane >> 2, t = lane & 3, tok = (g >> 1) + 4 * (g & 1);
+    const unsigned char* at[2] = {stage + L::place(tok, t * L::KB), stage + L::place(tok, L::KP > 1 ? (4 + t) * L::KB : 0)};
     float acc[2 * L::TB][4];
 #pragma unroll
     for (int i = 0; i < 2 * L::TB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     uint32_t sc[2 * L::TB];
+    constexpr int PS = L::KS / L::KP;                                 // MMA steps of a piece
 #pragma unroll
-    for (int st = 0; st < L::KS; ++st) {
-      const uint4 a = frag[st * 32 + lane];
-      uint2 z = make_uint2(0, 0);
-      if constexpr (BF) z = frag_lo[st * 32 + lane];
+    for (int p = 0; p < L::KP; ++p) {
+      uint32_t k[2 * L::TB][L::KB / 4];
 #pragma unroll
-      for (int i = 0; i < 2 * L::TB; ++i) {
-        uint32_t b0, b1;
-        if constexpr (KV == KV_BF16) {
-          b0 = k[i / 2][i & 1][st / 2][2 * (st & 1)];
-          b1 = k[i / 2][i & 1][st / 2][2 * (st & 1) + 1];
-        } else if constexpr (KV == KV_E4M3) {
-          const uint32_t w = k[i / 2][i & 1][st / 4][st % 4];
-          b0 = e4m3x2_to_h2bits(w);
-          b1 = e4m3x2_to_h2bits(w >> 16);
-        } else {
-          if (st % 4 == 0) {                                          // a scale per 16 channels
-            const uint32_t byte = ks[i / 2][i & 1] >> (8 * (st / 4)) & 0xffu;
-            sc[i] = e4m3x2_to_h2bits(byte | byte << 8);
-          }
-          uint32_t h[2];
-          e2m1x4_to_h2(k[i / 2][i & 1][0][st / 2] >> (16 * (st & 1)) & 0xffffu, h);
-          b0 = hmul2(h[0], sc[i]);
-          b1 = hmul2(h[1], sc[i]);
+      for (int i = 0; i < 2 * L::TB; ++i) lds(k[i], at[p & 1] + (i / 2) * L::UNIT + (i & 1) * 8 * L::ROW + p / 2 * 128);
+      if constexpr (KV == KV_FP4) {
+        const unsigned char* sb = stage + kBlockTokens * L::ROW + tok * (D / 16) + t * (D / 64);
+#pragma unroll
+        for (int i = 0; i < 2 * L::TB; ++i) {
+          const unsigned char* x = sb + (i / 2) * L::UNIT + (i & 1) * 8 * (D / 16);
+          sc[i] = D == 128 ? *reinterpret_cast<const uint16_t*>(x) : *x;
         }
-        mma<BF>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
-        if constexpr (BF) mma<BF>(acc[i], z.x, 0u, z.y, 0u, b0, b1);
+      }
+#pragma unroll
+      for (int q = 0; q < PS; ++q) {
+        const int st = p * PS + q;
+        const uint4 a = frag[st * 32 + lane];
+        uint2 z = make_uint2(0, 0);
+        if constexpr (BF) z = frag_lo[st * 32 + lane];
+#pragma unroll
+        for (int i = 0; i < 2 * L::TB; ++i) {
+          uint32_t b0, b1;
+          if constexpr (KV == KV_BF16) {
+            b0 = k[i][2 * q];
+            b1 = k[i][2 * q + 1];
+          } else if constexpr (KV == KV_E4M3) {
+            b0 = e4m3x2_to_h2bits(k[i][q]);
+            b1 = e4m3x2_to_h2bits(k[i][q] >> 16);
+          } else {                                                    // a scale per 16 channels, four steps
+            const uint32_t byte = sc[i] >> (8 * (q / 4)) & 0xffu, by = e4m3x2_to_h2bits(byte | byte << 8);
+            uint32_t h[2];
+            e2m1x4_to_h2(k[i][q / 2] >> (16 * (q & 1)) & 0xffffu, h);
+            b0 = hmul2(h[0], by);
+            b1 = hmul2(h[1], by);
+          }
+          mma<BF>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
+          if constexpr (BF) mma<BF>(acc[i], z.x, 0u, z.y, 0u, b0, b1);
+        }
       }
     }
 #pragma unroll
@@ -254,18 +264,18 @@ struct BlockWarp {
       }
   }
 
-  // Softmax of head g over the lane's tokens, then O = O * al + P V. live: tokens
-  // of each block that the row sees. spec: where values that are not finite go
-  // (null: they are not looked for).
-  __device__ __forceinline__ void rest(float (&s)[2 * L::TB][2], const int (&live)[L::TB], float fac, float* spec, int lane) {
+  // Softmax of head g over the lane's tokens: probabilities as A fragments of P V,
+  // and what the output so far is to be multiplied by. live: tokens of each block
+  // that the row sees.
+  __device__ __forceinline__ float soften(float (&s)[2 * L::TB][2], uint32_t (&pa)[2 * L::TB][3], const int (&live)[L::TB], float fac, int lane) {
     constexpr float UP = BF ? 0.f : 14.f;
-    const int g = lane >> 2, t = lane & 3;
+    const int t = lane & 3;
     float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 2 * L::TB; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        if (8 * (i & 1) + 2 * t + e >= live[i / 2]) s[i][e] = -INFINITY;
+        if (8 * (i & 1) + t + 4 * e >= live[i / 2]) s[i][e] = -INFINITY;
         mx = fmaxf(mx, s[i][e]);
       }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -274,7 +284,6 @@ struct BlockWarp {
     const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn, al = ex2((m - mu) * fac);
     m = mn;
     float sum = 0.f;
-    uint32_t pa[2 * L::TB][3];
 #pragma unroll
     for (int i = 0; i < 2 * L::TB; ++i) {
       const float p0 = ex2(fmaf(s[i][0] - mu, fac, UP)), p1 = ex2(fmaf(s[i][1] - mu, fac, UP));
@@ -282,12 +291,33 @@ struct BlockWarp {
       split<BF>(p0, p1, pa[i][0], pa[i][1], pa[i][2]);
     }
     l = fmaf(l, al, sum);
+    return al;
+  }
+
+  // O = O * al + P V for a step whose values are in the stage. spec: where values
+  // that are not finite go (null: they are not looked for).
+  __device__ __forceinline__ void values(const uint32_t (&pa)[2 * L::TB][3], const unsigned char* stage, const int (&live)[L::TB], float al, float* spec, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t v[L::TB][4][L::VP][L::VB / 4], vs[KV == KV_FP4 ? L::TB : 1][2];
+    const unsigned char* at[2] = {stage + L::place(t, g * L::VB), stage + L::place(t + 4, g * L::VB)};
+#pragma unroll
+    for (int b = 0; b < L::TB; ++b) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < L::VP; ++p) lds(v[b][i][p], at[i & 1] + b * L::UNIT + 8 * (i >> 1) * L::ROW + p * 128);
+      if constexpr (KV == KV_FP4) {
+        const unsigned char* x = stage + b * L::UNIT + kBlockTokens * L::ROW + t * (D / 16) + g * (D / 8) / 16;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) vs[b][n] = x[8 * n * (D / 16)] | (uint32_t)x[(8 * n + 4) * (D / 16)] << 8;
+      }
+    }
 #pragma unroll
     for (int b = 0; b < L::TB; ++b) {
       if (live[b] < kBlockTokens) {                                   // the same for the whole warp
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (2 * t + (i & 1) + 8 * (i >> 1) < live[b]) continue;
+          if (t + 4 * (i & 1) + 8 * (i >> 1) < live[b]) continue;
           if constexpr (KV == KV_FP4) {
             vs[b][i >> 1] &= (i & 1) ? 0x00ffu : 0xff00u;
           } else {
@@ -401,9 +431,9 @@ __global__ void __launch_bounds__(32 * kBaWarps, kBaPerSm / kBaWarps) block_atte
   constexpr bool BF = L::BF;
   __shared__ __align__(16) uint4 frag[L::KS * 32];
   __shared__ __align__(16) uint2 frag_lo[BF ? L::KS * 32 : 1];
-  __shared__ __align__(16) float so[kBaWarps * kBaHeads * D];         // [warp][head][D]
+  extern __shared__ __align__(128) unsigned char ring[];              // [warp][K stages, V stages]
+  float* so = reinterpret_cast<float*>(ring);                         // then [warp][head][D]
   __shared__ float sm_m[kBaWarps][kBaHeads], sm_l[kBaWarps][kBaHeads], cta_m[kBaHeads], cta_l[kBaHeads], sm_fac[kBaHeads];
-  __shared__ float sm_spec[BF ? kBaWarps : 1][BF ? D : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int sp = (int)(blockIdx.x % (unsigned)a.cluster), pair = (int)(blockIdx.x / (unsigned)a.cluster);
   const int hb = pair % a.hblocks, h = pair / a.hblocks % a.nkv, row = pair / a.hblocks / a.nkv;
@@ -437,17 +467,29 @@ __global__ void __launch_bounds__(32 * kBaWarps, kBaPerSm / kBaWarps) block_atte
   const unsigned char* kpool = reinterpret_cast<const unsigned char*>(a.kpool);
   const unsigned char* vpool = reinterpret_cast<const unsigned char*>(a.vpool);
   BlockWarp<D, KV> w;
-  int blk[L::TB], live[L::TB];
-  bool more = pk.any();
-  auto take = [&]() {
+  unsigned char* mine = ring + warp * L::RING;
+  const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(mine);
+  int blk[kBaStages][L::TB], live[kBaStages][L::TB];                  // of the steps under way
+  bool on[kBaStages];
+  auto step = [&](int i) {                                            // the next step's blocks
+    on[i] = pk.any();
 #pragma unroll
-    for (int b = 0; b < L::TB; ++b) pk.take(blk[b], live[b], pos);
+    for (int b = 0; b < L::TB; ++b)
+      if (on[i]) pk.take(blk[i][b], live[i][b], pos);
   };
-  if (more) {
-    take();
-    w.load_k(kpool, blk, a.nkv, h, lane);
-    w.load_v(vpool, blk, a.nkv, h, lane);
-  }
+  auto request = [&](int i, bool v) {
+    if (on[i]) w.request(mine_at + ((v ? kBaStages : 0) + i) * L::STAGE, v ? vpool : kpool, blk[i], a.nkv, h, lane);
+    else asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto begin = [&]() {
+#pragma unroll
+    for (int i = 0; i < kBaStages; ++i) {
+      step(i);
+      request(i, false);
+      request(i, true);
+    }
+  };
+  begin();
 
   // The queries' fragments, while the first blocks are under way. A power of two
   // per head brings the largest into FP16's range, or (BF16) a tiny one away from
@@ -479,20 +521,30 @@ __global__ void __launch_bounds__(32 * kBaWarps, kBaPerSm / kBaWarps) block_atte
   w.start();
 #pragma unroll 1
   while (true) {
+    bool more = true;
 #pragma unroll 1
     while (more) {
-      float s[2 * L::TB][2];
-      int now[L::TB];
-      w.scores(s, frag, frag_lo, lane);
 #pragma unroll
-      for (int b = 0; b < L::TB; ++b) now[b] = live[b];
-      more = pk.any();
-      if (more) {
-        take();
-        w.load_k(kpool, blk, a.nkv, h, lane);
+      for (int i = 0; i < kBaStages; ++i) {
+        if (!on[i]) { more = false; break; }
+        float s[2 * L::TB][2];
+        uint32_t pa[2 * L::TB][3];
+        int now[L::TB];
+        asm volatile("cp.async.wait_group %0;" ::"n"(2 * kBaStages - 1) : "memory");
+        __syncwarp();
+        w.scores(s, mine + i * L::STAGE, frag, frag_lo, lane);
+#pragma unroll
+        for (int b = 0; b < L::TB; ++b) now[b] = live[i][b];
+        __syncwarp();                                                 // the keys' stage may be refilled
+        step(i);
+        request(i, false);
+        const float al = w.soften(s, pa, now, fac, lane);
+        asm volatile("cp.async.wait_group %0;" ::"n"(2 * kBaStages - 1) : "memory");
+        __syncwarp();
+        w.values(pa, mine + (kBaStages + i) * L::STAGE, now, al, spec, lane);
+        __syncwarp();
+        request(i, true);
       }
-      w.rest(s, now, fac, spec, lane);
-      if (more) w.load_v(vpool, blk, a.nkv, h, lane);
     }
     w.l += __shfl_xor_sync(0xffffffffu, w.l, 1);
     w.l += __shfl_xor_sync(0xffffffffu, w.l, 2);
@@ -506,21 +558,17 @@ __global__ void __launch_bounds__(32 * kBaWarps, kBaPerSm / kBaWarps) block_atte
       odd = odd && w.l <= 3.4e38f;
     }
     if (!__any_sync(0xffffffffu, odd)) break;
-    spec = sm_spec[warp];
+    spec = reinterpret_cast<float*>(ring + warps * L::RING) + warp * D;
     for (int i = lane; i < D; i += 32) spec[i] = 0.f;
     __syncwarp();
     pk.at = first;
     pk.e2 = pk.entry();
     pk.mask = 0;
     w.start();
-    more = pk.any();
-    if (more) {
-      take();
-      w.load_k(kpool, blk, a.nkv, h, lane);
-      w.load_v(vpool, blk, a.nkv, h, lane);
-    }
+    begin();
   }
-  __syncwarp();
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();                                                    // every ring is drained
   w.leave(so + warp * kBaHeads * D, sm_m[warp], sm_l[warp], spec, lane);
   __syncthreads();
   // an infinity counts whatever its share
@@ -571,8 +619,14 @@ cudaError_t ba_launch(const BlockAttnArgs& a, cudaStream_t s) {
   BlockAttnArgs args = a;
   void* p[] = {&args};
   const long long grid = (long long)a.n * a.nkv * a.hblocks * a.cluster;
-  return launch_ex((const void*)block_attention_kernel<D, KV>, dim3((unsigned)grid), dim3(32 * a.warps), 0, s, p, false, -1,
-                   a.cluster > 1 ? a.cluster : 0);
+  return launch_ex((const void*)block_attention_kernel<D, KV>, dim3((unsigned)grid), dim3(32 * a.warps), a.warps * Lay<D, KV>::WARP, s,
+                   p, false, 100, a.cluster > 1 ? a.cluster : 0);
+}
+
+template <int D, int KV>
+cudaError_t ba_init() {
+  return cudaFuncSetAttribute((const void*)block_attention_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kBaWarps * Lay<D, KV>::WARP);
 }
 
 }  // namespace
@@ -584,11 +638,20 @@ cudaError_t launch_block_attention(const BlockAttnArgs& in, int num_sms, cudaStr
   if (pairs * kBaCluster > 0x7fffffffLL || a.k > 0x7fffffff - 32 * kBaWarps * kBaCluster) return cudaErrorInvalidValue;
   const long long want = std::min<long long>((a.k + 2 * kBaWarps - 1) / (2 * kBaWarps), (long long)kBaPerSm * num_sms / kBaWarps / pairs);
   a.cluster = (int)std::max<long long>(1, std::min<long long>(kBaCluster, want));
-  a.warps = kBaWarps;
+  a.warps = (int)std::max<long long>(1, std::min<long long>(kBaWarps, (long long)kBaPerSm * num_sms / pairs));
   const bool wide = a.d == 128;
   if (a.kv == KV_BF16) return wide ? ba_launch<128, KV_BF16>(a, s) : ba_launch<64, KV_BF16>(a, s);
   if (a.kv == KV_E4M3) return wide ? ba_launch<128, KV_E4M3>(a, s) : ba_launch<64, KV_E4M3>(a, s);
   return wide ? ba_launch<128, KV_FP4>(a, s) : ba_launch<64, KV_FP4>(a, s);
+}
+
+cudaError_t block_attention_init() {
+  cudaError_t e = ba_init<64, KV_BF16>();
+  if (e == cudaSuccess) e = ba_init<128, KV_BF16>();
+  if (e == cudaSuccess) e = ba_init<64, KV_E4M3>();
+  if (e == cudaSuccess) e = ba_init<128, KV_E4M3>();
+  if (e == cudaSuccess) e = ba_init<64, KV_FP4>();
+  return e == cudaSuccess ? ba_init<128, KV_FP4>() : e;
 }
 
 }  // namespace mbt

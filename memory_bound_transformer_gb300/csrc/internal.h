@@ -346,5 +346,6 @@ struct BlockAttnArgs {
   int hblocks, cluster, warps;      // set by the launch: groups of eight heads per KV head, CTAs per cluster, warps per CTA
 };
 cudaError_t launch_block_attention(const BlockAttnArgs& a, int num_sms, cudaStream_t s);
+cudaError_t block_attention_init();
 
 }  // namespace mbt

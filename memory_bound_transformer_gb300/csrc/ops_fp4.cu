@@ -25,7 +25,8 @@ int device_setup(int* sms) {
   if (!known[dev]) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MBT_ERR_NO_DEVICE;
-    if (attn_fp4_init() != cudaSuccess || prompt_attention_init() != cudaSuccess || block_select_init() != cudaSuccess)
+    if (attn_fp4_init() != cudaSuccess || prompt_attention_init() != cudaSuccess || block_select_init() != cudaSuccess ||
+        block_attention_init() != cudaSuccess)
       return MBT_ERR_CUDA;
     known[dev] = n;
   }
