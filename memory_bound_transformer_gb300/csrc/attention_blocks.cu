@@ -72,14 +72,30 @@ __device__ __forceinline__ void split(float x0, float x1, uint32_t& p0, uint32_t
     p2 = 0;
   }
 }
-template <bool BF>
+// d = a b + d, or + 0 where the sum begins.
+template <bool BF, bool ZERO = false>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (BF)
+  if constexpr (BF && ZERO)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else if constexpr (BF)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else if constexpr (ZERO)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The four e4m3 codes of a word as two FP16 pairs, exactly.
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_h2(uint32_t w) {           // of the low two
+  uint32_t r;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}\n" : "=r"(r) : "r"(w));
+  return r;
 }
 
 // A lane's N words of shared memory.
@@ -211,9 +227,7 @@ struct BlockWarp {
     const int g = lane >> 2, t = lane & 3, tok = (g >> 1) + 4 * (g & 1);
     const unsigned char* at[2] = {stage + L::place(tok, t * L::KB), stage + L::place(tok, L::KP > 1 ? (4 + t) * L::KB : 0)};
     float acc[2 * L::TB][4];
-#pragma unroll
-    for (int i = 0; i < 2 * L::TB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    uint32_t sc[2 * L::TB];
+    uint32_t sc[2 * L::TB], by[2 * L::TB];                            // 4-bit: scale bytes; the scale of 16 channels as FP16 pairs
     constexpr int PS = L::KS / L::KP;                                 // MMA steps of a piece
 #pragma unroll
     for (int p = 0; p < L::KP; ++p) {
@@ -228,30 +242,45 @@ struct BlockWarp {
           sc[i] = D == 128 ? *reinterpret_cast<const uint16_t*>(x) : *x;
         }
       }
+      auto product = [&](int st, int i, uint32_t b0, uint32_t b1, const uint4& a, const uint2& z) {
+        if (st == 0) mma<BF, true>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
+        else mma<BF>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
+        if constexpr (BF) mma<BF>(acc[i], z.x, 0u, z.y, 0u, b0, b1);
+      };
+      if constexpr (KV == KV_FP4) {
 #pragma unroll
-      for (int q = 0; q < PS; ++q) {
-        const int st = p * PS + q;
-        const uint4 a = frag[st * 32 + lane];
-        uint2 z = make_uint2(0, 0);
-        if constexpr (BF) z = frag_lo[st * 32 + lane];
+        for (int q = 0; q < PS; q += 2) {                             // a word: two steps
+          const uint4 a0 = frag[q * 32 + lane], a1 = frag[(q + 1) * 32 + lane];
 #pragma unroll
-        for (int i = 0; i < 2 * L::TB; ++i) {
-          uint32_t b0, b1;
-          if constexpr (KV == KV_BF16) {
-            b0 = k[i][2 * q];
-            b1 = k[i][2 * q + 1];
-          } else if constexpr (KV == KV_E4M3) {
-            b0 = e4m3x2_to_h2bits(k[i][q]);
-            b1 = e4m3x2_to_h2bits(k[i][q] >> 16);
-          } else {                                                    // a scale per 16 channels, four steps
-            const uint32_t byte = sc[i] >> (8 * (q / 4)) & 0xffu, by = e4m3x2_to_h2bits(byte | byte << 8);
-            uint32_t h[2];
-            e2m1x4_to_h2(k[i][q / 2] >> (16 * (q & 1)) & 0xffffu, h);
-            b0 = hmul2(h[0], by);
-            b1 = hmul2(h[1], by);
+          for (int i = 0; i < 2 * L::TB; ++i) {
+            if (q % 4 == 0) {
+              const uint32_t byte = sc[i] >> (8 * (q / 4)) & 0xffu;
+              by[i] = e4m3x2_h2(byte * 0x0101u);
+            }
+            uint32_t x[4];
+            e2m1x8_to_h2(k[i][q / 2], x);
+            product(q, i, hmul2(x[0], by[i]), hmul2(x[1], by[i]), a0, make_uint2(0, 0));
+            product(q + 1, i, hmul2(x[2], by[i]), hmul2(x[3], by[i]), a1, make_uint2(0, 0));
           }
-          mma<BF>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
-          if constexpr (BF) mma<BF>(acc[i], z.x, 0u, z.y, 0u, b0, b1);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < PS; ++q) {
+          const int st = p * PS + q;
+          const uint4 a = frag[st * 32 + lane];
+          uint2 z = make_uint2(0, 0);
+          if constexpr (BF) z = frag_lo[st * 32 + lane];
+#pragma unroll
+          for (int i = 0; i < 2 * L::TB; ++i) {
+            uint32_t b0, b1;
+            if constexpr (BF) {
+              b0 = k[i][2 * q];
+              b1 = k[i][2 * q + 1];
+            } else {
+              e4m3x4_to_h2(k[i][q], b0, b1);
+            }
+            product(st, i, b0, b1, a, z);
+          }
         }
       }
     }
@@ -272,12 +301,14 @@ struct BlockWarp {
     const int t = lane & 3;
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 2 * L::TB; ++i)
+    for (int b = 0; b < L::TB; ++b)
+      if (live[b] < kBlockTokens) {                                   // the same for the whole warp
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (8 * (i & 1) + t + 4 * e >= live[i / 2]) s[i][e] = -INFINITY;
-        mx = fmaxf(mx, s[i][e]);
+        for (int i = 0; i < 4; ++i)
+          if (8 * (i >> 1) + t + 4 * (i & 1) >= live[b]) s[2 * b + (i >> 1)][i & 1] = -INFINITY;
       }
+#pragma unroll
+    for (int i = 0; i < 2 * L::TB; ++i) mx = fmaxf(mx, fmaxf(s[i][0], s[i][1]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     // differences of scores first: equal ones stay equal however large they are
@@ -344,10 +375,11 @@ struct BlockWarp {
       }
     }
     auto add = [&](int c, const uint32_t (&f0)[L::TB], const uint32_t (&f1)[L::TB]) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float acc[4];
 #pragma unroll
       for (int b = 0; b < L::TB; ++b) {
-        mma<BF>(acc, pa[2 * b][0], pa[2 * b][1], pa[2 * b + 1][0], pa[2 * b + 1][1], f0[b], f1[b]);
+        if (b == 0) mma<BF, true>(acc, pa[0][0], pa[0][1], pa[1][0], pa[1][1], f0[0], f1[0]);
+        else mma<BF>(acc, pa[2 * b][0], pa[2 * b][1], pa[2 * b + 1][0], pa[2 * b + 1][1], f0[b], f1[b]);
         if constexpr (BF) mma<BF>(acc, pa[2 * b][2], 0u, pa[2 * b + 1][2], 0u, f0[b], f1[b]);
       }
       o[c][0] = fmaf(o[c][0], al, acc[0] + acc[2]);
@@ -377,8 +409,8 @@ struct BlockWarp {
           for (int b = 0; b < L::TB; ++b) {
             const uint32_t x = __byte_perm(v[b][0][0][w], v[b][1][0][w], half ? 0x7362 : 0x5140);
             const uint32_t y = __byte_perm(v[b][2][0][w], v[b][3][0][w], half ? 0x7362 : 0x5140);
-            f[0][b] = e4m3x2_to_h2bits(x); f[1][b] = e4m3x2_to_h2bits(x >> 16);
-            f2[0][b] = e4m3x2_to_h2bits(y); f2[1][b] = e4m3x2_to_h2bits(y >> 16);
+            e4m3x4_to_h2(x, f[0][b], f[1][b]);
+            e4m3x4_to_h2(y, f2[0][b], f2[1][b]);
           }
           add(4 * w + 2 * half, f[0], f2[0]);
           add(4 * w + 2 * half + 1, f[1], f2[1]);
@@ -386,7 +418,7 @@ struct BlockWarp {
     } else {
       uint32_t sc[L::TB][2];
 #pragma unroll
-      for (int b = 0; b < L::TB; ++b) { sc[b][0] = e4m3x2_to_h2bits(vs[b][0]); sc[b][1] = e4m3x2_to_h2bits(vs[b][1]); }
+      for (int b = 0; b < L::TB; ++b) { sc[b][0] = e4m3x2_h2(vs[b][0]); sc[b][1] = e4m3x2_h2(vs[b][1]); }
 #pragma unroll
       for (int w = 0; w < L::VB / 4; ++w)
 #pragma unroll
