@@ -390,17 +390,18 @@ def _device(fn: str, name: str, t) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{fn}: {name} must be a device tensor")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():                  # a device tensor: the runtime is up
         raise ValueError(f"{fn}: {name} is on another device than the current one")
     return dev
 
 
 def _shape(fn: str, name: str, t, dims: int):
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    if len(shape) != dims:
         raise ValueError(f"{fn}: {name} must be a tensor of {dims} dimensions")
-    if max(t.shape) > 0x7fffffff:                          # ctypes would pass what is left of it in 32 bits
+    if max(shape) > 0x7fffffff:                            # ctypes would pass what is left of it in 32 bits
         raise ValueError(f"{fn}: {name} has a dimension beyond 2^31 - 1")
-    return t.shape
+    return shape
 
 
 # op_kv_unit_bytes of the head sizes and cache formats the kernels take

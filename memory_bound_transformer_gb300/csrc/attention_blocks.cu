@@ -32,7 +32,7 @@ namespace mbt {
 namespace {
 
 constexpr int kBaWarps = 4;                 // most warps of a CTA
-constexpr int kBaPerSm = 12;                // warps per SM (168 registers a thread)
+__host__ __device__ constexpr int ba_per_sm(int d) { return d == 64 ? 16 : 12; }   // warps per SM (128, 168 registers a thread)
 constexpr int kBaHeads = 8;                 // query heads per CTA (MMA rows)
 constexpr int kBaCluster = 8;               // most CTAs of a cluster
 constexpr int kBaStages = 2;                // steps of a warp's rings of K and V
@@ -124,7 +124,7 @@ struct Lay {
   static constexpr int KB = ROW / 4 < 16 ? ROW / 4 : 16, KP = ROW / 4 / KB;       // bytes of a key's piece, pieces
   static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16, VP = ROW / 8 / VB;       // of a value's
   static constexpr int KC = D / 4 / KP, VC = D / 8 / VP;                          // channels of a piece
-  static constexpr int TB = KV == KV_BF16 ? 128 / D : KV == KV_E4M3 ? 256 / D : 4;   // blocks of a step
+  static constexpr int TB = KV == KV_BF16 ? 1 : KV == KV_E4M3 || D == 128 ? 2 : 4;   // blocks of a step
   static constexpr int KS = D / 16, NT = D / 8;                                   // MMA steps of a score, n-tiles of the output
   static constexpr int STAGE = TB * UNIT, RING = 2 * kBaStages * STAGE;           // K or V of a step; a warp's ring
   static constexpr int WARP = RING + (BF ? D * 4 : 0);                            // with the sums of values that are not finite
@@ -458,7 +458,7 @@ struct BlockWarp {
 // warps take the row's blocks in turn and the CTAs' parts merge through
 // distributed shared memory. One launch, no scratch.
 template <int D, int KV>
-__global__ void __launch_bounds__(32 * kBaWarps, kBaPerSm / kBaWarps) block_attention_kernel(const BlockAttnArgs a) {
+__global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_attention_kernel(const BlockAttnArgs a) {
   using L = Lay<D, KV>;
   constexpr bool BF = L::BF;
   __shared__ __align__(16) uint4 frag[L::KS * 32];
@@ -668,9 +668,9 @@ cudaError_t launch_block_attention(const BlockAttnArgs& in, int num_sms, cudaStr
   a.hblocks = (a.nq / a.nkv + kBaHeads - 1) / kBaHeads;
   const long long pairs = (long long)a.n * a.nkv * a.hblocks;
   if (pairs * kBaCluster > 0x7fffffffLL || a.k > 0x7fffffff - 32 * kBaWarps * kBaCluster) return cudaErrorInvalidValue;
-  const long long want = std::min<long long>((a.k + 2 * kBaWarps - 1) / (2 * kBaWarps), (long long)kBaPerSm * num_sms / kBaWarps / pairs);
+  const long long want = std::min<long long>((a.k + 2 * kBaWarps - 1) / (2 * kBaWarps), (long long)ba_per_sm(a.d) * num_sms / kBaWarps / pairs);
   a.cluster = (int)std::max<long long>(1, std::min<long long>(kBaCluster, want));
-  a.warps = (int)std::max<long long>(1, std::min<long long>(kBaWarps, (long long)kBaPerSm * num_sms / pairs));
+  a.warps = (int)std::max<long long>(1, std::min<long long>(kBaWarps, (long long)ba_per_sm(a.d) * num_sms / pairs));
   const bool wide = a.d == 128;
   if (a.kv == KV_BF16) return wide ? ba_launch<128, KV_BF16>(a, s) : ba_launch<64, KV_BF16>(a, s);
   if (a.kv == KV_E4M3) return wide ? ba_launch<128, KV_E4M3>(a, s) : ba_launch<64, KV_E4M3>(a, s);
