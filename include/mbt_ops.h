@@ -278,7 +278,8 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
  * cache write (op_rope_kv_write, op_rope_kv_write_fp4), op_key_bounds (the
  * ranges of the blocks written to), op_block_select, op_block_attention.
  * All take cache formats, head sizes, groups, scales and table widths as the
- * 4-bit section above says, and rows of any sequences: row i is at positions[i]
+ * 4-bit section above says, up to 2^30 rows, 2^16 KV heads and 2^26 chosen
+ * blocks per row and head, and rows of any sequences: row i is at positions[i]
  * of sequence row_seq[i] (NULL: sequence i, nseq >= n) of bt [nseq][bt_stride].
  * A row whose position or sequence is outside the table sets MBT_DEV_POS_RANGE;
  * an out-of-range block id sets MBT_DEV_BLOCK_RANGE. They keep nothing between

@@ -7,8 +7,9 @@
 using namespace mbt;
 
 namespace {
-bool rows_ok(int n, const int32_t* positions, const int32_t* row_seq, int nseq) {
-  return n >= 1 && positions && nseq >= 1 && (row_seq || nseq >= n);
+constexpr int kMostRows = 1 << 30, kMostPicks = 1 << 26, kMostHeads = 1 << 16;   // the kernels' indexes stay ints
+bool rows_ok(int n, const int32_t* positions, const int32_t* row_seq, int nseq, int nkv) {
+  return n >= 1 && n <= kMostRows && positions && nseq >= 1 && (row_seq || nseq >= n) && nkv >= 1 && nkv <= kMostHeads;
 }
 }  // namespace
 
@@ -17,8 +18,8 @@ extern "C" {
 int op_kv_extend(int nseq, const int32_t* ctx_lens, const int32_t* new_lens, int32_t* bt, int bt_stride, int num_blocks,
                  const int32_t* free_blocks, int nfree, const int32_t* free_at, int n, int32_t* held, int32_t* cu_seqlens,
                  int32_t* positions, int32_t* row_seq, int64_t* slots, int32_t* free_next, uint32_t* err, void* stream) {
-  if (nseq < 1 || nseq == 0x7fffffff || !ctx_lens || !new_lens || !table_ok(bt, bt_stride) || num_blocks < 1 || nfree < 0 ||
-      (nfree > 0 && !free_blocks) || !free_at || n < 1 || !held || !cu_seqlens || !positions || !row_seq || !slots ||
+  if (nseq < 1 || nseq > kMostRows || !ctx_lens || !new_lens || !table_ok(bt, bt_stride) || num_blocks < 1 || nfree < 0 ||
+      (nfree > 0 && !free_blocks) || !free_at || n < 1 || n > kMostRows || !held || !cu_seqlens || !positions || !row_seq || !slots ||
       !free_next)
     return MBT_ERR_BAD_ARG;
   KvExtendArgs a = {};
@@ -31,7 +32,7 @@ int op_kv_extend(int nseq, const int32_t* ctx_lens, const int32_t* new_lens, int
 int op_key_bounds(int n, const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
                   int nkv, int d, const void* kpool, int kv_dtype, int num_blocks, int8_t* bounds, float* scales,
                   uint32_t* err, void* stream) {
-  if (!rows_ok(n, positions, row_seq, nseq) || !table_ok(bt, bt_stride) || nkv < 1 || (d != 64 && d != 128) || !kpool ||
+  if (!rows_ok(n, positions, row_seq, nseq, nkv) || !table_ok(bt, bt_stride) || (d != 64 && d != 128) || !kpool ||
       !cache_ok(kv_dtype) || num_blocks < 1 || !bounds || !scales || !aligned16(kpool) || !aligned16(bounds))
     return MBT_ERR_BAD_ARG;
   int sms = 0;
@@ -48,7 +49,7 @@ size_t op_block_select_scratch(int n, int nkv, int bt_stride, int k) {
   int sms = 0;
   BlockSelectArgs a = {};
   a.n = n; a.nkv = nkv; a.bt_stride = bt_stride; a.k = k;
-  if (n < 1 || nkv < 1 || bt_stride < 1 || k < 1 || device_setup(&sms) != MBT_OK || block_select_plan(&a, sms) != cudaSuccess)
+  if (n < 1 || nkv < 1 || bt_stride < 1 || bt_stride > kMostPicks || k < 1 || device_setup(&sms) != MBT_OK || block_select_plan(&a, sms) != cudaSuccess)
     return 0;
   return block_select_scratch(a);
 }
@@ -57,9 +58,9 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
                     const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
                     int num_blocks, int keep_first, int keep_last, int k, int32_t* sel, void* scratch, size_t scratch_bytes,
                     uint32_t* err, void* stream) {
-  if (!rows_ok(n, positions, row_seq, nseq) || !q || !heads_ok(nq, nkv, d) || !bounds || !scales ||
+  if (!rows_ok(n, positions, row_seq, nseq, nkv) || !q || !heads_ok(nq, nkv, d) || !bounds || !scales ||
       !table_ok(bt, bt_stride) || num_blocks < 1 || keep_first < 0 || keep_last < 1 ||
-      (long long)keep_first + keep_last > k || !sel || !aligned16(q) || !aligned16(bounds) || !aligned16(scratch))
+      (long long)keep_first + keep_last > k || k > kMostPicks || !sel || !aligned16(q) || !aligned16(bounds) || !aligned16(scratch))
     return MBT_ERR_BAD_ARG;
   int sms = 0;
   const int rc = device_setup(&sms);
@@ -83,8 +84,8 @@ int op_block_attention(int n, const float* q, int nq, int nkv, int d, const void
                        float k_scale, float v_scale, const int32_t* positions, const int32_t* row_seq, int nseq,
                        const int32_t* bt, int bt_stride, const int32_t* sel, int k, int num_blocks, float* out,
                        uint32_t* err, void* stream) {
-  if (!rows_ok(n, positions, row_seq, nseq) || !q || !heads_ok(nq, nkv, d) || !kpool || !vpool || !cache_ok(kv_dtype) ||
-      !scale_ok(k_scale) || !scale_ok(v_scale) || !table_ok(bt, bt_stride) || !sel || k < 1 || num_blocks < 1 || !out ||
+  if (!rows_ok(n, positions, row_seq, nseq, nkv) || !q || !heads_ok(nq, nkv, d) || !kpool || !vpool || !cache_ok(kv_dtype) ||
+      !scale_ok(k_scale) || !scale_ok(v_scale) || !table_ok(bt, bt_stride) || !sel || k < 1 || k > kMostPicks || num_blocks < 1 || !out ||
       !aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out))
     return MBT_ERR_BAD_ARG;
   int sms = 0;

@@ -104,10 +104,20 @@ def test_extend(cuda_lib, nseq, most, in_place):
     assert Extend(ctx, new, 10, 3100, n, at=3, seed=nseq).check(in_place) == 0
 
 
-@pytest.mark.parametrize("n", [1, 15, 300, 5000])
-def test_extend_prompts(cuda_lib, n):
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n", [1, 15, 300, 4087, 4088, 70000])
+def test_extend_prompts(cuda_lib, n, in_place):
     """One long prompt, then nothing new, then a sequence that begins on a block's edge; rows left over."""
-    assert Extend([0, 33, 32], [n, 0, 1], n // 16 + 4, n // 16 + 5, n + 9, seed=n).check() == 0
+    assert Extend([0, 33, 32], [n, 0, 1], n // 16 + 4, n // 16 + 5, n + 8, seed=n).check(in_place) == 0
+
+
+@pytest.mark.parametrize("nseq", [4096, 4097, 9000])
+def test_extend_many_sequences(cuda_lib, nseq):
+    """More sequences than the rows' CTAs keep edges of, most of them without rows."""
+    rng = np.random.default_rng(nseq)
+    new = np.where(rng.random(nseq) < 0.3, rng.integers(1, 40, nseq), 0)
+    e = Extend(rng.integers(0, 30, nseq), new, 5, 9000, int(new.sum()) + 100, seed=nseq)
+    assert e.n > 4096 and e.check() == 0 and e.check(True) == 0
 
 
 def test_extend_nothing(cuda_lib):
@@ -133,11 +143,11 @@ def test_extend_when_something_runs_out(cuda_lib, seed):
     e.check(seed % 2 == 1)
 
 
-def test_extend_replayed(cuda_lib):
+@pytest.mark.parametrize("nseq,steps", [(70, 40), (4200, 5)])
+def test_extend_replayed(cuda_lib, nseq, steps):
     """Captured in place: each replay adds a token to every sequence and goes on in the free list."""
-    nseq, steps = 70, 40
     ctx = np.random.default_rng(1).integers(0, 50, nseq)
-    e = Extend(ctx, np.ones(nseq), 8, 400, nseq + 2, at=2)
+    e = Extend(ctx, np.ones(nseq), 8, 6 * nseq, nseq + 2, at=2)
     a = {k: dev(v) for k, v in dict(ctx=e.ctx, new=e.new, bt=e.bt, free=e.free, at=[2], cu=np.zeros(nseq + 1),
                                     positions=np.zeros(e.n), row_seq=np.zeros(e.n)).items()}
     slots, err = dev(np.zeros(e.n), torch.int64), dev([0])
@@ -322,6 +332,12 @@ def test_select_tables_of_two_launches(cuda_lib, held, k):
     call = lambda scratch: capi.op_block_select(*t[:1], 2, *t[1:], c.nb, 0, 1, sel, scratch=scratch)
     call(own)
     assert np.array_equal(sel.cpu().numpy(), want)
+    for stream in (torch.cuda.Stream(), torch.cuda.current_stream().cuda_stream):      # as an object and as a handle
+        sel.zero_()
+        torch.cuda.synchronize()
+        capi.op_block_select(*t[:1], 2, *t[1:], c.nb, 0, 1, sel, stream=stream)
+        torch.cuda.synchronize()
+        assert np.array_equal(sel.cpu().numpy(), want)
     if size:
         with pytest.raises(capi.MbtError) as e:
             call(own[:size - 1])

@@ -120,23 +120,23 @@ ATTEND = dict(n=4, q=P, nq=8, nkv=2, d=64, kpool=P, vpool=P, kv_dtype=0, k_scale
               row_seq=None, nseq=4, bt=P, bt_stride=3, sel=P, k=2, num_blocks=5, out=P, err=None, stream=None)
 BAD = {
     "op_kv_extend": (EXTEND, [
-        ("nseq", 0), ("nseq", -3), ("nseq", 2 ** 31 - 1), ("ctx", None), ("new", None), ("bt", None), ("bt_stride", 0),
+        ("nseq", 0), ("nseq", -3), ("nseq", 2 ** 31 - 1), ("n", 2 ** 30 + 1), ("ctx", None), ("new", None), ("bt", None), ("bt_stride", 0),
         ("bt_stride", (1 << 26) + 1), ("num_blocks", 0), ("free", None), ("nfree", -1), ("free_at", None), ("n", 0),
         ("held", None), ("cu", None), ("positions", None), ("row_seq", None), ("slots", None), ("free_next", None)]),
     "op_key_bounds": (BOUNDS, [
         ("n", 0), ("positions", None), ("nseq", 0), ("nseq", 3), ("bt", None), ("bt_stride", 0), ("bt_stride", (1 << 26) + 1),
-        ("nkv", 0), ("d", 32), ("d", 96), ("kpool", None), ("kpool", ODD), ("kv_dtype", 2), ("kv_dtype", 4),
+        ("nkv", 0), ("nkv", (1 << 16) + 1), ("d", 32), ("d", 96), ("kpool", None), ("kpool", ODD), ("kv_dtype", 2), ("kv_dtype", 4),
         ("kv_dtype", -1), ("num_blocks", 0), ("bounds", None), ("bounds", ODD), ("scales", None)]),
     "op_block_select": (SELECT, [
         ("n", 0), ("q", None), ("q", ODD), ("nq", 0), ("nq", 7), ("nq", 34), ("nkv", 0), ("d", 80), ("bounds", None),
         ("bounds", ODD), ("scales", None), ("positions", None), ("nseq", 0), ("nseq", 3), ("bt", None), ("bt_stride", 0),
-        ("num_blocks", 0), ("keep_first", -1), ("keep_last", 0), ("k", 1), ("k", 0), ("keep_first", 2 ** 31 - 1),
+        ("num_blocks", 0), ("keep_first", -1), ("keep_last", 0), ("k", 1), ("k", 0), ("keep_first", 2 ** 31 - 1), ("k", (1 << 26) + 1),
         ("sel", None), ("scratch", ODD), ("bt_stride", (1 << 26) + 1)]),
     "op_block_attention": (ATTEND, [
         ("n", 0), ("q", None), ("q", ODD), ("nq", 0), ("nq", 7), ("nq", 34), ("nkv", 0), ("d", 256), ("kpool", None),
         ("kpool", ODD), ("vpool", None), ("vpool", ODD), ("kv_dtype", 2), ("kv_dtype", 4), ("k_scale", 0.0),
         ("k_scale", 2.0 ** -65), ("v_scale", float("nan")), ("v_scale", 2.0 ** 65), ("positions", None), ("nseq", 0),
-        ("nseq", 3), ("bt", None), ("bt_stride", 0), ("bt_stride", (1 << 26) + 1), ("sel", None), ("k", 0),
+        ("nseq", 3), ("bt", None), ("bt_stride", 0), ("bt_stride", (1 << 26) + 1), ("sel", None), ("k", 0), ("k", (1 << 26) + 1),
         ("num_blocks", 0), ("out", None), ("out", ODD)]),
 }
 
