@@ -415,12 +415,13 @@ def _pools(fn: str, k, v, dev: int, nkv: int, d: int, num_blocks: int, kv_dtype:
         raise MbtError(fn, -1)
     need = (num_blocks + 1) * nkv * unit
     for name, t in (("kpool", k), ("vpool", v)):
+        if isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous() and t.nbytes >= need:
+            continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be a contiguous device tensor")
         if t.get_device() != dev:
             raise ValueError(f"{fn}: {name} is on another device than the current one")
-        if t.nbytes < need:
-            raise ValueError(f"{fn}: {name} is smaller than num_blocks + 1 blocks")
+        raise ValueError(f"{fn}: {name} is smaller than num_blocks + 1 blocks")
     return k.data_ptr(), v.data_ptr()
 
 

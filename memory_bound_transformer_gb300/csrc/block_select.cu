@@ -312,22 +312,26 @@ __device__ __forceinline__ void weigh(SelQuery<D>& m, uint32_t big, int G) {
   __syncthreads();
 }
 
+// Table entry i + lane of a run of cnt from j0 on; past its end block 0, not used.
+__device__ __forceinline__ int sel_entry(const SelRow& w, int j0, int cnt, int i) {
+  i += threadIdx.x & 31;
+  return i < cnt ? __ldg(w.table + j0 + i) : 0;
+}
+__device__ __forceinline__ int first_entry(const SelRow& w, int j0, int cnt) { return sel_entry(w, j0, cnt, threadIdx.x & ~31); }
+
 // Keys of the context's blocks [j0, j0 + cnt), 32 at a time per warp: a range is
-// read by 16 or 8 neighbouring lanes. put(place, key).
+// read by 16 or 8 neighbouring lanes. next: first_entry. put(place, key).
 template <int D, int WARPS, class Put>
-__device__ __forceinline__ void score_blocks(const SelQuery<D>& m, const BlockSelectArgs& a, const SelRow& w, int j0, int cnt, Put put) {
+__device__ __forceinline__ void score_blocks(const SelQuery<D>& m, const BlockSelectArgs& a, const SelRow& w, int j0, int cnt, int next, Put put) {
   constexpr int REC = 2 * D, LANES = REC / 16, PER = 32 / LANES;      // bytes of a range, lanes on one, ranges per load
   constexpr int BATCH = kSelLoads * PER, SAME = LANES / kSelLoads;    // ranges per round of loads, lanes left with one's sum
   const int lane = threadIdx.x & 31, l = lane % LANES, side = l < LANES / 2 ? -1 : 1;
   const unsigned char* ranges = reinterpret_cast<const unsigned char*>(a.bounds) + 16 * l;
   const uint4 w0 = *reinterpret_cast<const uint4*>(m.digit[0] + 16 * l), w1 = *reinterpret_cast<const uint4*>(m.digit[1] + 16 * l);
-  int i0 = 32 * (threadIdx.x >> 5);
-  auto entry = [&](int i) { return i + lane < cnt ? __ldg(w.table + j0 + i + lane) : 0; };   // past the end: block 0, not used
-  int next = entry(i0);
 #pragma unroll 1
-  for (; i0 < cnt; i0 += 32 * WARPS) {
+  for (int i0 = threadIdx.x & ~31; i0 < cnt; i0 += 32 * WARPS) {
     int id = next;
-    next = entry(i0 + 32 * WARPS);
+    next = sel_entry(w, j0, cnt, i0 + 32 * WARPS);
     if ((uint32_t)id > (uint32_t)a.num_blocks) {
       set_err(a.err, MBT_DEV_BLOCK_RANGE);
       id = a.num_blocks;
@@ -569,10 +573,11 @@ __global__ void __launch_bounds__(32 * kSelWarps, kSelPerSm) block_select_kernel
   const bool shared = a.cluster > 1;
   if (shared) cluster_arrive();
   const int share = (w.held + a.cluster - 1) / a.cluster, j0 = min(rank * share, w.held), cnt = min(share, w.held - j0);
+  const int first = first_entry(w, j0, cnt);                          // under way while the weights are made
   clear(chooser, threads);
   weigh<D, kSelWarps>(mem, big, a.nq / a.nkv);
   if (shared) cluster_wait();
-  score_blocks<D, kSelWarps>(mem, a, w, j0, cnt, [&](int i, uint32_t key) {
+  score_blocks<D, kSelWarps>(mem, a, w, j0, cnt, first, [&](int i, uint32_t key) {
     if (shared) st_dsmem_u32(keys + j0 + i, 0, key);
     else keys[i] = key;
   });
@@ -597,6 +602,7 @@ __global__ void __launch_bounds__(32 * kPartWarps, 2) block_candidates_kernel(co
   __shared__ SelQuery<D> mem;
   __shared__ Chooser chooser;
   const int part = (int)(blockIdx.x % (unsigned)a.parts), pair = (int)(blockIdx.x / (unsigned)a.parts);
+  pdl_launch_dependents();
   const uint32_t big = load_group<D, kPartWarps>(mem, a, pair / a.nkv, pair % a.nkv);
   const SelRow w = sel_row(a, pair);
   if (w.held <= a.k) return;
@@ -604,9 +610,10 @@ __global__ void __launch_bounds__(32 * kPartWarps, 2) block_candidates_kernel(co
   const int take = min(a.k, share);
   uint32_t* ck = a.keys + (size_t)pair * a.cand + (size_t)part * take;
   int* cj = a.places + (size_t)pair * a.cand + (size_t)part * take;
+  const int first = first_entry(w, j0, cnt);
   clear(chooser, threads);
   weigh<D, kPartWarps>(mem, big, a.nq / a.nkv);
-  score_blocks<D, kPartWarps>(mem, a, w, j0, cnt, [&](int i, uint32_t key) { keys[i] = key; });
+  score_blocks<D, kPartWarps>(mem, a, w, j0, cnt, first, [&](int i, uint32_t key) { keys[i] = key; });
   __syncthreads();
   if (cnt <= take) {
     for (int i = threadIdx.x; i < cnt; i += threads) { ck[i] = keys[i]; cj[i] = j0 + i; }
@@ -621,6 +628,7 @@ __global__ void __launch_bounds__(32 * kPartWarps) block_merge_kernel(const Bloc
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ Chooser chooser;
   const int pair = (int)blockIdx.x;
+  pdl_wait();                                                         // every CTA: the end of this launch is the end of both
   const SelRow w = sel_row(a, pair);
   int* sel = a.sel + (size_t)pair * a.k;
   if (w.bad && threadIdx.x == 0 && w.h == 0) set_err(a.err, MBT_DEV_POS_RANGE);
@@ -648,7 +656,7 @@ __global__ void __launch_bounds__(32 * kPartWarps) block_merge_kernel(const Bloc
     choose<kPartWarps>(chooser, n, a.k, [&](int i) { return keys[i]; }, put);
   } else {
     __syncthreads();
-    choose<kPartWarps>(chooser, n, a.k, [&](int i) { return __ldg(ck + i); }, put);
+    choose<kPartWarps>(chooser, n, a.k, [&](int i) { return ck[i]; }, put);
   }
 }
 
@@ -715,8 +723,8 @@ cudaError_t launch_block_select(const BlockSelectArgs& in, void* scratch, cudaSt
       launch_ex(a.d == 64 ? (const void*)block_candidates_kernel<64> : (const void*)block_candidates_kernel<128>,
                 dim3((unsigned)(pairs * a.parts)), dim3(32 * kPartWarps), share * sizeof(uint32_t), s, p, false, -1);
   if (e != cudaSuccess) return e;
-  return launch_ex((const void*)block_merge_kernel, dim3((unsigned)pairs), dim3(32 * kPartWarps),
-                   (size_t)std::min<long long>(a.cand * 4LL, kMergeSmem), s, p, false, -1);
+  return launch_pdl((const void*)block_merge_kernel, dim3((unsigned)pairs), dim3(32 * kPartWarps),
+                    (size_t)std::min<long long>(a.cand * 4LL, kMergeSmem), s, p);
 }
 
 }  // namespace mbt
