@@ -194,6 +194,7 @@ constexpr int kSelPerSm = 4;                 // such CTAs per SM (64 registers a
 constexpr int kSelCluster = 8;               // most CTAs of a cluster
 constexpr int kSelOne = 4096;                // widest table for which one CTA has all keys
 constexpr int kPartWarps = 16;               // warps of a CTA that scores a part of a long context, two per SM
+constexpr int kMergeWarps = 32;              // of one that chooses among the parts' candidates
 constexpr int kPartMost = 8192;              // most blocks of a part
 constexpr int kMergeSmem = 192 << 10;        // shared memory for the candidates of all parts
 constexpr int kSelLoads = 8;                 // 16-byte loads that a lane has under way
@@ -417,7 +418,7 @@ __device__ __forceinline__ void find_bin(const uint32_t* bins, uint32_t need, in
 // Shared memory of the choice.
 struct Chooser {
   __align__(16) uint32_t hist[2][kBins];
-  uint32_t red[kPartWarps][3], list[2][32], listed;
+  uint32_t red[kMergeWarps][3], list[2][32], listed;
 };
 __device__ __forceinline__ void clear(Chooser& m, int threads) {      // before the first barrier ahead of choose()
   for (int i = threadIdx.x; i < kBins / 2; i += threads) reinterpret_cast<uint4*>(m.hist)[i] = make_uint4(0, 0, 0, 0);
@@ -623,8 +624,8 @@ __global__ void __launch_bounds__(32 * kPartWarps, 2) block_candidates_kernel(co
                      [&](uint32_t at, uint32_t i) { ck[at] = keys[i]; cj[at] = j0 + (int)i; });
 }
 
-__global__ void __launch_bounds__(32 * kPartWarps) block_merge_kernel(const BlockSelectArgs a) {
-  constexpr int threads = 32 * kPartWarps;
+__global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const BlockSelectArgs a) {
+  constexpr int threads = 32 * kMergeWarps;
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ Chooser chooser;
   const int pair = (int)blockIdx.x;
@@ -647,16 +648,23 @@ __global__ void __launch_bounds__(32 * kPartWarps) block_merge_kernel(const Bloc
   clear(chooser, threads);
   auto put = [&](uint32_t at, uint32_t i) { sel[at] = cj[i]; };
   if (n * 4LL <= kMergeSmem) {
-    for (int i = threadIdx.x; i < n; i += threads) keys[i] = ck[i];
+    for (int i = threadIdx.x; i < n; i += 8 * threads) {
+      uint32_t k8[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) k8[u] = i + u * threads < n ? ck[i + u * threads] : 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i + u * threads < n) keys[i + u * threads] = k8[u];
+    }
     __syncthreads();
     if (n == a.k) {                                                   // cannot be fewer: the k best are among them
       for (int i = threadIdx.x; i < n; i += threads) put(i, i);
       return;
     }
-    choose<kPartWarps>(chooser, n, a.k, [&](int i) { return keys[i]; }, put);
+    choose<kMergeWarps>(chooser, n, a.k, [&](int i) { return keys[i]; }, put);
   } else {
     __syncthreads();
-    choose<kPartWarps>(chooser, n, a.k, [&](int i) { return ck[i]; }, put);
+    choose<kMergeWarps>(chooser, n, a.k, [&](int i) { return ck[i]; }, put);
   }
 }
 
@@ -723,7 +731,7 @@ cudaError_t launch_block_select(const BlockSelectArgs& in, void* scratch, cudaSt
       launch_ex(a.d == 64 ? (const void*)block_candidates_kernel<64> : (const void*)block_candidates_kernel<128>,
                 dim3((unsigned)(pairs * a.parts)), dim3(32 * kPartWarps), share * sizeof(uint32_t), s, p, false, -1);
   if (e != cudaSuccess) return e;
-  return launch_pdl((const void*)block_merge_kernel, dim3((unsigned)pairs), dim3(32 * kPartWarps),
+  return launch_pdl((const void*)block_merge_kernel, dim3((unsigned)pairs), dim3(32 * kMergeWarps),
                     (size_t)std::min<long long>(a.cand * 4LL, kMergeSmem), s, p);
 }
 
