@@ -192,12 +192,20 @@ struct Picks {
   }
 };
 
-template <int D, int KV>
+// FEW: at most four heads over a BF16 cache. Their three parts then fit the MMA's
+// 16 rows: rows 0..3 the high, 8..11 the middle and 4..7 the low ones, whose
+// products lanes 16 apart exchange.
+template <int D, int KV, bool FEW>
 struct BlockWarp {
   using L = Lay<D, KV>;
   static constexpr bool BF = L::BF;
+  static constexpr bool LOW = BF && !FEW;                             // low parts in MMAs of their own
   float m, l, o[L::NT][2];
 
+  // The parts of lane's head as those of its two MMA rows.
+  static __device__ __forceinline__ void rows(uint32_t& hi, uint32_t& mid, uint32_t lo, int lane) {
+    if (lane & 16) { hi = lo; mid = 0; }
+  }
   __device__ __forceinline__ void start() {
     m = -INFINITY;
     l = 0.f;
@@ -245,7 +253,7 @@ struct BlockWarp {
       auto product = [&](int st, int i, uint32_t b0, uint32_t b1, const uint4& a, const uint2& z) {
         if (st == 0) mma<BF, true>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
         else mma<BF>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
-        if constexpr (BF) mma<BF>(acc[i], z.x, 0u, z.y, 0u, b0, b1);
+        if constexpr (LOW) mma<BF>(acc[i], z.x, 0u, z.y, 0u, b0, b1);
       };
       if constexpr (KV == KV_FP4) {
 #pragma unroll
@@ -269,7 +277,7 @@ struct BlockWarp {
           const int st = p * PS + q;
           const uint4 a = frag[st * 32 + lane];
           uint2 z = make_uint2(0, 0);
-          if constexpr (BF) z = frag_lo[st * 32 + lane];
+          if constexpr (LOW) z = frag_lo[st * 32 + lane];
 #pragma unroll
           for (int i = 0; i < 2 * L::TB; ++i) {
             uint32_t b0, b1;
@@ -289,6 +297,7 @@ struct BlockWarp {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         s[i][e] = acc[i][e] + acc[i][e + 2];
+        if constexpr (FEW) s[i][e] += __shfl_xor_sync(0xffffffffu, s[i][e], 16);
         if constexpr (BF) s[i][e] += s[i][e] - s[i][e];               // of a key that is not finite: NaN
       }
   }
@@ -320,6 +329,7 @@ struct BlockWarp {
       const float p0 = ex2(fmaf(s[i][0] - mu, fac, UP)), p1 = ex2(fmaf(s[i][1] - mu, fac, UP));
       sum += p0 + p1;
       split<BF>(p0, p1, pa[i][0], pa[i][1], pa[i][2]);
+      if constexpr (FEW) rows(pa[i][0], pa[i][1], pa[i][2], lane);
     }
     l = fmaf(l, al, sum);
     return al;
@@ -380,7 +390,7 @@ struct BlockWarp {
       for (int b = 0; b < L::TB; ++b) {
         if (b == 0) mma<BF, true>(acc, pa[0][0], pa[0][1], pa[1][0], pa[1][1], f0[0], f1[0]);
         else mma<BF>(acc, pa[2 * b][0], pa[2 * b][1], pa[2 * b + 1][0], pa[2 * b + 1][1], f0[b], f1[b]);
-        if constexpr (BF) mma<BF>(acc, pa[2 * b][2], 0u, pa[2 * b + 1][2], 0u, f0[b], f1[b]);
+        if constexpr (LOW) mma<BF>(acc, pa[2 * b][2], 0u, pa[2 * b + 1][2], 0u, f0[b], f1[b]);
       }
       o[c][0] = fmaf(o[c][0], al, acc[0] + acc[2]);
       o[c][1] = fmaf(o[c][1], al, acc[1] + acc[3]);
@@ -449,7 +459,9 @@ struct BlockWarp {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int ch = L::v_channel(2 * t + e, c);
-        so[g * D + ch] = spec ? o[c][e] + spec[ch] : o[c][e];
+        float x = o[c][e];
+        if constexpr (FEW) x += __shfl_xor_sync(0xffffffffu, x, 16);
+        so[g * D + ch] = spec ? x + spec[ch] : x;
       }
   }
 };
@@ -457,12 +469,13 @@ struct BlockWarp {
 // One cluster of 1..8 CTAs per (row, KV head, group of eight query heads); its
 // warps take the row's blocks in turn and the CTAs' parts merge through
 // distributed shared memory. One launch, no scratch.
-template <int D, int KV>
+template <int D, int KV, bool FEW>
 __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_attention_kernel(const BlockAttnArgs a) {
   using L = Lay<D, KV>;
+  using Warp = BlockWarp<D, KV, FEW>;
   constexpr bool BF = L::BF;
   __shared__ __align__(16) uint4 frag[L::KS * 32];
-  __shared__ __align__(16) uint2 frag_lo[BF ? L::KS * 32 : 1];
+  __shared__ __align__(16) uint2 frag_lo[Warp::LOW ? L::KS * 32 : 1];
   extern __shared__ __align__(128) unsigned char ring[];              // [warp][K stages, V stages]
   float* so = reinterpret_cast<float*>(ring);                         // then [warp][head][D]
   __shared__ float sm_m[kBaWarps][kBaHeads], sm_l[kBaWarps][kBaHeads], cta_m[kBaHeads], cta_l[kBaHeads], sm_fac[kBaHeads];
@@ -471,7 +484,7 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   const int hb = pair % a.hblocks, h = pair / a.hblocks % a.nkv, row = pair / a.hblocks / a.nkv;
   const int G = a.nq / a.nkv, gn = min(kBaHeads, G - hb * kBaHeads);
   const size_t head0 = (size_t)row * a.nq + (size_t)h * G + hb * kBaHeads;
-  const int g = lane >> 2, t = lane & 3;
+  const int g = (lane >> 2) & (FEW ? 3 : 7), t = lane & 3;             // the lane's head
 
   Picks pk;
   const int pos = a.positions[row], seq = a.row_seq ? a.row_seq[row] : row;
@@ -498,7 +511,7 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   pk.mask = 0;
   const unsigned char* kpool = reinterpret_cast<const unsigned char*>(a.kpool);
   const unsigned char* vpool = reinterpret_cast<const unsigned char*>(a.vpool);
-  BlockWarp<D, KV> w;
+  Warp w;
   unsigned char* mine = ring + warp * L::RING;
   const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(mine);
   int blk[kBaStages][L::TB], live[kBaStages][L::TB];                  // of the steps under way
@@ -542,9 +555,13 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
     uint32_t h0, h1, m0, m1, l0, l1;
     split<BF>(x[4 * st] * up, x[4 * st + 1] * up, h0, m0, l0);
     split<BF>(x[4 * st + 2] * up, x[4 * st + 3] * up, h1, m1, l1);
+    if constexpr (FEW) {
+      Warp::rows(h0, m0, l0, lane);
+      Warp::rows(h1, m1, l1, lane);
+    }
     if (st % warps == warp) {
       frag[st * 32 + lane] = make_uint4(h0, m0, h1, m1);
-      if constexpr (BF) frag_lo[st * 32 + lane] = make_uint2(l0, l1);
+      if constexpr (Warp::LOW) frag_lo[st * 32 + lane] = make_uint2(l0, l1);
     }
   }
   __syncthreads();
@@ -646,18 +663,18 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   cluster_sync_all();                                                 // stay resident until the others have read
 }
 
-template <int D, int KV>
+template <int D, int KV, bool FEW = false>
 cudaError_t ba_launch(const BlockAttnArgs& a, cudaStream_t s) {
   BlockAttnArgs args = a;
   void* p[] = {&args};
   const long long grid = (long long)a.n * a.nkv * a.hblocks * a.cluster;
-  return launch_ex((const void*)block_attention_kernel<D, KV>, dim3((unsigned)grid), dim3(32 * a.warps), a.warps * Lay<D, KV>::WARP, s,
-                   p, false, 100, a.cluster > 1 ? a.cluster : 0);
+  return launch_ex((const void*)block_attention_kernel<D, KV, FEW>, dim3((unsigned)grid), dim3(32 * a.warps),
+                   a.warps * Lay<D, KV>::WARP, s, p, false, 100, a.cluster > 1 ? a.cluster : 0);
 }
 
-template <int D, int KV>
+template <int D, int KV, bool FEW = false>
 cudaError_t ba_init() {
-  return cudaFuncSetAttribute((const void*)block_attention_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute((const void*)block_attention_kernel<D, KV, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kBaWarps * Lay<D, KV>::WARP);
 }
 
@@ -672,6 +689,7 @@ cudaError_t launch_block_attention(const BlockAttnArgs& in, int num_sms, cudaStr
   a.cluster = (int)std::max<long long>(1, std::min<long long>(kBaCluster, want));
   a.warps = (int)std::max<long long>(1, std::min<long long>(kBaWarps, (long long)ba_per_sm(a.d) * num_sms / pairs));
   const bool wide = a.d == 128;
+  if (a.kv == KV_BF16 && a.nq / a.nkv <= 4) return wide ? ba_launch<128, KV_BF16, true>(a, s) : ba_launch<64, KV_BF16, true>(a, s);
   if (a.kv == KV_BF16) return wide ? ba_launch<128, KV_BF16>(a, s) : ba_launch<64, KV_BF16>(a, s);
   if (a.kv == KV_E4M3) return wide ? ba_launch<128, KV_E4M3>(a, s) : ba_launch<64, KV_E4M3>(a, s);
   return wide ? ba_launch<128, KV_FP4>(a, s) : ba_launch<64, KV_FP4>(a, s);
@@ -680,6 +698,8 @@ cudaError_t launch_block_attention(const BlockAttnArgs& in, int num_sms, cudaStr
 cudaError_t block_attention_init() {
   cudaError_t e = ba_init<64, KV_BF16>();
   if (e == cudaSuccess) e = ba_init<128, KV_BF16>();
+  if (e == cudaSuccess) e = ba_init<64, KV_BF16, true>();
+  if (e == cudaSuccess) e = ba_init<128, KV_BF16, true>();
   if (e == cudaSuccess) e = ba_init<64, KV_E4M3>();
   if (e == cudaSuccess) e = ba_init<128, KV_E4M3>();
   if (e == cudaSuccess) e = ba_init<64, KV_FP4>();

@@ -501,8 +501,8 @@ ALL = ["bf16", "fp8", "fp4"]
 
 
 @pytest.mark.parametrize("kind", ALL)
-@pytest.mark.parametrize("nq,nkv,d", [(32, 8, 128), (1, 1, 64), (4, 2, 64), (5, 1, 128), (16, 1, 128), (9, 1, 64), (40, 8, 64),
-                                      (39, 3, 128)])
+@pytest.mark.parametrize("nq,nkv,d", [(32, 8, 128), (1, 1, 64), (4, 2, 64), (3, 1, 128), (5, 1, 128), (16, 1, 128), (9, 1, 64),
+                                      (40, 8, 64), (12, 4, 64), (39, 3, 128)])
 def test_attention(cuda_lib, kind, nq, nkv, d):
     """Contexts from one token on, all or a few of their blocks."""
     Attend(kind, nq, nkv, d, [1, 2, 15, 16, 17, 31, 33, 100, 160, 161, 700], 10, seed=nq + d).check()
@@ -563,11 +563,13 @@ def test_attention_never_sees_past_a_position(cuda_lib, kind):
 
 
 @pytest.mark.parametrize("kind", ALL)
-def test_attention_values_that_are_not_finite(cuda_lib, kind):
+@pytest.mark.parametrize("nq", [8, 14])
+def test_attention_values_that_are_not_finite(cuda_lib, kind, nq):
     """A key: its rows. A value: its channel of the rows that see it, an infinity as such. Others keep every bit."""
-    c = Attend(kind, 8, 2, 64, [700, 700, 700], 8, seed=26)
+    h = nq // 2                                                      # heads of the second KV head from here on
+    c = Attend(kind, nq, 2, 64, [700, 700, 700], 8, seed=26)
     c.sel[1] = c.sel[0]
-    want = c.run()[0].reshape(3, 8, 64)
+    want = c.run()[0].reshape(3, nq, 64)
     nan = {"bf16": 0x7FC1, "fp8": 0x7F, "fp4": 0x7F}[kind]
     blk = c.bt[0, c.sel[0, 1, 2]]
     raw = c.vp.copy()
@@ -578,15 +580,15 @@ def test_attention_values_that_are_not_finite(cuda_lib, kind):
         raw[blk, 1, 5, 33] = nan
         hit = np.arange(64) == 33
     c.vp, keep = raw, c.vp
-    got = c.run()[0].reshape(3, 8, 64)
-    assert np.isnan(got[0, 4:][:, hit]).all()
-    got[0, 4:][:, hit] = want[0, 4:][:, hit]
+    got = c.run()[0].reshape(3, nq, 64)
+    assert np.isnan(got[0, h:][:, hit]).all()
+    got[0, h:][:, hit] = want[0, h:][:, hit]
     assert np.array_equal(got, want)
     if kind == "bf16":
         raw[blk, 1, 5, 33], raw[blk, 1, 6, 40], raw[blk, 1, 7, 40], raw[blk, 1, 15, 63] = 0x7F80, 0x7F80, 0xFF80, 0xFF80
-        got = c.run()[0].reshape(3, 8, 64)
-        assert np.all(got[0, 4:, 33] == np.inf) and np.isnan(got[0, 4:, 40]).all() and np.all(got[0, 4:, 63] == -np.inf)
-        got[0, 4:][:, [33, 40, 63]] = want[0, 4:][:, [33, 40, 63]]
+        got = c.run()[0].reshape(3, nq, 64)
+        assert np.all(got[0, h:, 33] == np.inf) and np.isnan(got[0, h:, 40]).all() and np.all(got[0, h:, 63] == -np.inf)
+        got[0, h:][:, [33, 40, 63]] = want[0, h:][:, [33, 40, 63]]
         assert np.array_equal(got, want)
     c.vp, raw = keep, c.kp.copy()
     for bad in ((nan, 0x7F80, 0xFF80) if kind == "bf16" else (nan,)):
@@ -595,19 +597,20 @@ def test_attention_values_that_are_not_finite(cuda_lib, kind):
             c.kp.reshape(c.nb + 1, 2, -1)[blk, 1, 16 * 32 + 5 * 4 + 2] = bad
         else:
             c.kp[blk, 1, 5, 33] = bad
-        got = c.run()[0].reshape(3, 8, 64)
-        assert np.isnan(got[0, 4:]).all()
-        got[0, 4:] = want[0, 4:]
+        got = c.run()[0].reshape(3, nq, 64)
+        assert np.isnan(got[0, h:]).all()
+        got[0, h:] = want[0, h:]
         assert np.array_equal(got, want)
 
 
 @pytest.mark.parametrize("kind", ALL)
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
-def test_attention_queries_that_are_not_finite(cuda_lib, kind, bad):
-    c = Attend(kind, 8, 2, 64, [700, 20], 8, seed=27)
-    want = c.run()[0].reshape(2, 8, 64)
+@pytest.mark.parametrize("nq", [8, 14])
+def test_attention_queries_that_are_not_finite(cuda_lib, kind, bad, nq):
+    c = Attend(kind, nq, 2, 64, [700, 20], 8, seed=27)
+    want = c.run()[0].reshape(2, nq, 64)
     c.q[1, 5, 9] = bad
-    got = c.run()[0].reshape(2, 8, 64)
+    got = c.run()[0].reshape(2, nq, 64)
     assert np.isnan(got[1, 5]).all()
     got[1, 5] = want[1, 5]
     assert np.array_equal(got, want)
@@ -615,9 +618,10 @@ def test_attention_queries_that_are_not_finite(cuda_lib, kind, bad):
 
 @pytest.mark.parametrize("kind", ALL)
 @pytest.mark.parametrize("scale", [0.0, 1e-44, 1e-30, 10.0, 100.0, 1e30])
-def test_attention_queries_of_every_size(cuda_lib, kind, scale):
+@pytest.mark.parametrize("nq", [8, 14])
+def test_attention_queries_of_every_size(cuda_lib, kind, scale, nq):
     """Even and one-hot softmaxes; heads of very different size in one group."""
-    c = Attend(kind, 8, 2, 128, [700, 20, 333], 40, seed=28)
+    c = Attend(kind, nq, 2, 128, [700, 20, 333], 40, seed=28)
     c.q[:, 1::2] *= np.float32(scale)
     if scale >= 100:                                                 # scores that fp32's own rounding does not reorder
         keep = np.zeros_like(c.q[:, 1::2])
@@ -626,9 +630,10 @@ def test_attention_queries_of_every_size(cuda_lib, kind, scale):
     c.check()
 
 
-def test_attention_bf16_values_of_every_size(cuda_lib):
+@pytest.mark.parametrize("nq", [8, 14])
+def test_attention_bf16_values_of_every_size(cuda_lib, nq):
     """Keys and values from the smallest to the largest BF16 numbers, in one block and over blocks."""
-    c = Attend("bf16", 8, 2, 64, [900] * 3, 30, seed=29, kg=1.0, vg=1.0)
+    c = Attend("bf16", nq, 2, 64, [900] * 3, 30, seed=29, kg=1.0, vg=1.0)
     rng = np.random.default_rng(30)
     v = bf16_decode(c.vp) * 2.0 ** rng.integers(-120, 100, c.vp.shape[:3] + (1,))
     c.vp = round_bf16(v.astype(np.float32))
