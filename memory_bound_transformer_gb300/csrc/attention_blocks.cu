@@ -4,24 +4,35 @@
 // maximum and sum of the softmax ("GPU Inference Internals", "The KV-Cache
 // Ledger": the bytes of the cache are what a decode step reads).
 //
-// What bounds it: every chosen block is read once, 2 x 16 tokens of d values, so
-// the work per value has to stay below what the SM issues meanwhile. A warp
-// takes whole blocks from the list, straight from memory into registers: no
-// shared memory, no barrier in the loop.
+// What bounds it: every chosen block is read once, 2 x 16 tokens of d values in
+// runs of 1 to 4 KB (a gather of those alone reaches 6.1 to 6.2 TB/s), so the work
+// per value has to stay below what the SM issues meanwhile.
 // * Queries and probabilities enter mma.sync.m16n8k16 as parts stacked on M: rows
 //   0..7 the high parts of the group's heads, rows 8..15 the next. Over a BF16
-//   cache they are three BF16 parts (24 bits; the third in a second MMA whose rows
-//   8..15 are zeros), over the narrow caches, whose values FP16 holds exactly, two
-//   FP16 parts (2^-22), probabilities relative to 2^-14 of the largest so that
-//   FP16's smallest steps lie at 2^-39 of it.
+//   cache they are three BF16 parts (24 bits; the third in a second MMA, or for up
+//   to four heads in the same one), over the narrow caches, whose values FP16 holds
+//   exactly, two FP16 parts (2^-22), probabilities relative to 2^-14 of the largest
+//   so that FP16's smallest steps lie at 2^-39 of it.
 // * The contraction may run over channels in any order: thread (g, t) of a warp
-//   takes 16-byte pieces of token g's key, and the queries are laid out the same
-//   way. V's pairs are two tokens of one channel, interleaved from two tokens'
-//   words. The score accumulators are the A fragments of P V as they stand.
+//   takes 16-byte pieces of a key, and the queries are laid out the same way. V's
+//   pairs are two tokens of one channel, interleaved from two tokens' words. The
+//   score accumulators are the A fragments of P V as they stand.
 // * The tensor core's fp32 accumulation truncates, so chains are short (d / 16
 //   steps for scores, a step's blocks for P V) and sums over steps are IEEE fp32.
-// * The loads of the next step's keys are under way while the softmax and P V of
-//   this one are done, its values' from there on.
+// * A warp takes whole blocks from the row's list and has rings of two steps of its
+//   own for K and for V, filled by 16-byte asynchronous copies and refilled as soon
+//   as read: no barrier in the loop. (Straight into registers, which hold one step,
+//   the e4m3 case below took 69 us against 66 at that stage.)
+// * Few (row, KV head) pairs are shared by clusters and many get a warp each, so
+//   that one wave of 12 warps per SM (16 at d = 64) holds them.
+// Measured in a graph, us: 64 rows of 32 + 2 x 8 heads of 128 over 64 BF16 blocks
+// 51 (5.3 TB/s; the copies alone 47), 128 rows 90 (6.0 TB/s); 64 rows of 64 + 2 x 8
+// over 128 e4m3 blocks 55 (copies 48); the same over 4-bit blocks 51 (copies 32: issue);
+// 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks
+// each 76 (issue, 250 a block); one row of 32 + 2 x 8 heads of 128 over 64 BF16 blocks
+// 8.8, of which 7.4 are the launch, four round trips (position, entry, table, block)
+// and the merge. A wave whose SMs hold three or four CTAs of three warps ends
+// unevenly: 20 % of the first case's cycles.
 #include <algorithm>
 
 #include "fp4.cuh"
@@ -663,13 +674,35 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   cluster_sync_all();                                                 // stay resident until the others have read
 }
 
+// CTAs of so many warps that an SM holds, by registers and by shared memory.
+template <int D, int KV, bool FEW>
+long long ba_places(int warps, int num_sms) {
+  using L = Lay<D, KV>;
+  constexpr int FIXED = L::KS * 32 * (BlockWarp<D, KV, FEW>::LOW ? 24 : 16) + 512 + 1024;   // fragments; sums; what a CTA is charged
+  return (long long)num_sms * std::min(ba_per_sm(D) / warps, (228 << 10) / (warps * L::WARP + FIXED));
+}
+
 template <int D, int KV, bool FEW = false>
-cudaError_t ba_launch(const BlockAttnArgs& a, cudaStream_t s) {
-  BlockAttnArgs args = a;
-  void* p[] = {&args};
-  const long long grid = (long long)a.n * a.nkv * a.hblocks * a.cluster;
-  return launch_ex((const void*)block_attention_kernel<D, KV, FEW>, dim3((unsigned)grid), dim3(32 * a.warps),
-                   a.warps * Lay<D, KV>::WARP, s, p, false, 100, a.cluster > 1 ? a.cluster : 0);
+cudaError_t ba_launch(const BlockAttnArgs& in, long long pairs, int num_sms, cudaStream_t s) {
+  using L = Lay<D, KV>;
+  BlockAttnArgs a = in;
+  // Four warps a CTA while one wave holds all pairs, then two, then one, and two again for
+  // several waves. 64 rows of 8 KV heads over 64 BF16 blocks (512 pairs; 4 heads a
+  // KV head; us): four warps 61, three 51, two 48, one 53; 40 rows 36, 34, 35, 48; 112
+  // rows 83, 82, 94, 78; 256 rows 170, 170, 165, 180. e4m3, 8 heads: 40 rows 24 (four), 29
+  // (two); 64 rows 44, 32; 128 rows 67, 74, and 57 with one.
+  a.warps = pairs <= ba_places<D, KV, FEW>(4, num_sms) ? 4 : pairs <= ba_places<D, KV, FEW>(2, num_sms) ? 2
+          : pairs <= ba_places<D, KV, FEW>(1, num_sms) ? 1 : 2;
+  // Clusters of a power of two (seven CTAs for 64 pairs: 23 us, four 14, one 17) while pairs
+  // are few: up to 4/3 CTAs per SM over BF16 caches, which bound by memory, 8/3 over
+  // the others (64 pairs over 256 4-bit blocks, d = 64: four 13 us, two 18, one 28), no warp with less than a step, or from 32 pairs on than four blocks.
+  const long long room = (L::BF ? 4LL : 8LL) * num_sms / 3 / pairs, least = std::max(L::TB, pairs > 32 ? 4 : 1);
+  const long long most = std::min(room, a.k / (kBaWarps * least));
+  a.cluster = 1;
+  while (a.warps == kBaWarps && 2 * a.cluster <= std::min<long long>(kBaCluster, most)) a.cluster *= 2;
+  void* p[] = {&a};
+  return launch_ex((const void*)block_attention_kernel<D, KV, FEW>, dim3((unsigned)(pairs * a.cluster)), dim3(32 * a.warps),
+                   a.warps * L::WARP, s, p, false, 100, a.cluster > 1 ? a.cluster : 0);
 }
 
 template <int D, int KV, bool FEW = false>
@@ -685,14 +718,11 @@ cudaError_t launch_block_attention(const BlockAttnArgs& in, int num_sms, cudaStr
   a.hblocks = (a.nq / a.nkv + kBaHeads - 1) / kBaHeads;
   const long long pairs = (long long)a.n * a.nkv * a.hblocks;
   if (pairs * kBaCluster > 0x7fffffffLL || a.k > 0x7fffffff - 32 * kBaWarps * kBaCluster) return cudaErrorInvalidValue;
-  const long long want = std::min<long long>((a.k + 2 * kBaWarps - 1) / (2 * kBaWarps), (long long)ba_per_sm(a.d) * num_sms / kBaWarps / pairs);
-  a.cluster = (int)std::max<long long>(1, std::min<long long>(kBaCluster, want));
-  a.warps = (int)std::max<long long>(1, std::min<long long>(kBaWarps, (long long)ba_per_sm(a.d) * num_sms / pairs));
   const bool wide = a.d == 128;
-  if (a.kv == KV_BF16 && a.nq / a.nkv <= 4) return wide ? ba_launch<128, KV_BF16, true>(a, s) : ba_launch<64, KV_BF16, true>(a, s);
-  if (a.kv == KV_BF16) return wide ? ba_launch<128, KV_BF16>(a, s) : ba_launch<64, KV_BF16>(a, s);
-  if (a.kv == KV_E4M3) return wide ? ba_launch<128, KV_E4M3>(a, s) : ba_launch<64, KV_E4M3>(a, s);
-  return wide ? ba_launch<128, KV_FP4>(a, s) : ba_launch<64, KV_FP4>(a, s);
+  if (a.kv == KV_BF16 && a.nq / a.nkv <= 4) return wide ? ba_launch<128, KV_BF16, true>(a, pairs, num_sms, s) : ba_launch<64, KV_BF16, true>(a, pairs, num_sms, s);
+  if (a.kv == KV_BF16) return wide ? ba_launch<128, KV_BF16>(a, pairs, num_sms, s) : ba_launch<64, KV_BF16>(a, pairs, num_sms, s);
+  if (a.kv == KV_E4M3) return wide ? ba_launch<128, KV_E4M3>(a, pairs, num_sms, s) : ba_launch<64, KV_E4M3>(a, pairs, num_sms, s);
+  return wide ? ba_launch<128, KV_FP4>(a, pairs, num_sms, s) : ba_launch<64, KV_FP4>(a, pairs, num_sms, s);
 }
 
 cudaError_t block_attention_init() {

@@ -1,7 +1,11 @@
 // Ranges of the keys in a cache block and the choice of blocks by them.
 //
 // key_bounds_kernel: per (block, KV head) and channel the smallest and largest
-// key as 8-bit codes, rounded outwards on a power-of-two grid.
+// key as 8-bit codes, rounded outwards on a power-of-two grid. Reads the keys of
+// the blocks written to once; bound by latency for a step's rows (64 rows of 8
+// heads of 128, BF16: 2.5 us in a graph) and by the instructions per key for a
+// prompt's (4084 rows of 8 x 128, e4m3: 5.2 us; 50021 rows of 8 x 64, 4-bit: 12.7 us,
+// 1.4 TB/s; with every lane encoding eight channels and no keys under way 53).
 //
 // block_select_kernel: for integers u = rint(q 2^(10 - x)) of the group's
 // queries, P_i and N_i the sums of the positive and negative ones,
@@ -9,6 +13,11 @@
 // for every key of the block; the right side with the 8-bit codes is an exact
 // integer (|.| < 2^29: P - N <= 2^14, codes <= 127, 128 channels), so that no
 // order of summation can move a block over the border of the chosen ones.
+// Bound by the gather of the ranges, 2 d bytes each (6.2 TB/s alone for 256): four
+// byte products per instruction, on two bytes of each weight. Measured in a graph,
+// us, 32 + 2 x 8 heads of 128: one row over 2048 blocks 8.4 (five round trips, the
+// choice 2.6 of them); 64 rows over 1000 to 2048 blocks 40 (64 heads; 5.0 TB/s, the
+// scores alone 35); two rows over 62500 blocks 55.5 (4.7 TB/s), one 40.
 #include <algorithm>
 
 #include "fp4.cuh"
@@ -192,7 +201,10 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Key
 constexpr int kSelWarps = 8;                 // warps of a CTA that chooses from one context
 constexpr int kSelPerSm = 4;                 // such CTAs per SM (64 registers a thread)
 constexpr int kSelCluster = 8;               // most CTAs of a cluster
-constexpr int kSelOne = 4096;                // widest table for which one CTA has all keys
+// Widest table for which one CTA has all keys. One row of 8 KV heads over 2048 blocks
+// 8.4 us (two launches 14.2), 4096 12.4 (14.6), 8192 20.3 (16.0); 64 rows over 4096 87
+// (101), 8192 251 (183).
+constexpr int kSelOne = 4096;
 constexpr int kPartWarps = 16;               // warps of a CTA that scores a part of a long context, two per SM
 constexpr int kMergeWarps = 32;              // of one that chooses among the parts' candidates
 constexpr int kPartMost = 8192;              // most blocks of a part
@@ -672,7 +684,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Blo
 
 cudaError_t launch_key_bounds(const KeyBoundsArgs& in, int num_sms, cudaStream_t s) {
   KeyBoundsArgs a = in;
-  // all CTAs resident at once, four per SM: most of a prompt's rows leave their block to the next
+  // all CTAs resident at once, four per SM (eight: 4084 rows 6.1 us against 5.2, 50021 rows
+  // 13.6 against 12.6): most of a prompt's rows leave their block to the next
   a.rows = (int)std::min<long long>(kBoundsRows, (a.n + 4LL * num_sms - 1) / (4LL * num_sms));
   auto go = [&](auto kernel) {
     kernel<<<(unsigned)((a.n + (long long)a.rows - 1) / a.rows), 32 * kBoundsWarps, 0, s>>>(a);
@@ -699,7 +712,8 @@ cudaError_t block_select_plan(BlockSelectArgs* a, int num_sms) {
   a->parts = 0;
   a->cand = 0;
   if (blocks <= kSelOne) {
-    // one wave of CTAs, none with less than 32 blocks of a full table per warp
+    // One wave of CTAs, none with less than 32 blocks of a full table per warp. (One
+    // row over 2048 blocks in one CTA per KV head: all keys behind eight warps' loads.)
     const long long want = std::min((blocks + 32 * kSelWarps - 1) / (32 * kSelWarps), (long long)kSelPerSm * num_sms / pairs);
     a->cluster = (int)std::max<long long>(1, std::min<long long>(want, kSelCluster));
     return pairs * a->cluster > 0x7fffffffLL ? cudaErrorInvalidValue : cudaSuccess;

@@ -2,9 +2,11 @@
 // lengths alone: sequence s with ctx_s cached and new_s new tokens needs
 //   need_s = ceil((ctx_s + new_s) / 16) - ceil(ctx_s / 16)
 // blocks, which are those of the free list behind the ones that sequences before
-// it need, and its rows stand behind theirs: two prefix sums, and a third over
-// the sequences that fit ("Kernels, Fusion & CUDA Graphs", "The serving engine's
-// kernel stack": block tables of the paged cache).
+// it need, and its rows stand behind theirs: two prefix sums, and the same over
+// those that fit where not all do ("Kernels, Fusion & CUDA Graphs", "The serving
+// engine's kernel stack": block tables of the paged cache). Bound by latency: 64
+// sequences by a token each take 3.1 us in a graph, 512 by 65 k rows, in two
+// launches, 9.2.
 #include "common.cuh"
 #include "internal.h"
 
@@ -13,7 +15,9 @@ namespace mbt {
 namespace {
 
 constexpr int kPlanThreads = 1024;           // most threads of the tables' CTA, a sequence each
-constexpr int kPlanRows = 4096;              // rows up to which it lays them out itself
+// Rows up to which that CTA lays them out itself: 1024 rows of 64 sequences 4.7 us
+// (5.4 in two launches), 2048 6.0 (5.5), 4096 7.9 (5.5).
+constexpr int kPlanRows = 1024;
 constexpr int kRowThreads = 256;
 constexpr int kRowSeqs = 4096;               // row edges that the rows' CTAs keep in shared memory
 

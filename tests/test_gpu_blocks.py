@@ -604,6 +604,27 @@ def test_attention_values_that_are_not_finite(cuda_lib, kind, nq):
 
 
 @pytest.mark.parametrize("kind", ALL)
+@pytest.mark.parametrize("n", [40, 64, 110, 300])
+def test_attention_many_rows(cuda_lib, kind, n):
+    """CTAs of four, two and one warps, one wave and several; over a BF16 cache with infinities in some rows' values."""
+    rng = np.random.default_rng(n)
+    c = Attend(kind, 16, 8, 128, rng.integers(1, 90, n), 3, seed=n)
+    for i in range(0, n, 13):
+        c.sel[i, i % 8] = -1
+    got, (want, most) = c.run()[0], c.want()
+    assert np.all(np.abs(got - want) <= 2e-5 * most)
+    if kind == "bf16":
+        for i in range(0, n, 7):
+            c.vp[c.bt[i, c.pos[i] // 16], i % 8, 0, i % 128] = 0x7F80
+        odd = np.zeros((n, 8, 2, 128), bool)
+        for i in range(0, n, 7):
+            if (c.sel[i, i % 8] == c.pos[i] // 16).any():
+                odd[i, i % 8, :, i % 128] = True
+        odd, again = odd.reshape(n, -1), c.run()[0]
+        assert odd.any() and np.all(again[odd] == np.inf) and np.array_equal(again[~odd], got[~odd])
+
+
+@pytest.mark.parametrize("kind", ALL)
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
 @pytest.mark.parametrize("nq", [8, 14])
 def test_attention_queries_that_are_not_finite(cuda_lib, kind, bad, nq):
