@@ -414,7 +414,7 @@ def _pools(fn: str, k, v, dev: int, nkv: int, d: int, num_blocks: int, kv_dtype:
     if unit is None or nkv < 1 or num_blocks < 1:          # here, before ctypes takes 32 bits of them
         raise MbtError(fn, -1)
     need = (num_blocks + 1) * nkv * unit
-    for name, t in (("kpool", k), ("vpool", v)):
+    for name, t in (("kpool", k), ("vpool", v)) if v is not k else (("kpool", k),):
         if isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous() and t.nbytes >= need:
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():

@@ -23,16 +23,15 @@
 //   own for K and for V, filled by 16-byte asynchronous copies and refilled as soon
 //   as read: no barrier in the loop. (Straight into registers, which hold one step,
 //   the e4m3 case below took 69 us against 66 at that stage.)
-// * Few (row, KV head) pairs are shared by clusters and many get a warp each, so
-//   that one wave of 12 warps per SM (16 at d = 64) holds them.
+// * Few (row, KV head) pairs are shared by clusters, many get CTAs of two warps or
+//   one, so that one wave of up to 12 warps per SM (16 at d = 64) holds them.
 // Measured in a graph, us: 64 rows of 32 + 2 x 8 heads of 128 over 64 BF16 blocks
-// 51 (5.3 TB/s; the copies alone 47), 128 rows 90 (6.0 TB/s); 64 rows of 64 + 2 x 8
-// over 128 e4m3 blocks 55 (copies 48); the same over 4-bit blocks 51 (copies 32: issue);
-// 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks
-// each 76 (issue, 250 a block); one row of 32 + 2 x 8 heads of 128 over 64 BF16 blocks
-// 8.8, of which 7.4 are the launch, four round trips (position, entry, table, block)
-// and the merge. A wave whose SMs hold three or four CTAs of three warps ends
-// unevenly: 20 % of the first case's cycles.
+// 48.7 (5.6 TB/s; the copies alone 46.8 with three warps a CTA, 52.8 then), 128 rows 88
+// (6.2 TB/s); 64 rows of 64 + 2 x 8 over 128 e4m3 blocks 51.8 (copies 48), over 128 4-bit
+// blocks 51 (copies 32: issue); 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks each
+// 77 (issue, 250 instructions a block); one row of 32 + 2 x 8 heads of 128 over 64 BF16
+// blocks 8.8, of which 7.4 are the launch, four round trips (position, entry, table,
+// block) and the merge.
 #include <algorithm>
 
 #include "fp4.cuh"
