@@ -279,7 +279,8 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
  * ranges of the blocks written to), op_block_select, op_block_attention.
  * All take cache formats, head sizes, groups, scales and table widths as the
  * 4-bit section above says, up to 2^30 rows, 2^16 KV heads and 2^26 chosen
- * blocks per row and head, and rows of any sequences: row i is at positions[i]
+ * blocks per row and head (the last two entry points 2^28 products of rows, KV
+ * heads and groups of eight query heads), and rows of any sequences: row i is at positions[i]
  * of sequence row_seq[i] (NULL: sequence i, nseq >= n) of bt [nseq][bt_stride].
  * A row whose position or sequence is outside the table sets MBT_DEV_POS_RANGE;
  * an out-of-range block id sets MBT_DEV_BLOCK_RANGE. They keep nothing between
@@ -321,8 +322,9 @@ int op_kv_extend(int nseq, const int32_t* ctx_lens, const int32_t* new_lens, int
  * scale 0 where M is 0, +infinity (and codes 0) where a key is not finite.
  * bounds [num_blocks + 1][nkv][2][d] int8, scales [num_blocks + 1][nkv] fp32.
  * A row leaves its block to the next row when that is in the same block of the
- * same sequence; rows that are in one block otherwise must have the same
- * position, or which of them counts is unspecified. A row with an error is left
+ * same sequence, so a sequence's rows come in increasing order, one after
+ * another; rows that are in one block otherwise must have the same position, or
+ * which of them counts is unspecified. A row with an error is left
  * out; every other range stays as it was. */
 int op_key_bounds(int n, const int32_t* positions, const int32_t* row_seq, int nseq, const int32_t* bt, int bt_stride,
                   int nkv, int d, const void* kpool, int kv_dtype, int num_blocks, int8_t* bounds, float* scales,
@@ -364,7 +366,10 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
  * fp32, out [n][nq * d] fp32. An out-of-range id reads the null block. Cache
  * contents past a row's position never reach it. A query that is not finite
  * makes its row NaN in that head, a key that is not the rows that attend to it;
- * an infinity or a NaN in V reaches them in its channel. */
+ * an infinity or a NaN in V reaches them in its channel. Queries and
+ * probabilities are exact to 2^-24 over a BF16 cache, whose values' sum over the
+ * row's tokens has to stay in fp32's range, and to 2^-22 over the others,
+ * probabilities below 2^-17 of the row's largest to 2^-39 of that. */
 int op_block_attention(int n, const float* q, int nq, int nkv, int d, const void* kpool, const void* vpool, int kv_dtype,
                        float k_scale, float v_scale, const int32_t* positions, const int32_t* row_seq, int nseq,
                        const int32_t* bt, int bt_stride, const int32_t* sel, int k, int num_blocks, float* out,

@@ -312,7 +312,7 @@ struct KvExtendArgs {
   int nseq; const int* ctx_lens; const int* new_lens; int* bt; int bt_stride; int num_blocks;
   const int* free_blocks; int nfree; const int* free_at; int n;
   int* held; int* cu; int* positions; int* row_seq; int64_t* slots; int* free_next; uint32_t* err;
-  int here;                         // set by the launch: the tables' CTA lays out the rows too
+  bool in_place;                    // set by the launch: lengths or the list's place are written where they are read
 };
 cudaError_t launch_kv_extend(const KvExtendArgs& a, cudaStream_t s);
 

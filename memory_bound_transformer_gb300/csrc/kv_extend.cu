@@ -4,9 +4,15 @@
 // blocks, which are those of the free list behind the ones that sequences before
 // it need, and its rows stand behind theirs: two prefix sums, and the same over
 // those that fit where not all do ("Kernels, Fusion & CUDA Graphs", "The serving
-// engine's kernel stack": block tables of the paged cache). Bound by latency: 64
-// sequences by a token each take 3.1 us in a graph, 512 by 65 k rows, in two
-// launches, 9.2.
+// engine's kernel stack": block tables of the paged cache).
+//
+// Each CTA computes the sums, which costs less than a second launch or handing them
+// over, and lays out its share of the rows; the row that begins a block enters it
+// into the table. Where lengths are updated in place the CTAs are one cluster of up
+// to eight, and none writes before all have read. Bound by latency (lengths, sums, a
+// free or table entry per row). In a graph, us: 64 sequences by a token each 2.6;
+// 512 by 65 k rows 4.2 (in place 9.4; one CTA for the sums and tables and a grid
+// for the rows 9.1, and 2.5 more of the caller's time).
 #include "common.cuh"
 #include "internal.h"
 
@@ -14,12 +20,10 @@ namespace mbt {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;           // most threads of the tables' CTA, a sequence each
-// Rows up to which that CTA lays them out itself: 1024 rows of 64 sequences 4.7 us
-// (5.4 in two launches), 2048 6.0 (5.5), 4096 7.9 (5.5).
-constexpr int kPlanRows = 1024;
-constexpr int kRowThreads = 256;
-constexpr int kRowSeqs = 4096;               // row edges that the rows' CTAs keep in shared memory
+constexpr int kPlanThreads = 1024;           // most threads of a CTA, a sequence each at a time
+constexpr int kPlanCluster = 8;              // most CTAs in place
+constexpr int kPlanGrid = 128;               // most CTAs otherwise
+constexpr int kPlanRows = 2;                 // rows of a thread at a time (four: 1024 rows 4.9 us against 4.4)
 
 __device__ __forceinline__ int blocks_for(long long tokens) { return (int)((tokens + kBlockTokens - 1) / kBlockTokens); }
 
@@ -47,45 +51,15 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair* scratch, Pair& total) {
   return v;
 }
 
-// Last entry of the non-decreasing edge[0 .. n] that is <= x, for edge[0] <= x < edge[n].
-__device__ __forceinline__ int segment_of(const int* edge, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (edge[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
-// Row i of sequence seq (nseq: padding) at position pos.
-__device__ __forceinline__ void lay_row(const KvExtendArgs& a, int i, int seq, int pos) {
-  long long slot = (long long)a.num_blocks * kBlockTokens;
-  if (seq < a.nseq) {
-    const int blk = a.bt[(size_t)seq * a.bt_stride + pos / kBlockTokens];
-    const bool ok = blk >= 0 && blk <= a.num_blocks;
-    if (!ok) set_err(a.err, MBT_DEV_BLOCK_RANGE);
-    slot = ok ? (long long)blk * kBlockTokens + pos % kBlockTokens : -1;
-  }
-  a.positions[i] = pos;
-  a.row_seq[i] = seq;
-  a.slots[i] = slot;
-}
-
-// One CTA: tables, lengths and row edges, a sequence per thread at a time, and the
-// rows where they are few. What a sequence reads of arrays that may be written in
-// place it reads before. Bound by latency: the lengths, the free list's entries
-// and the rows' table entries are three round trips, a launch the rest.
 __global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvExtendArgs a) {
   __shared__ Pair scratch[32];
   __shared__ int took_edge[kPlanThreads + 1], row_edge[kPlanThreads + 1], sm_have[kPlanThreads], sm_ctx[kPlanThreads];
-  const int tid = threadIdx.x, threads = blockDim.x;
-  pdl_launch_dependents();
+  const int tid = threadIdx.x, threads = blockDim.x, rank = blockIdx.x;
   const int at0 = *a.free_at;
   const bool at_ok = at0 >= 0 && at0 <= a.nfree;
   if (!at_ok && tid == 0) set_err(a.err, MBT_DEV_BLOCK_RANGE);
   long long needed = 0, asked = 0, rows = 0, taken = 0;
-  if (tid == 0) a.cu[0] = took_edge[0] = row_edge[0] = 0;
+  if (tid == 0) took_edge[0] = row_edge[0] = 0;
   for (int s0 = 0; s0 < a.nseq; s0 += threads) {
     const int s = s0 + tid;
     const bool in = s < a.nseq;
@@ -111,54 +85,60 @@ __global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvExtendA
       }
       got = block_scan(Pair{need, add}, scratch, got_total);
     }
-    if (in) {
+    took_edge[tid + 1] = (int)got.x;
+    row_edge[tid + 1] = (int)got.y;
+    sm_have[tid] = have;
+    sm_ctx[tid] = ctx;
+    if (a.in_place) cluster_sync_all();                               // every CTA has read these sequences
+    else __syncthreads();
+    if (in && rank == 0) {
       a.held[s] = ctx + add;
       a.cu[s + 1] = (int)(rows + got.y);
     }
-    took_edge[tid + 1] = (int)got.x;
-    row_edge[tid + 1] = (int)(rows + got.y);
-    sm_have[tid] = have;
-    sm_ctx[tid] = ctx;
-    __syncthreads();
-    for (int i = tid; i < (int)got_total.x; i += threads) {
-      const int q = segment_of(took_edge, threads, i), id = a.free_blocks[at0 + taken + i];
-      if (id < 0 || id > a.num_blocks) set_err(a.err, MBT_DEV_BLOCK_RANGE);
-      a.bt[(size_t)(s0 + q) * a.bt_stride + sm_have[q] + i - took_edge[q]] = id;
-    }
-    __syncthreads();
-    if (a.here) {
-      for (int i = (int)rows + tid; i < (int)(rows + got_total.y); i += threads) {
-        const int q = segment_of(row_edge, threads, i);
-        lay_row(a, i, s0 + q, sm_ctx[q] + i - row_edge[q]);
+    const int count = (int)got_total.y, stride = threads * gridDim.x;
+    for (int i0 = rank * threads + tid; i0 < count; i0 += kPlanRows * stride) {
+      int q[kPlanRows], id[kPlanRows];                                // the row's sequence: the last edge <= the row
+#pragma unroll
+      for (int u = 0; u < kPlanRows; ++u) q[u] = 0;
+      for (int step = threads >> 1; step > 0; step >>= 1)
+#pragma unroll
+        for (int u = 0; u < kPlanRows; ++u)
+          if (row_edge[q[u] + step] <= i0 + u * stride) q[u] += step;
+#pragma unroll
+      for (int u = 0; u < kPlanRows; ++u) {
+        const int i = i0 + u * stride, pos = sm_ctx[q[u]] + i - row_edge[q[u]], b = pos / kBlockTokens;
+        if (i >= count) continue;
+        id[u] = b >= sm_have[q[u]] ? a.free_blocks[at0 + taken + took_edge[q[u]] + b - sm_have[q[u]]]
+                                   : a.bt[(size_t)(s0 + q[u]) * a.bt_stride + b];
       }
-      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kPlanRows; ++u) {
+        const int i = i0 + u * stride, pos = sm_ctx[q[u]] + i - row_edge[q[u]], b = pos / kBlockTokens;
+        if (i >= count) continue;
+        const bool ok = id[u] >= 0 && id[u] <= a.num_blocks;
+        if (!ok) set_err(a.err, MBT_DEV_BLOCK_RANGE);
+        if (b >= sm_have[q[u]] && pos % kBlockTokens == 0) a.bt[(size_t)(s0 + q[u]) * a.bt_stride + b] = id[u];
+        const int row = (int)rows + i;
+        a.positions[row] = pos;
+        a.row_seq[row] = s0 + q[u];
+        a.slots[row] = ok ? (long long)id[u] * kBlockTokens + pos % kBlockTokens : -1;
+      }
     }
     needed += total.x;
     asked += total.y;
     rows += got_total.y;
     taken += got_total.x;
-    if (tid == 0) row_edge[0] = (int)rows;
+    __syncthreads();                                                  // the edges may be written again
   }
-  if (a.here)
-    for (int i = (int)rows + tid; i < a.n; i += threads) lay_row(a, i, a.nseq, 0);
-  if (tid == 0) *a.free_next = at0 + (int)taken;
-}
-
-// The packed rows of a large step, one per thread.
-__global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const KvExtendArgs a) {
-  __shared__ int edge[kRowSeqs + 1];
-  pdl_wait();
-  const bool small = a.nseq <= kRowSeqs;
-  if (small) {
-    for (int s = threadIdx.x; s <= a.nseq; s += kRowThreads) edge[s] = a.cu[s];
-    __syncthreads();
+  for (int i = (int)rows + rank * threads + tid; i < a.n; i += threads * gridDim.x) {
+    a.positions[i] = 0;
+    a.row_seq[i] = a.nseq;
+    a.slots[i] = (long long)a.num_blocks * kBlockTokens;
   }
-  const int* cu = small ? edge : a.cu;
-  const int i = blockIdx.x * kRowThreads + threadIdx.x;
-  if (i >= a.n) return;
-  if (i >= cu[a.nseq]) return lay_row(a, i, a.nseq, 0);
-  const int seq = segment_of(cu, a.nseq, i);
-  lay_row(a, i, seq, a.held[seq] - cu[seq + 1] + i);
+  if (tid == 0 && rank == 0) {
+    a.cu[0] = 0;
+    *a.free_next = at0 + (int)taken;
+  }
 }
 
 }  // namespace
@@ -166,13 +146,12 @@ __global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const KvExtendArgs
 cudaError_t launch_kv_extend(const KvExtendArgs& in, cudaStream_t s) {
   KvExtendArgs a = in;
   void* p[] = {&a};
-  // few sequences or rows: a barrier of few warps. Rows beyond a few per thread go to a grid of their own.
+  // few sequences and rows: a barrier of few warps
   const int most = a.nseq > a.n ? a.nseq : a.n, threads = most <= 128 ? 128 : most <= 512 ? 512 : kPlanThreads;
-  a.here = a.n <= kPlanRows;
-  const cudaError_t e = launch_ex((const void*)kv_extend_kernel, dim3(1), dim3(threads), 0, s, p, false, -1);
-  if (e != cudaSuccess || a.here) return e;
-  return launch_pdl((const void*)kv_rows_kernel, dim3((unsigned)((a.n + (long long)kRowThreads - 1) / kRowThreads)),
-                    dim3(kRowThreads), 0, s, p);
+  a.in_place = a.held == a.ctx_lens || a.free_next == a.free_at;
+  int ctas = 1;
+  while (ctas * kPlanThreads < a.n && ctas < (a.in_place ? kPlanCluster : kPlanGrid)) ctas *= 2;
+  return launch_ex((const void*)kv_extend_kernel, dim3(ctas), dim3(threads), 0, s, p, false, -1, a.in_place ? ctas : 0);
 }
 
 }  // namespace mbt
