@@ -4,8 +4,8 @@
 // key as 8-bit codes, rounded outwards on a power-of-two grid. Reads the keys of
 // the blocks written to once; bound by latency for a step's rows (64 rows of 8
 // heads of 128, BF16: 2.5 us in a graph) and by the instructions per key for a
-// prompt's (4084 rows of 8 x 128, e4m3: 5.2 us; 50021 rows of 8 x 64, 4-bit: 12.7 us,
-// 1.4 TB/s; with every lane encoding eight channels and no keys under way 53).
+// prompt's (4084 rows of 8 x 128, e4m3: 5.0 us; 50021 rows of 8 x 64, 4-bit: 11.6 us,
+// 1.6 TB/s; with every lane encoding eight channels and no keys under way 53).
 //
 // block_select_kernel: for integers u = rint(q 2^(10 - x)) of the group's
 // queries, P_i and N_i the sums of the positive and negative ones,
@@ -121,16 +121,21 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Key
   __syncthreads();
   constexpr size_t UNIT = KV == KV_BF16 ? kBlockTokens * D * 2 : KV == KV_E4M3 ? kBlockTokens * D : fp4_unit_bytes(D);
   constexpr int LOADS = kBlockTokens / TOK, OWN = 4 / TOK;            // pairs that a lane encodes
-  const int c = lane % LANES, tasks = sm_count * a.nkv;
+  const int c = lane % LANES, count = sm_count;
   Key8<D, KV> key[LOADS];
-  auto load = [&](int i) {
-    const unsigned char* unit = reinterpret_cast<const unsigned char*>(a.kpool) + ((size_t)sm_blk[i / a.nkv] * a.nkv + i % a.nkv) * UNIT;
+  size_t next = 0;                                                    // the (block, head) whose keys are under way
+  auto load = [&](int b, int h) {
+    next = (size_t)sm_blk[b] * a.nkv + h;
+    const unsigned char* unit = reinterpret_cast<const unsigned char*>(a.kpool) + next * UNIT;
 #pragma unroll
-    for (int t = 0; t < LOADS; ++t) key[t].load(unit, min(t * TOK + lane / LANES, sm_upto[i / a.nkv]), c);
+    for (int t = 0; t < LOADS; ++t) key[t].load(unit, min(t * TOK + lane / LANES, sm_upto[b]), c);
   };
-  if (warp < tasks) load(warp);
-  for (int i = warp; i < tasks; i += kBoundsWarps) {
-    const size_t at = (size_t)sm_blk[i / a.nkv] * a.nkv + i % a.nkv;
+  int b = 0, h = warp;                                                // the heads of all blocks, over the warps in turn
+  auto settle = [&]() { while (h >= a.nkv) { h -= a.nkv; ++b; } };
+  settle();
+  if (b < count) load(b, h);
+  while (b < count) {
+    const size_t at = next;
     uint32_t lo[4], hi[4];
 #pragma unroll
     for (int t = 0; t < LOADS; ++t) {
@@ -142,7 +147,9 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Key
         hi[k] = t ? max_nan(hi[k], p[k], BF) : p[k];
       }
     }
-    if (i + kBoundsWarps < tasks) load(i + kBoundsWarps);
+    h += kBoundsWarps;
+    settle();
+    if (b < count) load(b, h);
     int ch = 8 * c;                                                   // the lane's first channel
 #pragma unroll
     for (int o = 16, n = 2; o >= LANES; o >>= 1, n >>= 1) {
