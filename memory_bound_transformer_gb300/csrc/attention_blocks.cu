@@ -30,7 +30,7 @@
 // (6.2 TB/s); 64 rows of 64 + 2 x 8 over 128 e4m3 blocks 51.8 (copies 48), over 128 4-bit
 // blocks 51 (copies 32: issue); 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks each
 // 77 (issue, 250 instructions a block); one row of 32 + 2 x 8 heads of 128 over 64 BF16
-// blocks 8.8, of which 7.4 are the launch, four round trips (position, entry, table,
+// blocks 8.4, of which some 7 are the launch, four round trips (position, entry, table,
 // block) and the merge.
 #include <algorithm>
 
@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   const size_t head0 = (size_t)row * a.nq + (size_t)h * G + hb * kBaHeads;
   const int g = (lane >> 2) & (FEW ? 3 : 7), t = lane & 3;             // the lane's head
 
+  pdl_enter();
   Picks pk;
   const int pos = a.positions[row], seq = a.row_seq ? a.row_seq[row] : row;
   pk.sel = a.sel + ((size_t)row * a.nkv + h) * a.k;
@@ -701,7 +702,7 @@ cudaError_t ba_launch(const BlockAttnArgs& in, long long pairs, int num_sms, cud
   while (a.warps == kBaWarps && 2 * a.cluster <= std::min<long long>(kBaCluster, most)) a.cluster *= 2;
   void* p[] = {&a};
   return launch_ex((const void*)block_attention_kernel<D, KV, FEW>, dim3((unsigned)(pairs * a.cluster)), dim3(32 * a.warps),
-                   a.warps * L::WARP, s, p, false, 100, a.cluster > 1 ? a.cluster : 0);
+                   a.warps * L::WARP, s, p, pdl_pays(pairs * a.cluster, num_sms), 100, a.cluster > 1 ? a.cluster : 0);
 }
 
 template <int D, int KV, bool FEW = false>

@@ -15,7 +15,7 @@
 // order of summation can move a block over the border of the chosen ones.
 // Bound by the gather of the ranges, 2 d bytes each (6.2 TB/s alone for 256): four
 // byte products per instruction, on two bytes of each weight. Measured in a graph,
-// us, 32 + 2 x 8 heads of 128: one row over 2048 blocks 8.4 (five round trips, the
+// us, 32 + 2 x 8 heads of 128: one row over 2048 blocks 8.1 (five round trips, the
 // choice 2.6 of them); 64 rows over 1000 to 2048 blocks 40 (64 heads; 5.0 TB/s, the
 // scores alone 35); two rows over 62500 blocks 55.5 (4.7 TB/s), one 40.
 #include <algorithm>
@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Key
   constexpr bool BF = KV == KV_BF16;
   __shared__ int sm_blk[kBoundsRows], sm_upto[kBoundsRows], sm_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x * a.rows + tid;
+  pdl_enter();
   if (tid == 0) sm_count = 0;
   __syncthreads();
   if (tid < a.rows && row < a.n) {
@@ -579,6 +580,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, kSelPerSm) block_select_kernel
   __shared__ Chooser chooser;
   const int tid = threadIdx.x;
   const int rank = (int)(blockIdx.x % (unsigned)a.cluster), pair = (int)(blockIdx.x / (unsigned)a.cluster);
+  pdl_enter();
   const uint32_t big = load_group<D, kSelWarps>(mem, a, pair / a.nkv, pair % a.nkv);
   const SelRow w = sel_row(a, pair);
   int* sel = a.sel + (size_t)pair * a.k;
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(32 * kPartWarps, 2) block_candidates_kernel(co
   __shared__ SelQuery<D> mem;
   __shared__ Chooser chooser;
   const int part = (int)(blockIdx.x % (unsigned)a.parts), pair = (int)(blockIdx.x / (unsigned)a.parts);
-  pdl_launch_dependents();
+  pdl_enter();
   const uint32_t big = load_group<D, kPartWarps>(mem, a, pair / a.nkv, pair % a.nkv);
   const SelRow w = sel_row(a, pair);
   if (w.held <= a.k) return;
@@ -648,7 +650,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) block_merge_kernel(const Blo
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ Chooser chooser;
   const int pair = (int)blockIdx.x;
-  pdl_wait();                                                         // every CTA: the end of this launch is the end of both
+  pdl_enter();
   const SelRow w = sel_row(a, pair);
   int* sel = a.sel + (size_t)pair * a.k;
   if (w.bad && threadIdx.x == 0 && w.h == 0) set_err(a.err, MBT_DEV_POS_RANGE);
@@ -695,8 +697,9 @@ cudaError_t launch_key_bounds(const KeyBoundsArgs& in, int num_sms, cudaStream_t
   // 13.6 against 12.6): most of a prompt's rows leave their block to the next
   a.rows = (int)std::min<long long>(kBoundsRows, (a.n + 4LL * num_sms - 1) / (4LL * num_sms));
   auto go = [&](auto kernel) {
-    kernel<<<(unsigned)((a.n + (long long)a.rows - 1) / a.rows), 32 * kBoundsWarps, 0, s>>>(a);
-    return cudaGetLastError();
+    void* p[] = {&a};
+    const unsigned ctas = (unsigned)((a.n + (long long)a.rows - 1) / a.rows);
+    return launch_ex((const void*)kernel, dim3(ctas), dim3(32 * kBoundsWarps), 0, s, p, pdl_pays(ctas, num_sms), -1);
   };
   if (a.d == 64)
     return a.kv == KV_BF16 ? go(key_bounds_kernel<64, KV_BF16>) : a.kv == KV_E4M3 ? go(key_bounds_kernel<64, KV_E4M3>)
@@ -740,21 +743,21 @@ size_t block_select_scratch(const BlockSelectArgs& a) {
   return (size_t)a.n * a.nkv * a.cand * (sizeof(uint32_t) + sizeof(int));
 }
 
-cudaError_t launch_block_select(const BlockSelectArgs& in, void* scratch, cudaStream_t s) {
+cudaError_t launch_block_select(const BlockSelectArgs& in, void* scratch, int num_sms, cudaStream_t s) {
   BlockSelectArgs a = in;
   void* p[] = {&a};
   const long long pairs = (long long)a.n * a.nkv;
   if (!a.parts) {
     const size_t smem = (size_t)a.bt_stride * sizeof(uint32_t);
     return launch_ex(a.d == 64 ? (const void*)block_select_kernel<64> : (const void*)block_select_kernel<128>,
-                     dim3((unsigned)(pairs * a.cluster)), dim3(32 * kSelWarps), smem, s, p, false, -1, a.cluster > 1 ? a.cluster : 0);
+                     dim3((unsigned)(pairs * a.cluster)), dim3(32 * kSelWarps), smem, s, p, pdl_pays(pairs * a.cluster, num_sms), -1, a.cluster > 1 ? a.cluster : 0);
   }
   a.keys = (uint32_t*)scratch;
   a.places = (int*)(a.keys + (size_t)pairs * a.cand);
   const size_t share = (a.bt_stride + a.parts - 1) / a.parts;
   const cudaError_t e =
       launch_ex(a.d == 64 ? (const void*)block_candidates_kernel<64> : (const void*)block_candidates_kernel<128>,
-                dim3((unsigned)(pairs * a.parts)), dim3(32 * kPartWarps), share * sizeof(uint32_t), s, p, false, -1);
+                dim3((unsigned)(pairs * a.parts)), dim3(32 * kPartWarps), share * sizeof(uint32_t), s, p, pdl_pays(pairs * a.parts, num_sms), -1);
   if (e != cudaSuccess) return e;
   return launch_pdl((const void*)block_merge_kernel, dim3((unsigned)pairs), dim3(32 * kMergeWarps),
                     (size_t)std::min<long long>(a.cand * 4LL, kMergeSmem), s, p);

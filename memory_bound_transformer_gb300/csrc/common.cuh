@@ -38,6 +38,14 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// For a kernel that is launched early but does nothing before its predecessor is
+// done: every thread calls it first, so that the end of this launch is the end of
+// all before it, and the next one may come to wait on the SMs.
+__device__ __forceinline__ void pdl_enter() {
+  pdl_wait();
+  pdl_launch_dependents();
+}
+
 // Pull read-only bytes into L2 ahead of use (16-byte aligned, size a multiple of 16).
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");

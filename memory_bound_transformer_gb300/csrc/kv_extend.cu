@@ -10,8 +10,8 @@
 // over, and lays out its share of the rows; the row that begins a block enters it
 // into the table. Where lengths are updated in place the CTAs are one cluster of up
 // to eight, and none writes before all have read. Bound by latency (lengths, sums, a
-// free or table entry per row). In a graph, us: 64 sequences by a token each 2.6;
-// 512 by 65 k rows 4.2 (in place 9.4; one CTA for the sums and tables and a grid
+// free or table entry per row). In a graph, us: 64 sequences by a token each 2.4;
+// 512 by 65 k rows 4.0 (in place 9.4; one CTA for the sums and tables and a grid
 // for the rows 9.1, and 2.5 more of the caller's time).
 #include "common.cuh"
 #include "internal.h"
@@ -55,6 +55,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvExtendA
   __shared__ Pair scratch[32];
   __shared__ int took_edge[kPlanThreads + 1], row_edge[kPlanThreads + 1], sm_have[kPlanThreads], sm_ctx[kPlanThreads];
   const int tid = threadIdx.x, threads = blockDim.x, rank = blockIdx.x;
+  // Comes to wait itself, but lets no successor start early: attention may read
+  // tables and lengths before it waits.
+  pdl_wait();
   const int at0 = *a.free_at;
   const bool at_ok = at0 >= 0 && at0 <= a.nfree;
   if (!at_ok && tid == 0) set_err(a.err, MBT_DEV_BLOCK_RANGE);
@@ -151,7 +154,7 @@ cudaError_t launch_kv_extend(const KvExtendArgs& in, cudaStream_t s) {
   a.in_place = a.held == a.ctx_lens || a.free_next == a.free_at;
   int ctas = 1;
   while (ctas * kPlanThreads < a.n && ctas < (a.in_place ? kPlanCluster : kPlanGrid)) ctas *= 2;
-  return launch_ex((const void*)kv_extend_kernel, dim3(ctas), dim3(threads), 0, s, p, false, -1, a.in_place ? ctas : 0);
+  return launch_ex((const void*)kv_extend_kernel, dim3(ctas), dim3(threads), 0, s, p, true, -1, a.in_place ? ctas : 0);
 }
 
 }  // namespace mbt

@@ -73,9 +73,9 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
   cudaStream_t s = (cudaStream_t)stream;
   const size_t bytes = block_select_scratch(a);
   if (!bytes || scratch)
-    return scratch_bytes < bytes ? MBT_ERR_SCRATCH : status(launch_block_select(a, scratch, s));
+    return scratch_bytes < bytes ? MBT_ERR_SCRATCH : status(launch_block_select(a, scratch, sms, s));
   if (cudaMallocAsync(&scratch, bytes, s) != cudaSuccess) return MBT_ERR_OOM;
-  const int done = status(launch_block_select(a, scratch, s));
+  const int done = status(launch_block_select(a, scratch, sms, s));
   const cudaError_t freed = cudaFreeAsync(scratch, s);
   return done != MBT_OK ? done : status(freed);
 }

@@ -829,6 +829,52 @@ def test_a_serving_loop(cuda_lib, graph):
         assert np.all(np.abs(b["out"][:rows].double().cpu().numpy() - ref) <= 2e-5 * most)
 
 
+def test_captured_between_other_work(cuda_lib):
+    """Behind copies, fills and another stream's work, and before what overwrites its inputs, many times over."""
+    att, sel = Attend("bf16", 8, 2, 128, [900, 40], 20, seed=45), Select(8, 2, 64, [16 * 300, 16 * 90], 20, 1, 1, seed=46)
+    ext = Extend([3, 40], [20, 1], 5, 40, 24, seed=47)
+    e, want = ext.run(), (att.run()[0], sel.run()[0])
+    a = (dev(att.q, torch.float32), raw_pool(att.kp), raw_pool(att.vp), dev(att.pos), dev(att.bt), dev(att.sel))
+    b = (dev(sel.q, torch.float32), dev(sel.codes, torch.int8), dev(sel.scales, torch.float32), dev(sel.pos), dev(sel.bt))
+    c = (dev(ext.ctx), dev(ext.new), dev(ext.bt), dev(ext.free), dev([0]))
+    mine = [[torch.zeros_like(t) for t in x] for x in (a, b, c)]
+    out, chosen = torch.zeros((2, 8 * 128), device=DEV), dev(np.zeros((2, 2, 20)))
+    held, cu, pos, seq, nxt = dev([0, 0]), dev([0] * 3), dev(np.zeros(24)), dev(np.zeros(24)), dev([0])
+    slots, side = dev(np.zeros(24), torch.int64), torch.cuda.Stream()
+    codes, scales = torch.zeros((att.nb + 1, 2, 2, 128), dtype=torch.int8, device=DEV), torch.zeros((att.nb + 1, 2), device=DEV)
+
+    def step():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for m, t in zip(mine[0] + mine[1], a + b):
+                m.copy_(t)
+        for m, t in zip(mine[2], c):
+            m.copy_(t)
+        out.fill_(float("nan"))
+        capi.op_kv_extend(*mine[2][:3], ext.nb, *mine[2][3:], held, cu, pos, seq, slots, nxt)
+        torch.cuda.current_stream().wait_stream(side)
+        capi.op_key_bounds(mine[0][3], mine[0][4], mine[0][1], 2, 128, capi.DTYPE_BF16, att.nb, codes, scales)
+        capi.op_block_select(mine[1][0], 2, *mine[1][1:], sel.nb, 1, 1, chosen)
+        capi.op_block_attention(mine[0][0], 2, *mine[0][1:3], capi.DTYPE_BF16, att.kg, att.vg, *mine[0][3:], att.nb, out)
+        for m in mine[0] + mine[1] + mine[2]:                        # the next step's copies do not wait for more than this
+            m.fill_(0)
+
+    step()
+    torch.cuda.synchronize()
+    first = codes.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            step()
+    for _ in range(5):
+        for t in (out, chosen, slots, codes):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(out.double().cpu().numpy(), want[0]) and np.array_equal(chosen.cpu().numpy(), want[1])
+        assert torch.equal(slots, e["slots"]) and torch.equal(held, e["held"]) and torch.equal(codes, first) and first.any()
+
+
 def test_two_threads_at_once(cuda_lib):
     """Calls from two host threads on streams of their own."""
     from concurrent.futures import ThreadPoolExecutor
