@@ -1,5 +1,5 @@
 """Build libmbt.so in-tree for sm_103a with nvcc (one process per translation
-unit, in parallel, then one link). Usage: python -m memory_bound_transformer_gb300.build"""
+unit, in parallel, then one link) and the native part of the Python binding. Usage: python -m memory_bound_transformer_gb300.build"""
 from __future__ import annotations
 
 import os
@@ -12,6 +12,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmbt.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["gemv.cu", "misc.cu", "attention.cu", "tc_gemm.cu", "tc_stream.cu", "sampling.cu", "runtime.cu", "ops.cu",
            "ops_noalloc.cu", "kv_fp4.cu", "attention_fp4.cu", "prompt_attention.cu",
            "ops_fp4.cu", "kv_extend.cu", "block_select.cu", "attention_blocks.cu", "ops_blocks.cu"]
@@ -35,6 +36,18 @@ def _stale(src: str, obj: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_flags():
+    """Compiler and linker flags of the Python extension, for the torch and the Python that run this."""
+    import sysconfig
+    import torch
+    at = os.path.dirname(os.path.abspath(torch.__file__))
+    lib, inc = os.path.join(at, "lib"), [os.path.join(at, "include"), os.path.join(at, "include/torch/csrc/api/include"),
+                                         sysconfig.get_paths()["include"],
+                                         os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    return (["-O2", "-std=c++17", "-fPIC", *(f"-I{i}" for i in inc)],
+            [f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-L{PKG}", "-lmbt", "-Wl,-rpath,$ORIGIN"])
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     cc = nvcc()
@@ -47,6 +60,13 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             if ptxas_info:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
+
+    bsrc, bobj = os.path.join(CSRC, "binding.cpp"), os.path.join(OBJ, "binding.o")
+    compile_flags, link_flags = _binding_flags()
+    nvcc_jobs = len(jobs)
+    if _stale(bsrc, bobj):
+        jobs.insert(0, ["g++", *compile_flags, "-c", bsrc, "-o", bobj])
+    rebind = len(jobs) > nvcc_jobs
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -64,12 +84,17 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if failed:
         raise RuntimeError("nvcc failed")
     objs = [os.path.join(OBJ, s.replace(".cu", ".o")) for s in SOURCES]
-    if jobs or not os.path.exists(LIB):
+    if nvcc_jobs or not os.path.exists(LIB):
         link = [cc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"]
         r = subprocess.run(link, capture_output=True, text=True)
         if r.returncode:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
+    if rebind or not os.path.exists(BINDING):
+        r = subprocess.run(["g++", "-shared", bobj, "-o", BINDING, *link_flags], capture_output=True, text=True)
+        if r.returncode:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link of the binding failed")
     return LIB
 
 

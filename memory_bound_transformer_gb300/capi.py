@@ -1,7 +1,9 @@
 """ctypes binding of libmbt.so (include/mbt.h, include/mbt_ops.h).
 
 Argument marshalling only: tensors are passed as raw device (or host) pointers
-and every step of the decode path runs in the library's CUDA kernels. There is
+and every step of the decode path runs in the library's CUDA kernels. The
+selected-block operators, calls of a few microseconds, are checked and called by
+a Python extension instead (csrc/binding.cpp). There is
 no fallback: if the library is missing or no sm_103 GPU is present the calls
 raise.
 """
@@ -414,7 +416,7 @@ def _pools(fn: str, k, v, dev: int, nkv: int, d: int, num_blocks: int, kv_dtype:
     if unit is None or nkv < 1 or num_blocks < 1:          # here, before ctypes takes 32 bits of them
         raise MbtError(fn, -1)
     need = (num_blocks + 1) * nkv * unit
-    for name, t in (("kpool", k), ("vpool", v)) if v is not k else (("kpool", k),):
+    for name, t in (("kpool", k), ("vpool", v)):
         if isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous() and t.nbytes >= need:
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
@@ -524,46 +526,43 @@ def op_prompt_attention(q, nkv, cu_seqlens, ctx_lens, kpool, vpool, kv_dtype, k_
         _tensor(fn, "out", out, dev, torch.float32, (n, nq * d)), _err(fn, err, dev), _stream_of(stream, dev)))
 
 
+# The selected-block operators: checked and called natively (csrc/binding.cpp), for these calls are a few us long.
+
+_native = None
+
+
+def _binding():
+    global _native
+    if _native is None:
+        load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError("the native binding is missing: build it with "
+                               "`python -m memory_bound_transformer_gb300.build`") from e
+        _native = module
+    return _native
+
+
+def _handle(stream) -> Optional[int]:
+    return None if stream is None else _stream(stream)
+
+
 def op_kv_extend(ctx_lens, new_lens, bt, num_blocks, free_blocks, free_at, held, cu_seqlens, positions, row_seq, slots,
                  free_next, err=None, stream=None) -> None:
     """Table entries from the free list and the packed rows' layout for new_lens[s] more tokens of each sequence: ctx_lens,
     new_lens, held [sequences], bt [sequences][width], free_blocks [any], free_at, free_next [1], cu_seqlens
     [sequences + 1], positions, row_seq [n] (all int32), slots [n] int64. held may be ctx_lens, free_next free_at."""
-    fn = "op_kv_extend"
-    nseq, width = _shape(fn, "bt", bt, 2)
-    n, = _shape(fn, "positions", positions, 1)
-    nfree, = _shape(fn, "free_blocks", free_blocks, 1)
-    dev = _device(fn, "bt", bt)
-    if not 1 <= num_blocks <= 0x7fffffff:
-        raise MbtError(fn, -1)
-    i32, seqs, rows, one = torch.int32, (nseq,), (n,), (1,)
-    _check(fn, load().op_kv_extend(
-        nseq, _tensor(fn, "ctx_lens", ctx_lens, dev, i32, seqs), _tensor(fn, "new_lens", new_lens, dev, i32, seqs),
-        _tensor(fn, "bt", bt, dev, i32, (nseq, width)), width, num_blocks,
-        _tensor(fn, "free_blocks", free_blocks, dev, i32, (nfree,)), nfree, _tensor(fn, "free_at", free_at, dev, i32, one), n,
-        _tensor(fn, "held", held, dev, i32, seqs), _tensor(fn, "cu_seqlens", cu_seqlens, dev, i32, (nseq + 1,)),
-        _tensor(fn, "positions", positions, dev, i32, rows), _tensor(fn, "row_seq", row_seq, dev, i32, rows),
-        _tensor(fn, "slots", slots, dev, torch.int64, rows), _tensor(fn, "free_next", free_next, dev, i32, one),
-        _err(fn, err, dev), _stream_of(stream, dev)))
+    _check("op_kv_extend", _binding().op_kv_extend(ctx_lens, new_lens, bt, num_blocks, free_blocks, free_at, held, cu_seqlens,
+                                                   positions, row_seq, slots, free_next, err, _handle(stream)))
 
 
 def op_key_bounds(positions, bt, kpool, nkv, d, kv_dtype, num_blocks, bounds, scales, row_seq=None, err=None,
                   stream=None) -> None:
     """Per-channel ranges of the keys in the blocks that the rows are in: bounds [num_blocks + 1][nkv][2][d] int8, scales
     [num_blocks + 1][nkv] fp32; kv_dtype DTYPE_BF16, DTYPE_E4M3 or DTYPE_E2M1."""
-    fn = "op_key_bounds"
-    n, = _shape(fn, "positions", positions, 1)
-    dev = _device(fn, "positions", positions)
-    nseq, width = _shape(fn, "bt", bt, 2)
-    pk, _ = _pools(fn, kpool, kpool, dev, nkv, d, num_blocks, kv_dtype)
-    _check(fn, load().op_key_bounds(
-        n, _tensor(fn, "positions", positions, dev, torch.int32, (n,)), _rows_of(fn, n, row_seq, nseq, dev), nseq,
-        _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, nkv, d, pk, kv_dtype, num_blocks,
-        _tensor(fn, "bounds", bounds, dev, torch.int8, (num_blocks + 1, nkv, 2, d)),
-        _tensor(fn, "scales", scales, dev, torch.float32, (num_blocks + 1, nkv)), _err(fn, err, dev), _stream_of(stream, dev)))
-
-
-SELECT_PLAIN = 4096                                        # tables up to this width need no scratch
+    _check("op_key_bounds", _binding().op_key_bounds(positions, bt, kpool, nkv, d, kv_dtype, num_blocks, bounds, scales, row_seq,
+                                                     err, _handle(stream)))
 
 
 def op_block_select_scratch(n: int, nkv: int, width: int, k: int) -> int:
@@ -576,43 +575,13 @@ def op_block_select(q, nkv, bounds, scales, positions, bt, num_blocks, keep_firs
     """The blocks with the largest possible scores per row and KV head: q [n][nq][d] fp32, bounds and scales as
     op_key_bounds leaves them, sel [n][nkv][k] int32 (ascending places in the table, then -1). scratch: uint8 device
     tensor of op_block_select_scratch(n, nkv, width, k) bytes; None takes it from torch's allocator, on the call's stream."""
-    fn = "op_block_select"
-    n, nq, d = _shape(fn, "q", q, 3)
-    dev = _device(fn, "q", q)
-    nseq, width = _shape(fn, "bt", bt, 2)
-    k = _shape(fn, "sel", sel, 3)[2]
-    if num_blocks < 1 or keep_first < 0 or keep_last < 1 or keep_first + keep_last > k:   # before ctypes takes 32 bits of them
-        raise MbtError(fn, -1)
-    if scratch is None and width > SELECT_PLAIN:
-        on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(on):                        # the allocator's stream order is then the call's
-            scratch = torch.empty(op_block_select_scratch(n, nkv, width, k), dtype=torch.uint8, device=q.device)
-    size = 0
-    if scratch is not None:
-        size, = _shape(fn, "scratch", scratch, 1)
-        _tensor(fn, "scratch", scratch, dev, torch.uint8, (size,))
-    _check(fn, load().op_block_select(
-        n, _tensor(fn, "q", q, dev, torch.float32, (n, nq, d)), nq, nkv, d,
-        _tensor(fn, "bounds", bounds, dev, torch.int8, (num_blocks + 1, nkv, 2, d)),
-        _tensor(fn, "scales", scales, dev, torch.float32, (num_blocks + 1, nkv)),
-        _tensor(fn, "positions", positions, dev, torch.int32, (n,)), _rows_of(fn, n, row_seq, nseq, dev), nseq,
-        _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, num_blocks, keep_first, keep_last, k,
-        _tensor(fn, "sel", sel, dev, torch.int32, (n, nkv, k)), _ptr(scratch), size, _err(fn, err, dev),
-        _stream_of(stream, dev)))
+    _check("op_block_select", _binding().op_block_select(q, nkv, bounds, scales, positions, bt, num_blocks, keep_first, keep_last,
+                                                         sel, row_seq, scratch, err, _handle(stream)))
 
 
 def op_block_attention(q, nkv, kpool, vpool, kv_dtype, k_scale, v_scale, positions, bt, sel, num_blocks, out, row_seq=None,
                        err=None, stream=None) -> None:
     """Attention over the selected blocks of a paged cache: q [n][nq][d] fp32, sel [n][nkv][k] int32, out [n][nq * d]
     fp32; kv_dtype DTYPE_BF16, DTYPE_E4M3 or DTYPE_E2M1."""
-    fn = "op_block_attention"
-    n, nq, d = _shape(fn, "q", q, 3)
-    dev = _device(fn, "q", q)
-    nseq, width = _shape(fn, "bt", bt, 2)
-    k = _shape(fn, "sel", sel, 3)[2]
-    pk, pv = _pools(fn, kpool, vpool, dev, nkv, d, num_blocks, kv_dtype)
-    _check(fn, load().op_block_attention(
-        n, _tensor(fn, "q", q, dev, torch.float32, (n, nq, d)), nq, nkv, d, pk, pv, kv_dtype, k_scale, v_scale,
-        _tensor(fn, "positions", positions, dev, torch.int32, (n,)), _rows_of(fn, n, row_seq, nseq, dev), nseq,
-        _tensor(fn, "bt", bt, dev, torch.int32, (nseq, width)), width, _tensor(fn, "sel", sel, dev, torch.int32, (n, nkv, k)),
-        k, num_blocks, _tensor(fn, "out", out, dev, torch.float32, (n, nq * d)), _err(fn, err, dev), _stream_of(stream, dev)))
+    _check("op_block_attention", _binding().op_block_attention(q, nkv, kpool, vpool, kv_dtype, k_scale, v_scale, positions, bt, sel,
+                                                               num_blocks, out, row_seq, err, _handle(stream)))

@@ -327,7 +327,7 @@ def test_select_tables_of_two_launches(cuda_lib, held, k):
     assert err == 0 and np.array_equal(got, want)
     t = (dev(c.q, torch.float32), dev(c.codes, torch.int8), dev(c.scales, torch.float32), dev(c.pos), dev(c.bt))
     size = capi.op_block_select_scratch(4, 2, c.bt.shape[1], k)
-    assert (size > 0) == (c.bt.shape[1] > capi.SELECT_PLAIN)
+    assert (size > 0) == (c.bt.shape[1] > 4096)
     own, sel = torch.zeros(max(size, 1), dtype=torch.uint8, device=DEV), dev(np.zeros(want.shape))
     call = lambda scratch: capi.op_block_select(*t[:1], 2, *t[1:], c.nb, 0, 1, sel, scratch=scratch)
     call(own)
@@ -925,4 +925,40 @@ def test_binding_refuses(cuda_lib, what):
             wrong[w] = bad(args[w])
             with pytest.raises(ValueError):
                 fn(*wrong)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("first,last,k", [(2 ** 32, 1, 3), (0, 2 ** 32 + 1, 3), (-1, 1, 3), (0, 0, 3), (2, 2, 3), (2 ** 80, 1, 3)])
+def test_kept_blocks_beyond_k(cuda_lib, first, last, k):
+    """The numbers of kept blocks are checked as they are, not what 32 bits leave of them."""
+    c = Select(8, 2, 64, [16 * 30], k, seed=48)
+    c.first, c.last = first, last
+    with pytest.raises(capi.MbtError) as e:
+        c.run()
+    assert e.value.code == -1
+
+
+def test_binding_numbers_and_pools(cuda_lib):
+    """Numbers beyond 32 bits, head sizes and formats that are not there, small pools, missing row_seq, other types."""
+    c = Attend("fp4", 8, 2, 64, [100], 4, seed=49)
+    t = [dev(c.q, torch.float32), 2, raw_pool(c.kp), raw_pool(c.vp), capi.DTYPE_E2M1, 1.0, 1.0, dev(c.pos), dev(c.bt), dev(c.sel),
+         c.nb, torch.zeros((1, 512), device=DEV)]
+    capi.op_block_attention(*t)
+    capi.op_block_attention(*t, stream=torch.cuda.current_stream().cuda_stream)
+
+    def wrong(i, x):
+        return t[:i] + [x] + t[i + 1:]
+
+    for args in (wrong(10, c.nb + 2 ** 32), wrong(4, capi.DTYPE_E2M1 + 2 ** 32), wrong(4, 2), wrong(1, 2 - 2 ** 32), wrong(10, 0),
+                 wrong(5, 0.0), wrong(6, float("nan"))):
+        with pytest.raises(capi.MbtError) as e:
+            capi.op_block_attention(*args)
+        assert e.value.code == -1
+    for args in (wrong(2, t[2][:-1].contiguous()), wrong(3, t[3].cpu()), wrong(0, c.q), wrong(7, dev(np.zeros(2))), wrong(10, c.nb + 1),
+                 wrong(8, torch.zeros((0, 7), dtype=torch.int32, device=DEV)), wrong(0, t[0][0])):
+        with pytest.raises(ValueError):
+            capi.op_block_attention(*args)
+    for args in (wrong(5, "1"), wrong(1, 2.0)):
+        with pytest.raises(TypeError):
+            capi.op_block_attention(*args)
     torch.cuda.synchronize()

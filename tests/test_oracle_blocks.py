@@ -163,13 +163,3 @@ def test_binding_refuses_host_tensors_and_wide_numbers(lib):
         capi.op_block_select(q, 2, codes, sc, pos, i, 5, 1, 1, sel)
     with pytest.raises(ValueError):
         capi.op_block_attention(q, 2, p, p, 3, 1.0, 1.0, pos, i, sel, 5, q.view(4, 256))
-
-
-@pytest.mark.parametrize("first,last,k", [(2 ** 32, 1, 3), (0, 2 ** 32 + 1, 3), (-1, 1, 3), (0, 0, 3), (2, 2, 3)])
-def test_kept_blocks_beyond_k(monkeypatch, first, last, k):
-    """The numbers of kept blocks are checked as they are, not what ctypes leaves of them."""
-    monkeypatch.setattr(capi, "_device", lambda fn, name, t: 0)
-    i = torch.zeros((4, 1), dtype=torch.int32)
-    with pytest.raises(capi.MbtError) as e:
-        capi.op_block_select(torch.zeros((4, 4, 64)), 2, None, None, i[:, 0], i, 5, first, last, torch.zeros((4, 2, k)))
-    assert e.value.code == -1
