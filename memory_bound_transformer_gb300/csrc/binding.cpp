@@ -92,6 +92,13 @@ class Call {
     if (t.nbytes() / unit / (size_t)nkv < (size_t)num_blocks + 1) refuse(name, "is smaller than num_blocks + 1 blocks");
     return t.data_ptr();
   }
+  // Bytes on the device, any number of them.
+  void* bytes(int i, const char* name, size_t& count) {
+    const at::Tensor& t = tensor(i, name);
+    check(t, name, at::kByte);
+    count = t.nbytes();
+    return t.data_ptr();
+  }
   const int32_t* rows(int i, int64_t n, int64_t nseq) {   // row_seq, or null: row i is sequence i
     if (!none(i)) return dense<int32_t>(i, "row_seq", at::kInt, {n});
     if (nseq < n) {
@@ -244,9 +251,7 @@ PyObject* block_select(PyObject*, PyObject* const* args, Py_ssize_t given) {
     size_t bytes = 0;
     at::Tensor made;                                      // lives until the launches are in the stream
     if (!c.none(11)) {
-      const at::Tensor& s = c.own(11, "scratch", at::kByte, 1);
-      scratch = s.data_ptr();
-      bytes = s.nbytes();
+      scratch = c.bytes(11, "scratch", bytes);
     } else if ((bytes = op_block_select_scratch(n, nkv, size(bt, 1), k)) > 0) {
       made = c.scratch(bytes, 13);
       scratch = made.data_ptr();

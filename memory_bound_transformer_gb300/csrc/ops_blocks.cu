@@ -49,7 +49,8 @@ size_t op_block_select_scratch(int n, int nkv, int bt_stride, int k) {
   int sms = 0;
   BlockSelectArgs a = {};
   a.n = n; a.nkv = nkv; a.bt_stride = bt_stride; a.k = k;
-  if (n < 1 || nkv < 1 || bt_stride < 1 || bt_stride > kMostPicks || k < 1 || device_setup(&sms) != MBT_OK || block_select_plan(&a, sms) != cudaSuccess)
+  if (n < 1 || n > kMostRows || nkv < 1 || nkv > kMostHeads || bt_stride < 1 || bt_stride > kMostPicks || k < 1 || k > kMostPicks ||
+      device_setup(&sms) != MBT_OK || block_select_plan(&a, sms) != cudaSuccess)
     return 0;
   return block_select_scratch(a);
 }

@@ -359,6 +359,20 @@ def test_select_tables_of_two_launches(cuda_lib, held, k):
         assert np.array_equal(sel.cpu().numpy(), want)
 
 
+def test_select_scratch_of_any_size(cuda_lib):
+    """A serving program's scratch may pass 2^31 bytes; sizes that no call takes need none."""
+    c = Select(8, 2, 64, [16 * 5000 - 3, 40], 20, 0, 1, seed=4)
+    t = (dev(c.q, torch.float32), dev(c.codes, torch.int8), dev(c.scales, torch.float32), dev(c.pos), dev(c.bt))
+    want = c.want()
+    sel = dev(np.zeros(want.shape))
+    capi.op_block_select(*t[:1], 2, *t[1:], c.nb, 0, 1, sel, scratch=torch.empty(2 ** 31 + 512, dtype=torch.uint8, device=DEV))
+    assert np.array_equal(sel.cpu().numpy(), want)
+    assert capi.op_block_select_scratch(1, 1, 5000, 1) > 0
+    for n, nkv, width, k in ((2 ** 30 + 1, 1, 5000, 1), (1, 2 ** 16 + 1, 5000, 1), (1, 1, 2 ** 26 + 1, 1), (1, 1, 5000, 2 ** 26 + 1),
+                             (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 26, 2 ** 26), (0, 1, 5000, 1), (1, 0, 5000, 1), (1, 1, 0, 1), (1, 1, 5000, 0)):
+        assert capi.op_block_select_scratch(n, nkv, width, k) == 0
+
+
 def test_select_widest_table(cuda_lib):
     """A quarter of a million blocks, few different ones, so most scores are equal."""
     c = Select(2, 1, 64, [16 * 40], 5000, 2, 3, seed=3)
