@@ -12,11 +12,16 @@
 //   cache they are three BF16 parts (24 bits; the third in a second MMA, or for up
 //   to four heads in the same one), over the narrow caches, whose values FP16 holds
 //   exactly, two FP16 parts (2^-22), probabilities relative to 2^-14 of the largest
-//   so that FP16's smallest steps lie at 2^-39 of it.
+//   so that FP16's smallest steps lie at 2^-39 of it. Over those, up to four heads are
+//   turned over, keys on M and parts on N: half the MMAs, softmax and output registers
+//   (the 4-bit case of 510 rows below 64 us against 77; 256 rows of 32 + 2 x 8 heads of
+//   128 over 64 e4m3 blocks 94 against 105, 4-bit 73 against 88; 20 or 24 warps per SM at
+//   d = 64 64 and 68, 16 at d = 128 99 and 72).
 // * The contraction may run over channels in any order: thread (g, t) of a warp
 //   takes 16-byte pieces of a key, and the queries are laid out the same way. V's
 //   pairs are two tokens of one channel, interleaved from two tokens' words. The
-//   score accumulators are the A fragments of P V as they stand.
+//   score accumulators are the A fragments of P V as they stand (turned over: the B
+//   fragments after a transposition).
 // * The tensor core's fp32 accumulation truncates, so chains are short (d / 16
 //   steps for scores, a step's blocks for P V) and sums over steps are IEEE fp32.
 // * A warp takes whole blocks from the row's list and has rings of two steps of its
@@ -28,11 +33,14 @@
 // Measured in a graph, us: 64 rows of 32 + 2 x 8 heads of 128 over 64 BF16 blocks
 // 48.7 (5.6 TB/s; the copies alone 46.8 with three warps a CTA, 52.8 then), 128 rows 88
 // (6.2 TB/s); 64 rows of 64 + 2 x 8 over 128 e4m3 blocks 51.8 (copies 48), over 128 4-bit
-// blocks 51 (copies 32: issue); 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks each
-// 77 (issue, 250 instructions a block); one row of 32 + 2 x 8 heads of 128 over 64 BF16
+// blocks 54 (copies 32: issue); 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks each
+// 64 (issue); one row of 32 + 2 x 8 heads of 128 over 64 BF16
 // blocks 8.4, of which some 7 are the launch, four round trips (position, entry, table,
 // block) and the merge.
 #include <algorithm>
+#include <type_traits>
+
+#include <cuda_fp16.h>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -81,6 +89,16 @@ __device__ __forceinline__ void split(float x0, float x1, uint32_t& p0, uint32_t
     p1 = pack_h2(x0 - h.x, x1 - h.y);
     p2 = 0;
   }
+}
+// The two FP16 parts of a value as a pair.
+__device__ __forceinline__ uint32_t parts(float x) {
+  return pack_h2(x, x - __half2float(__float2half_rn(x)));
+}
+// Of an 8 x 8 matrix of 16-bit values, whose row `lane / 4` a lane has two neighbours of, the transpose.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 // d = a b + d, or + 0 where the sum begins.
 template <bool BF, bool ZERO = false>
@@ -202,15 +220,23 @@ struct Picks {
   }
 };
 
-// FEW: at most four heads over a BF16 cache. Their three parts then fit the MMA's
+// FEW: at most four heads. Over a BF16 cache their three parts then fit the MMA's
 // 16 rows: rows 0..3 the high, 8..11 the middle and 4..7 the low ones, whose
-// products lanes 16 apart exchange.
+// products lanes 16 apart exchange. Over the narrow caches the products are turned
+// over: keys, and V's channels, lie along M's 16 and the two parts of four heads
+// along N's eight, columns 2 h and 2 h + 1. A lane then has the scores of head t for
+// the tokens of rows g and g + 8, none for heads that are not there, and both parts
+// of a product; an 8 x 8 transposition makes P's B fragments of two parts packed
+// into a word.
 template <int D, int KV, bool FEW>
 struct BlockWarp {
   using L = Lay<D, KV>;
   static constexpr bool BF = L::BF;
   static constexpr bool LOW = BF && !FEW;                             // low parts in MMAs of their own
-  float m, l, o[L::NT][2];
+  static constexpr bool TURN = FEW && !BF;
+  static constexpr int S = TURN ? L::TB : 2 * L::TB, E = TURN ? 1 : 2;   // pairs of scores, outputs per channel
+  using Frag = std::conditional_t<TURN, uint2, uint4>;                // the queries' fragment of an MMA step
+  float m, l, o[L::NT][E];
 
   // The parts of lane's head as those of its two MMA rows.
   static __device__ __forceinline__ void rows(uint32_t& hi, uint32_t& mid, uint32_t lo, int lane) {
@@ -220,7 +246,9 @@ struct BlockWarp {
     m = -INFINITY;
     l = 0.f;
 #pragma unroll
-    for (int i = 0; i < L::NT; ++i) o[i][0] = o[i][1] = 0.f;
+    for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[i][e] = 0.f;
   }
   // Requests the K or V units of a step's blocks into a stage (a shared address).
   static __device__ __forceinline__ void request(uint32_t stage, const unsigned char* pool, const int (&blk)[L::TB], int nkv, int h, int lane) {
@@ -238,13 +266,24 @@ struct BlockWarp {
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
 
-  // Scores of a step: s[2 b + n][e] of head g and token t + 4 e + 8 n of block b.
-  // stage: its keys; frag: the queries' fragments, [KS][32 lanes] x 4 words;
-  // frag_lo: the third parts', x 2.
-  __device__ __forceinline__ void scores(float (&s)[2 * L::TB][2], const unsigned char* stage, const uint4* frag, const uint2* frag_lo, int lane) {
+  // Token of a block that s[i][e] of a lane is for.
+  static __device__ __forceinline__ int token(int i, int e, int lane) {
+    return TURN ? (lane >> 3) + (lane & 4) + 8 * e : 8 * (i & 1) + (lane & 3) + 4 * e;
+  }
+  // Largest of, or sum over, the lanes that have the same head.
+  template <class F>
+  static __device__ __forceinline__ float over_head(float x, F f) {
+#pragma unroll
+    for (int o = TURN ? 4 : 1; o <= (TURN ? 16 : 2); o <<= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  }
+
+  // Scores of a step: s[i][e] of head g and block i / 2 (turned: head t and block i).
+  // stage: its keys; frag: the queries' fragments, [KS][32 lanes]; frag_lo: the third parts'.
+  __device__ __forceinline__ void scores(float (&s)[S][2], const unsigned char* stage, const Frag* frag, const uint2* frag_lo, int lane) {
     const int g = lane >> 2, t = lane & 3, tok = (g >> 1) + 4 * (g & 1);
     const unsigned char* at[2] = {stage + L::place(tok, t * L::KB), stage + L::place(tok, L::KP > 1 ? (4 + t) * L::KB : 0)};
-    float acc[2 * L::TB][4];
+    float acc[S][4];
     uint32_t sc[2 * L::TB], by[2 * L::TB];                            // 4-bit: scale bytes; the scale of 16 channels as FP16 pairs
     constexpr int PS = L::KS / L::KP;                                 // MMA steps of a piece
 #pragma unroll
@@ -260,86 +299,112 @@ struct BlockWarp {
           sc[i] = D == 128 ? *reinterpret_cast<const uint16_t*>(x) : *x;
         }
       }
-      auto product = [&](int st, int i, uint32_t b0, uint32_t b1, const uint4& a, const uint2& z) {
-        if (st == 0) mma<BF, true>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
-        else mma<BF>(acc[i], a.x, a.y, a.z, a.w, b0, b1);
-        if constexpr (LOW) mma<BF>(acc[i], z.x, 0u, z.y, 0u, b0, b1);
+      // of the two keys of a lane in block b
+      auto product = [&](int st, int b, const uint32_t (&x)[2], const uint32_t (&y)[2], const Frag& a, const uint2& z) {
+        if constexpr (TURN) {
+          if (st == 0) mma<BF, true>(acc[b], x[0], y[0], x[1], y[1], a.x, a.y);
+          else mma<BF>(acc[b], x[0], y[0], x[1], y[1], a.x, a.y);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t b0 = n ? y[0] : x[0], b1 = n ? y[1] : x[1];
+            if (st == 0) mma<BF, true>(acc[2 * b + n], a.x, a.y, a.z, a.w, b0, b1);
+            else mma<BF>(acc[2 * b + n], a.x, a.y, a.z, a.w, b0, b1);
+            if constexpr (LOW) mma<BF>(acc[2 * b + n], z.x, 0u, z.y, 0u, b0, b1);
+          }
+        }
       };
       if constexpr (KV == KV_FP4) {
 #pragma unroll
         for (int q = 0; q < PS; q += 2) {                             // a word: two steps
-          const uint4 a0 = frag[q * 32 + lane], a1 = frag[(q + 1) * 32 + lane];
+          const Frag a0 = frag[q * 32 + lane], a1 = frag[(q + 1) * 32 + lane];
 #pragma unroll
-          for (int i = 0; i < 2 * L::TB; ++i) {
-            if (q % 4 == 0) {
-              const uint32_t byte = sc[i] >> (8 * (q / 4)) & 0xffu;
-              by[i] = e4m3x2_h2(byte * 0x0101u);
+          for (int b = 0; b < L::TB; ++b) {
+            uint32_t y[2][2][2];                                      // [step][key]
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const int i = 2 * b + n;
+              if (q % 4 == 0) {
+                const uint32_t byte = sc[i] >> (8 * (q / 4)) & 0xffu;
+                by[i] = e4m3x2_h2(byte * 0x0101u);
+              }
+              uint32_t x[4];
+              e2m1x8_to_h2(k[i][q / 2], x);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) y[c >> 1][n][c & 1] = hmul2(x[c], by[i]);
             }
-            uint32_t x[4];
-            e2m1x8_to_h2(k[i][q / 2], x);
-            product(q, i, hmul2(x[0], by[i]), hmul2(x[1], by[i]), a0, make_uint2(0, 0));
-            product(q + 1, i, hmul2(x[2], by[i]), hmul2(x[3], by[i]), a1, make_uint2(0, 0));
+            product(q, b, y[0][0], y[0][1], a0, make_uint2(0, 0));
+            product(q + 1, b, y[1][0], y[1][1], a1, make_uint2(0, 0));
           }
         }
       } else {
 #pragma unroll
         for (int q = 0; q < PS; ++q) {
           const int st = p * PS + q;
-          const uint4 a = frag[st * 32 + lane];
+          const Frag a = frag[st * 32 + lane];
           uint2 z = make_uint2(0, 0);
           if constexpr (LOW) z = frag_lo[st * 32 + lane];
 #pragma unroll
-          for (int i = 0; i < 2 * L::TB; ++i) {
-            uint32_t b0, b1;
-            if constexpr (BF) {
-              b0 = k[i][2 * q];
-              b1 = k[i][2 * q + 1];
-            } else {
-              e4m3x4_to_h2(k[i][q], b0, b1);
+          for (int b = 0; b < L::TB; ++b) {
+            uint32_t x[2][2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const int i = 2 * b + n;
+              if constexpr (BF) {
+                x[n][0] = k[i][2 * q];
+                x[n][1] = k[i][2 * q + 1];
+              } else {
+                e4m3x4_to_h2(k[i][q], x[n][0], x[n][1]);
+              }
             }
-            product(st, i, b0, b1, a, z);
+            product(st, b, x[0], x[1], a, z);
           }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2 * L::TB; ++i)
+    for (int i = 0; i < S; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        s[i][e] = acc[i][e] + acc[i][e + 2];
-        if constexpr (FEW) s[i][e] += __shfl_xor_sync(0xffffffffu, s[i][e], 16);
+        s[i][e] = TURN ? acc[i][2 * e] + acc[i][2 * e + 1] : acc[i][e] + acc[i][e + 2];
+        if constexpr (FEW && BF) s[i][e] += __shfl_xor_sync(0xffffffffu, s[i][e], 16);
         if constexpr (BF) s[i][e] += s[i][e] - s[i][e];               // of a key that is not finite: NaN
       }
   }
 
-  // Softmax of head g over the lane's tokens: probabilities as A fragments of P V,
-  // and what the output so far is to be multiplied by. live: tokens of each block
-  // that the row sees.
-  __device__ __forceinline__ float soften(float (&s)[2 * L::TB][2], uint32_t (&pa)[2 * L::TB][3], const int (&live)[L::TB], float fac, int lane) {
+  // Softmax over the lane's tokens: probabilities as A fragments of P V (turned: as B
+  // fragments, pa[b][0 .. 1]), and what the output so far is to be multiplied by.
+  // live: tokens of each block that the row sees.
+  __device__ __forceinline__ float soften(float (&s)[S][2], uint32_t (&pa)[S][3], const int (&live)[L::TB], float fac, int lane) {
     constexpr float UP = BF ? 0.f : 14.f;
-    const int t = lane & 3;
     float mx = -INFINITY;
 #pragma unroll
     for (int b = 0; b < L::TB; ++b)
       if (live[b] < kBlockTokens) {                                   // the same for the whole warp
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (8 * (i >> 1) + t + 4 * (i & 1) >= live[b]) s[2 * b + (i >> 1)][i & 1] = -INFINITY;
+        for (int i = b * S / L::TB; i < (b + 1) * S / L::TB; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (token(i, e, lane) >= live[b]) s[i][e] = -INFINITY;
       }
 #pragma unroll
-    for (int i = 0; i < 2 * L::TB; ++i) mx = fmaxf(mx, fmaxf(s[i][0], s[i][1]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    for (int i = 0; i < S; ++i) mx = fmaxf(mx, fmaxf(s[i][0], s[i][1]));
+    mx = over_head(mx, [](float x, float y) { return fmaxf(x, y); });
     // differences of scores first: equal ones stay equal however large they are
     const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn, al = ex2((m - mu) * fac);
     m = mn;
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * L::TB; ++i) {
+    for (int i = 0; i < S; ++i) {
       const float p0 = ex2(fmaf(s[i][0] - mu, fac, UP)), p1 = ex2(fmaf(s[i][1] - mu, fac, UP));
       sum += p0 + p1;
-      split<BF>(p0, p1, pa[i][0], pa[i][1], pa[i][2]);
-      if constexpr (FEW) rows(pa[i][0], pa[i][1], pa[i][2], lane);
+      if constexpr (TURN) {
+        pa[i][0] = transposed(parts(p0));
+        pa[i][1] = transposed(parts(p1));
+      } else {
+        split<BF>(p0, p1, pa[i][0], pa[i][1], pa[i][2]);
+        if constexpr (FEW) rows(pa[i][0], pa[i][1], pa[i][2], lane);
+      }
     }
     l = fmaf(l, al, sum);
     return al;
@@ -347,7 +412,7 @@ struct BlockWarp {
 
   // O = O * al + P V for a step whose values are in the stage. spec: where values
   // that are not finite go (null: they are not looked for).
-  __device__ __forceinline__ void values(const uint32_t (&pa)[2 * L::TB][3], const unsigned char* stage, const int (&live)[L::TB], float al, float* spec, int lane) {
+  __device__ __forceinline__ void values(const uint32_t (&pa)[S][3], const unsigned char* stage, const int (&live)[L::TB], float al, float* spec, int lane) {
     const int g = lane >> 2, t = lane & 3;
     uint32_t v[L::TB][4][L::VP][L::VB / 4], vs[KV == KV_FP4 ? L::TB : 1][2];
     const unsigned char* at[2] = {stage + L::place(t, g * L::VB), stage + L::place(t + 4, g * L::VB)};
@@ -405,6 +470,22 @@ struct BlockWarp {
       o[c][0] = fmaf(o[c][0], al, acc[0] + acc[2]);
       o[c][1] = fmaf(o[c][1], al, acc[1] + acc[3]);
     };
+    // the same for the n-tiles (turned: halves of an m-tile) c and d
+    auto add2 = [&](int c, int d, const uint32_t (&f0)[L::TB], const uint32_t (&f1)[L::TB], const uint32_t (&h0)[L::TB], const uint32_t (&h1)[L::TB]) {
+      if constexpr (TURN) {
+        float acc[4];
+#pragma unroll
+        for (int b = 0; b < L::TB; ++b) {
+          if (b == 0) mma<BF, true>(acc, f0[0], h0[0], f1[0], h1[0], pa[0][0], pa[0][1]);
+          else mma<BF>(acc, f0[b], h0[b], f1[b], h1[b], pa[b][0], pa[b][1]);
+        }
+        o[c][0] = fmaf(o[c][0], al, acc[0] + acc[1]);
+        o[d][0] = fmaf(o[d][0], al, acc[2] + acc[3]);
+      } else {
+        add(c, f0, f1);
+        add(d, h0, h1);
+      }
+    };
     uint32_t f[4][L::TB], f2[4][L::TB];
     if constexpr (KV == KV_BF16) {
 #pragma unroll
@@ -432,8 +513,7 @@ struct BlockWarp {
             e4m3x4_to_h2(x, f[0][b], f[1][b]);
             e4m3x4_to_h2(y, f2[0][b], f2[1][b]);
           }
-          add(4 * w + 2 * half, f[0], f2[0]);
-          add(4 * w + 2 * half + 1, f[1], f2[1]);
+          add2(4 * w + 2 * half, 4 * w + 2 * half + 1, f[0], f2[0], f[1], f2[1]);
         }
     } else {
       uint32_t sc[L::TB][2];
@@ -455,7 +535,7 @@ struct BlockWarp {
             for (int c = 0; c < 4; ++c) { f[c][b] = hmul2(x[c], sc[b][0]); f2[c][b] = hmul2(y[c], sc[b][1]); }
           }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) add(8 * w + 2 * c + odd, f[c], f2[c]);
+          for (int c = 0; c < 4; c += 2) add2(8 * w + 2 * c + odd, 8 * w + 2 * c + 2 + odd, f[c], f2[c], f[c + 1], f2[c + 1]);
         }
     }
   }
@@ -463,11 +543,17 @@ struct BlockWarp {
   // The warp's state to shared memory: so [head][D], sm_m and sm_l [head].
   __device__ __forceinline__ void leave(float* so, float* sm_m, float* sm_l, const float* spec, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    if constexpr (TURN) {
+      if (g == 0) { sm_m[t] = m; sm_l[t] = l; }
+#pragma unroll
+      for (int c = 0; c < L::NT; ++c) so[t * D + L::v_channel(g, c)] = o[c][0];
+      return;
+    }
     if (t == 0) { sm_m[g] = m; sm_l[g] = l; }
 #pragma unroll
     for (int c = 0; c < L::NT; ++c)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int ch = L::v_channel(2 * t + e, c);
         float x = o[c][e];
         if constexpr (FEW) x += __shfl_xor_sync(0xffffffffu, x, 16);
@@ -484,7 +570,7 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   using L = Lay<D, KV>;
   using Warp = BlockWarp<D, KV, FEW>;
   constexpr bool BF = L::BF;
-  __shared__ __align__(16) uint4 frag[L::KS * 32];
+  __shared__ __align__(16) typename Warp::Frag frag[L::KS * 32];
   __shared__ __align__(16) uint2 frag_lo[Warp::LOW ? L::KS * 32 : 1];
   extern __shared__ __align__(128) unsigned char ring[];              // [warp][K stages, V stages]
   float* so = reinterpret_cast<float*>(ring);                         // then [warp][head][D]
@@ -494,7 +580,7 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   const int hb = pair % a.hblocks, h = pair / a.hblocks % a.nkv, row = pair / a.hblocks / a.nkv;
   const int G = a.nq / a.nkv, gn = min(kBaHeads, G - hb * kBaHeads);
   const size_t head0 = (size_t)row * a.nq + (size_t)h * G + hb * kBaHeads;
-  const int g = (lane >> 2) & (FEW ? 3 : 7), t = lane & 3;             // the lane's head
+  const int g = Warp::TURN ? lane >> 3 : (lane >> 2) & (FEW ? 3 : 7), t = lane & 3;   // the head whose query the lane splits
 
   pdl_enter();
   Picks pk;
@@ -561,17 +647,19 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   fac = fmaxf(fac, 1.2e-38f);                                         // masked scores (-inf) stay -inf
   if (big >= 0x7f800000u) fac = __int_as_float(0x7fc00000);           // a non-finite query: its row is NaN
   if (t == 0) sm_fac[g] = fac;                                        // every warp the same
+  if constexpr (Warp::TURN) fac = __shfl_sync(0xffffffffu, fac, 8 * t);   // scores are of head t
 #pragma unroll
   for (int st = 0; st < L::KS; ++st) {
     uint32_t h0, h1, m0, m1, l0, l1;
     split<BF>(x[4 * st] * up, x[4 * st + 1] * up, h0, m0, l0);
     split<BF>(x[4 * st + 2] * up, x[4 * st + 3] * up, h1, m1, l1);
-    if constexpr (FEW) {
+    if constexpr (FEW && BF) {
       Warp::rows(h0, m0, l0, lane);
       Warp::rows(h1, m1, l1, lane);
     }
     if (st % warps == warp) {
-      frag[st * 32 + lane] = make_uint4(h0, m0, h1, m1);
+      if constexpr (Warp::TURN) frag[st * 32 + lane] = lane & 4 ? make_uint2(m0, m1) : make_uint2(h0, h1);
+      else frag[st * 32 + lane] = make_uint4(h0, m0, h1, m1);
       if constexpr (Warp::LOW) frag_lo[st * 32 + lane] = make_uint2(l0, l1);
     }
   }
@@ -587,8 +675,8 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
 #pragma unroll
       for (int i = 0; i < kBaStages; ++i) {
         if (!on[i]) { more = false; break; }
-        float s[2 * L::TB][2];
-        uint32_t pa[2 * L::TB][3];
+        float s[Warp::S][2];
+        uint32_t pa[Warp::S][3];
         int now[L::TB];
         asm volatile("cp.async.wait_group %0;" ::"n"(2 * kBaStages - 1) : "memory");
         __syncwarp();
@@ -606,15 +694,16 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
         request(i, true);
       }
     }
-    w.l += __shfl_xor_sync(0xffffffffu, w.l, 1);
-    w.l += __shfl_xor_sync(0xffffffffu, w.l, 2);
+    w.l = Warp::over_head(w.l, [](float x, float y) { return x + y; });
     if constexpr (!BF) break;
     // BF16 values may be infinite or NaN, and a product with a part that is 0 is
     // then NaN: such a warp goes through its blocks again and adds them apart.
     bool odd = false;
     if (!spec) {
 #pragma unroll
-      for (int c = 0; c < L::NT; ++c) odd |= !(fabsf(w.o[c][0]) <= 3.4e38f) || !(fabsf(w.o[c][1]) <= 3.4e38f);
+      for (int c = 0; c < L::NT; ++c)
+#pragma unroll
+        for (int e = 0; e < Warp::E; ++e) odd |= !(fabsf(w.o[c][e]) <= 3.4e38f);
       odd = odd && w.l <= 3.4e38f;
     }
     if (!__any_sync(0xffffffffu, odd)) break;
@@ -678,11 +767,12 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
 template <int D, int KV, bool FEW>
 long long ba_places(int warps, int num_sms) {
   using L = Lay<D, KV>;
-  constexpr int FIXED = L::KS * 32 * (BlockWarp<D, KV, FEW>::LOW ? 24 : 16) + 512 + 1024;   // fragments; sums; what a CTA is charged
+  using Warp = BlockWarp<D, KV, FEW>;
+  constexpr int FIXED = L::KS * 32 * ((int)sizeof(typename Warp::Frag) + (Warp::LOW ? 8 : 0)) + 512 + 1024;   // fragments; sums; what a CTA is charged
   return (long long)num_sms * std::min(ba_per_sm(D) / warps, (228 << 10) / (warps * L::WARP + FIXED));
 }
 
-template <int D, int KV, bool FEW = false>
+template <int D, int KV, bool FEW>
 cudaError_t ba_launch(const BlockAttnArgs& in, long long pairs, int num_sms, cudaStream_t s) {
   using L = Lay<D, KV>;
   BlockAttnArgs a = in;
@@ -705,7 +795,7 @@ cudaError_t ba_launch(const BlockAttnArgs& in, long long pairs, int num_sms, cud
                    a.warps * L::WARP, s, p, pdl_pays(pairs * a.cluster, num_sms), 100, a.cluster > 1 ? a.cluster : 0);
 }
 
-template <int D, int KV, bool FEW = false>
+template <int D, int KV, bool FEW>
 cudaError_t ba_init() {
   return cudaFuncSetAttribute((const void*)block_attention_kernel<D, KV, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kBaWarps * Lay<D, KV>::WARP);
@@ -719,21 +809,25 @@ cudaError_t launch_block_attention(const BlockAttnArgs& in, int num_sms, cudaStr
   const long long pairs = (long long)a.n * a.nkv * a.hblocks;
   if (pairs * kBaCluster > 0x7fffffffLL || a.k > 0x7fffffff - 32 * kBaWarps * kBaCluster) return cudaErrorInvalidValue;
   const bool wide = a.d == 128;
-  if (a.kv == KV_BF16 && a.nq / a.nkv <= 4) return wide ? ba_launch<128, KV_BF16, true>(a, pairs, num_sms, s) : ba_launch<64, KV_BF16, true>(a, pairs, num_sms, s);
-  if (a.kv == KV_BF16) return wide ? ba_launch<128, KV_BF16>(a, pairs, num_sms, s) : ba_launch<64, KV_BF16>(a, pairs, num_sms, s);
-  if (a.kv == KV_E4M3) return wide ? ba_launch<128, KV_E4M3>(a, pairs, num_sms, s) : ba_launch<64, KV_E4M3>(a, pairs, num_sms, s);
-  return wide ? ba_launch<128, KV_FP4>(a, pairs, num_sms, s) : ba_launch<64, KV_FP4>(a, pairs, num_sms, s);
+  const bool few = a.nq / a.nkv <= 4;
+  auto go = [&](auto kv) {
+    constexpr int KV = decltype(kv)::value;
+    return wide ? few ? ba_launch<128, KV, true>(a, pairs, num_sms, s) : ba_launch<128, KV, false>(a, pairs, num_sms, s)
+                : few ? ba_launch<64, KV, true>(a, pairs, num_sms, s) : ba_launch<64, KV, false>(a, pairs, num_sms, s);
+  };
+  if (a.kv == KV_BF16) return go(std::integral_constant<int, KV_BF16>());
+  if (a.kv == KV_E4M3) return go(std::integral_constant<int, KV_E4M3>());
+  return go(std::integral_constant<int, KV_FP4>());
 }
 
 cudaError_t block_attention_init() {
-  cudaError_t e = ba_init<64, KV_BF16>();
-  if (e == cudaSuccess) e = ba_init<128, KV_BF16>();
-  if (e == cudaSuccess) e = ba_init<64, KV_BF16, true>();
-  if (e == cudaSuccess) e = ba_init<128, KV_BF16, true>();
-  if (e == cudaSuccess) e = ba_init<64, KV_E4M3>();
-  if (e == cudaSuccess) e = ba_init<128, KV_E4M3>();
-  if (e == cudaSuccess) e = ba_init<64, KV_FP4>();
-  return e == cudaSuccess ? ba_init<128, KV_FP4>() : e;
+  for (auto init : {ba_init<64, KV_BF16, false>, ba_init<128, KV_BF16, false>, ba_init<64, KV_BF16, true>, ba_init<128, KV_BF16, true>,
+                    ba_init<64, KV_E4M3, false>, ba_init<128, KV_E4M3, false>, ba_init<64, KV_E4M3, true>, ba_init<128, KV_E4M3, true>,
+                    ba_init<64, KV_FP4, false>, ba_init<128, KV_FP4, false>, ba_init<64, KV_FP4, true>, ba_init<128, KV_FP4, true>}) {
+    const cudaError_t e = init();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace mbt
