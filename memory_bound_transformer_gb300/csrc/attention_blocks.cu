@@ -34,8 +34,8 @@
 // 48.7 (5.6 TB/s; the copies alone 46.8 with three warps a CTA, 52.8 then), 128 rows 88
 // (6.2 TB/s); 64 rows of 64 + 2 x 8 over 128 e4m3 blocks 51.8 (copies 48), over 128 4-bit
 // blocks 54 (copies 32: issue); 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks each
-// 64 (issue); one row of 32 + 2 x 8 heads of 128 over 64 BF16
-// blocks 8.4, of which some 7 are the launch, four round trips (position, entry, table,
+// 59.5 (issue); one row of 32 + 2 x 8 heads of 128 over 64 BF16
+// blocks 8.0, of which some 7 are the launch, four round trips (position, entry, table,
 // block) and the merge.
 #include <algorithm>
 #include <type_traits>
@@ -611,24 +611,31 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   Warp w;
   unsigned char* mine = ring + warp * L::RING;
   const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(mine);
-  int blk[kBaStages][L::TB], live[kBaStages][L::TB];                  // of the steps under way
+  // Steps in one body of code, or one for each stage. The former saves fetches of
+  // instructions where a step is long (510 rows over 4-bit blocks of 64 channels 59.5 us
+  // against 64.2; 256 rows of eight heads 58 against 59.5) or BF16 is read for few heads
+  // (one row 8.0 against 8.3, 64 rows the same); the latter registers (64 rows, 128
+  // channels: e4m3 51.6 against 52.2, 4-bit 24.7 against 25.5, BF16 of 8 heads 51.1
+  // against 51.7).
+  constexpr bool ROLLED = L::TB == 4 || (BF && FEW);
+  int blk[L::TB], live[kBaStages][L::TB];                             // of the last step and of those under way
   bool on[kBaStages];
   auto step = [&](int i) {                                            // the next step's blocks
     on[i] = pk.any();
 #pragma unroll
     for (int b = 0; b < L::TB; ++b)
-      if (on[i]) pk.take(blk[i][b], live[i][b], pos);
+      if (on[i]) pk.take(blk[b], live[i][b], pos);
   };
-  auto request = [&](int i, bool v) {
-    if (on[i]) w.request(mine_at + ((v ? kBaStages : 0) + i) * L::STAGE, v ? vpool : kpool, blk[i], a.nkv, h, lane);
+  auto request = [&](bool there, int stage, bool v) {
+    if (there) w.request(mine_at + ((v ? kBaStages : 0) + stage) * L::STAGE, v ? vpool : kpool, blk, a.nkv, h, lane);
     else asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto begin = [&]() {
 #pragma unroll
     for (int i = 0; i < kBaStages; ++i) {
       step(i);
-      request(i, false);
-      request(i, true);
+      request(on[i], i, false);
+      request(on[i], i, true);
     }
   };
   begin();
@@ -669,29 +676,50 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   w.start();
 #pragma unroll 1
   while (true) {
-    bool more = true;
+    auto turn = [&](int at, int slot) {                               // the step in this stage and place of `live`
+      float s[Warp::S][2];
+      uint32_t pa[Warp::S][3];
+      int now[L::TB];
+      asm volatile("cp.async.wait_group %0;" ::"n"(2 * kBaStages - 1) : "memory");
+      __syncwarp();
+      w.scores(s, mine + at * L::STAGE, frag, frag_lo, lane);
+#pragma unroll
+      for (int b = 0; b < L::TB; ++b) now[b] = live[slot][b];
+      if constexpr (ROLLED) {
+        slot = kBaStages - 1;
+#pragma unroll
+        for (int i = 0; i < kBaStages - 1; ++i) {
+          on[i] = on[i + 1];
+#pragma unroll
+          for (int b = 0; b < L::TB; ++b) live[i][b] = live[i + 1][b];
+        }
+      }
+      __syncwarp();                                                   // the keys' stage may be refilled
+      step(slot);
+      request(on[slot], at, false);
+      const float al = w.soften(s, pa, now, fac, lane);
+      asm volatile("cp.async.wait_group %0;" ::"n"(2 * kBaStages - 1) : "memory");
+      __syncwarp();
+      w.values(pa, mine + (kBaStages + at) * L::STAGE, now, al, spec, lane);
+      __syncwarp();
+      request(on[slot], at, true);
+    };
+    if constexpr (ROLLED) {
+      int at = 0;
 #pragma unroll 1
-    while (more) {
+      while (on[0]) {
+        turn(at, 0);
+        at = at == kBaStages - 1 ? 0 : at + 1;
+      }
+    } else {
+      bool more = true;
+#pragma unroll 1
+      while (more) {
 #pragma unroll
-      for (int i = 0; i < kBaStages; ++i) {
-        if (!on[i]) { more = false; break; }
-        float s[Warp::S][2];
-        uint32_t pa[Warp::S][3];
-        int now[L::TB];
-        asm volatile("cp.async.wait_group %0;" ::"n"(2 * kBaStages - 1) : "memory");
-        __syncwarp();
-        w.scores(s, mine + i * L::STAGE, frag, frag_lo, lane);
-#pragma unroll
-        for (int b = 0; b < L::TB; ++b) now[b] = live[i][b];
-        __syncwarp();                                                 // the keys' stage may be refilled
-        step(i);
-        request(i, false);
-        const float al = w.soften(s, pa, now, fac, lane);
-        asm volatile("cp.async.wait_group %0;" ::"n"(2 * kBaStages - 1) : "memory");
-        __syncwarp();
-        w.values(pa, mine + (kBaStages + i) * L::STAGE, now, al, spec, lane);
-        __syncwarp();
-        request(i, true);
+        for (int i = 0; i < kBaStages; ++i) {
+          if (!on[i]) { more = false; break; }
+          turn(i, i);
+        }
       }
     }
     w.l = Warp::over_head(w.l, [](float x, float y) { return x + y; });
