@@ -382,7 +382,8 @@ __device__ __forceinline__ void score_blocks(const SelQuery<D>& m, const BlockSe
       const float sc = __shfl_sync(0xffffffffu, scale, r);
       if (i < cnt && l % SAME == 0) {
         const float inf = __int_as_float(0x7f800000);
-        put(i, j < a.keep_first || j >= w.held - a.keep_last ? kKept : key_of(sc < inf ? (float)total * sc : inf));
+        // no scale that is not finite: 0 times -infinity would be a NaN, whose bits are kKept
+        put(i, j < a.keep_first || j >= w.held - a.keep_last ? kKept : key_of(fabsf(sc) < inf ? (float)total * sc : inf));
       }
     }
   }
