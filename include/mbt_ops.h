@@ -362,11 +362,12 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
  * t <= positions[i] of the blocks sel[i][KV head of h][0 .. k). Negative entries
  * of sel are skipped; one beyond the row's context sets MBT_DEV_BLOCK_RANGE and
  * is skipped. Entries may come in any order; a block entered twice counts twice.
- * A row that is left with no token, or outside its table, is 0. q [n][nq][d]
- * fp32, out [n][nq * d] fp32. An out-of-range id reads the null block. Cache
- * contents past a row's position never reach it. A query that is not finite
- * makes its row NaN in that head, a key that is not the rows that attend to it;
- * an infinity or a NaN in V reaches them in its channel. Queries and
+ * A row that is left with no token, or outside its table, is 0 whatever its
+ * query. q [n][nq][d] fp32, out [n][nq * d] fp32. An out-of-range id reads the
+ * null block. Cache contents past a row's position never reach it. A query that
+ * is not finite makes its row, if that has a token, NaN in that head, a key that
+ * is not the rows that attend to it; an infinity or a NaN in V reaches them in its
+ * channel. Queries and
  * probabilities are exact to 2^-24 over a BF16 cache, whose values' sum over the
  * row's tokens has to stay in fp32's range, and to 2^-22 over the others,
  * probabilities below 2^-17 of the row's largest to 2^-39 of that. */

@@ -7,7 +7,8 @@ attention's are derived at each test."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_blocks import Select
+from memory_bound_transformer_gb300 import capi
+from tests.test_gpu_blocks import ALL, Attend, Select
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,27 @@ def test_select_scales_of_minus_infinity(cuda_lib, d, width):
     c.check()
     c.codes[:] = 0
     c.check()
+
+
+# ---------------------------------------------------------------------------
+# attention
+
+@pytest.mark.parametrize("kind", ALL)
+@pytest.mark.parametrize("nq,d", [(8, 64), (14, 128), (8, 128), (14, 64)])
+@pytest.mark.parametrize("n,k", [(6, 40), (6, 3), (400, 3)])
+def test_attention_rows_without_a_token(cuda_lib, kind, nq, d, n, k):
+    """They are 0 (the tolerance there is 0 too) whatever the query, in CTAs and in clusters: empty lists, rows outside the
+    table, and, flagged as well, lists of blocks behind the context."""
+    c = Attend(kind, nq, 2, d, [700, 20, 333], k, seed=50, rows=[(i % 3, (699, 19, 332)[i % 3]) for i in range(n)])
+    bad = (np.nan, np.inf, -np.inf, np.nan, np.inf)
+    for i in range(5):
+        c.q[i, i % nq::2, 7] = bad[i]
+    c.q[4] = np.nan
+    c.sel[0] = -1
+    c.sel[1], c.sel[3] = 0, 0
+    c.seq[1], c.pos[1] = 3, 0                                        # a padding row
+    c.sel[2] = 44
+    c.pos[3] = -1
+    c.sel[4, 0], c.sel[4, 1] = -7, 2 ** 31 - 1
+    got = c.check(capi.DEV_POS_RANGE | capi.DEV_BLOCK_RANGE)
+    assert not got[:5].any() and got[5].any()
