@@ -367,10 +367,11 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
  * null block. Cache contents past a row's position never reach it. A query that
  * is not finite makes its row, if that has a token, NaN in that head, a key that
  * is not the rows that attend to it; an infinity or a NaN in V reaches them in its
- * channel. Queries and
- * probabilities are exact to 2^-24 over a BF16 cache, whose values' sum over the
- * row's tokens has to stay in fp32's range, and to 2^-22 over the others,
- * probabilities below 2^-17 of the row's largest to 2^-39 of that. */
+ * channel. Twice a query's product with a key as the cache holds it (before
+ * k_scale) has to stay in fp32's range, and so has the sum of a BF16 cache's
+ * values over the row's tokens. Queries and probabilities are exact to 2^-24 over
+ * a BF16 cache and to 2^-22 over the others, probabilities below 2^-17 of the
+ * row's largest to 2^-39 of that. */
 int op_block_attention(int n, const float* q, int nq, int nkv, int d, const void* kpool, const void* vpool, int kv_dtype,
                        float k_scale, float v_scale, const int32_t* positions, const int32_t* row_seq, int nseq,
                        const int32_t* bt, int bt_stride, const int32_t* sel, int k, int num_blocks, float* out,

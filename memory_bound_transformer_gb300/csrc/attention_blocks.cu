@@ -642,13 +642,16 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
 
   // The queries' fragments, while the first blocks are under way. A power of two
   // per head brings the largest into FP16's range, or (BF16) a tiny one away from
-  // the smallest numbers; `fac` takes scores back to the log2 domain.
+  // the smallest numbers: below 2^-9, so that D products with keys below 2^128, and
+  // differences of such sums, stay in fp32's range, and no further than `fac`, which
+  // takes scores back to the log2 domain, is a normal number.
   uint32_t big = 0;                                                   // largest magnitude's bits; a NaN's are larger than inf's
 #pragma unroll
   for (int i = 0; i < D / 4; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
   big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
   big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-  const int ex = (int)(big >> 23), e = BF ? (ex < 87 ? min(120, 127 - ex) : 0) : min(120, 140 - ex);
+  const int ex = (int)(big >> 23), ks = (int)(__float_as_uint(a.k_scale) >> 23) - 127;
+  const int e = BF ? (ex < 87 ? min(117 - ex, 122 + ks) : 0) : min(120, 140 - ex);
   const float up = __int_as_float((e + 127) << 23);
   float fac = 1.4426950408889634f / sqrtf((float)D) * a.k_scale * __int_as_float((127 - e) << 23);
   fac = fmaxf(fac, 1.2e-38f);                                         // masked scores (-inf) stay -inf

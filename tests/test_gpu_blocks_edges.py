@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 from memory_bound_transformer_gb300 import capi
+from oracle.numerics import bf16_decode, round_bf16
 from tests.test_gpu_blocks import ALL, Attend, Select
 
 pytestmark = pytest.mark.gpu
@@ -56,3 +57,22 @@ def test_attention_rows_without_a_token(cuda_lib, kind, nq, d, n, k):
     c.sel[4, 0], c.sel[4, 1] = -7, 2 ** 31 - 1
     got = c.check(capi.DEV_POS_RANGE | capi.DEV_BLOCK_RANGE)
     assert not got[:5].any() and got[5].any()
+
+
+@pytest.mark.parametrize("nq", [8, 14])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q,k,scale", [(-60, 124, -64), (-124, 124, 0), (-118, 118, 0), (-41, 105, -64), (-90, 120, -30), (-140, 124, 16),
+                                       (-100, 124, -64), (-140, 124, -64), (-60, 124, 0), (-100, 124, 30), (-45, 110, 0), (-140, 124, 64)])
+def test_attention_tiny_queries_and_huge_keys(cuda_lib, nq, d, q, k, scale):
+    """BF16 queries, keys and k_scale of 2^q, 2^k and 2^scale: the sums in between stay in range too. Scores of ordinary size
+    or smaller are as exact as ordinary ones, which 2e-5 * max |V| allows for. Where they are far larger, one channel
+    alone counts: keys that differ do by 2^-8 of a score beyond 2^40, so that all but the largest ones' shares are 0."""
+    c = Attend("bf16", nq, 2, d, [700, 20, 333], 40, seed=51, kg=2.0 ** scale)
+    c.kp = round_bf16((bf16_decode(c.kp) * 2.0 ** k).astype(np.float32))
+    if q + k + scale > 0:
+        keep = np.zeros_like(c.q)
+        keep[..., 3] = c.q[..., 3]
+        c.q = keep
+    c.q[:, 1::2] = (c.q[:, 1::2].astype(np.float64) * 2.0 ** q).astype(np.float32)
+    c.q[:, ::2] = (c.q[:, ::2].astype(np.float64) * 2.0 ** (q - 3)).astype(np.float32)
+    c.check()
