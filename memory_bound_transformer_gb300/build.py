@@ -27,12 +27,18 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _stale(src: str, obj: str) -> bool:
-    if not os.path.exists(obj):
+def _deps(src: str):
+    """A source and every header it may include."""
+    inc = os.path.join(os.path.dirname(PKG), "include")
+    return [src] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
+        os.path.join(inc, f) for f in os.listdir(inc)]
+
+
+def _older(target: str, deps) -> bool:
+    """Whether a file is missing or older than one of those it is made from."""
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(obj)
-    deps = [src] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    deps += [os.path.join(PKG, "..", "include", f) for f in os.listdir(os.path.join(PKG, "..", "include"))]
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -48,6 +54,56 @@ def _binding_flags():
             [f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-L{PKG}", "-lmbt", "-Wl,-rpath,$ORIGIN"])
 
 
+def _binding_stamp(flags) -> str:
+    """What the extension's binary interface hangs on besides its sources."""
+    import torch
+    return "\n".join([sys.version, torch.__version__, *flags[0], *flags[1]]) + "\n"
+
+
+def _run(cmd):
+    return cmd, subprocess.run(cmd, capture_output=True, text=True)
+
+
+def _check(results, what: str, verbose: bool = False) -> None:
+    bad = False
+    for cmd, r in results:
+        if verbose or r.returncode:
+            sys.stderr.write(r.stdout + r.stderr)
+        if r.returncode:
+            bad = True
+            sys.stderr.write("FAILED: " + " ".join(cmd) + "\n")
+    if bad:
+        raise RuntimeError(what + " failed")
+
+
+def _link(cmd, out: str, what: str) -> None:
+    """A linked file appears whole; where that fails the old one is gone."""
+    if os.path.exists(out):
+        os.remove(out)
+    part = f"{out}.{os.getpid()}.part"
+    try:
+        _check([_run([*cmd, "-o", part])], what)
+        os.replace(part, out)
+    finally:
+        if os.path.exists(part):
+            os.remove(part)
+
+
+def _compile_binding(flags, verbose: bool) -> str:
+    """The extension's object, for this Python and this torch."""
+    src, obj, stamp = os.path.join(CSRC, "binding.cpp"), os.path.join(OBJ, "binding.o"), os.path.join(OBJ, "binding.stamp")
+    want = _binding_stamp(flags)
+    same = os.path.exists(stamp) and open(stamp).read() == want
+    if not same or _older(obj, _deps(src)):
+        for f in (stamp, obj, BINDING):                    # what a failure leaves missing is made the next time
+            if os.path.exists(f):
+                os.remove(f)
+        _check([_run(["g++", *flags[0], "-c", src, "-o", obj])], "g++", verbose)
+        with open(stamp, "w") as f:
+            f.write(want)
+    return obj
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     cc = nvcc()
@@ -55,46 +111,23 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     for src in SOURCES:
         s = os.path.join(CSRC, src)
         o = os.path.join(OBJ, src.replace(".cu", ".o"))
-        if _stale(s, o) or ptxas_info:
+        if _older(o, _deps(s)) or ptxas_info:
             cmd = [cc, *ARCH, *FLAGS, "-c", s, "-o", o]
             if ptxas_info:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
-
-    bsrc, bobj = os.path.join(CSRC, "binding.cpp"), os.path.join(OBJ, "binding.o")
-    compile_flags, link_flags = _binding_flags()
-    nvcc_jobs = len(jobs)
-    if _stale(bsrc, bobj):
-        jobs.insert(0, ["g++", *compile_flags, "-c", bsrc, "-o", bobj])
-    rebind = len(jobs) > nvcc_jobs
-
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        return cmd, r
-
-    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
-        results = list(ex.map(run, jobs))
-    failed = False
-    for cmd, r in results:
-        if verbose or ptxas_info or r.returncode:
-            sys.stderr.write(r.stdout + r.stderr)
-        if r.returncode:
-            failed = True
-            sys.stderr.write("FAILED: " + " ".join(cmd) + "\n")
-    if failed:
-        raise RuntimeError("nvcc failed")
+    flags = _binding_flags()
+    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_compile_binding, flags, verbose)
+        _check(list(ex.map(_run, jobs)), "nvcc", verbose or ptxas_info)
     objs = [os.path.join(OBJ, s.replace(".cu", ".o")) for s in SOURCES]
-    if nvcc_jobs or not os.path.exists(LIB):
-        link = [cc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"]
-        r = subprocess.run(link, capture_output=True, text=True)
-        if r.returncode:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link failed")
-    if rebind or not os.path.exists(BINDING):
-        r = subprocess.run(["g++", "-shared", bobj, "-o", BINDING, *link_flags], capture_output=True, text=True)
-        if r.returncode:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link of the binding failed")
+    if _older(LIB, objs):
+        if os.path.exists(BINDING):                        # it calls the library by the old one's signatures
+            os.remove(BINDING)
+        _link([cc, *ARCH, "-shared", *objs, "-lcudart"], LIB, "link")
+    bobj = binding.result()
+    if _older(BINDING, [bobj, LIB]):
+        _link(["g++", "-shared", bobj, *flags[1]], BINDING, "link of the binding")
     return LIB
 
 
