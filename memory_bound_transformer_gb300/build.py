@@ -1,7 +1,11 @@
 """Build libmbt.so in-tree for sm_103a with nvcc (one process per translation
-unit, in parallel, then one link) and the native part of the Python binding. Usage: python -m memory_bound_transformer_gb300.build"""
+unit, in parallel, then one link) and the native part of the Python binding.
+Usage: python -m memory_bound_transformer_gb300.build [--library]
+The library needs nvcc alone. The extension also needs torch, Python's headers
+and g++; --library leaves it out, and so does a Python without torch."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -104,7 +108,8 @@ def _compile_binding(flags, verbose: bool) -> str:
     return obj
 
 
-def build(verbose: bool = False, ptxas_info: bool = False) -> str:
+def build(verbose: bool = False, ptxas_info: bool = False, library_only: bool = False) -> str:
+    """Makes what is missing or out of date; the library's path. A failure of the extension leaves the library made."""
     os.makedirs(OBJ, exist_ok=True)
     cc = nvcc()
     jobs = []
@@ -116,20 +121,26 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             if ptxas_info:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
-    flags = _binding_flags()
+    flags = None
+    if not library_only:
+        if importlib.util.find_spec("torch"):
+            flags = _binding_flags()
+        else:
+            sys.stderr.write("no torch: the Python extension is left out\n")
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
-        binding = ex.submit(_compile_binding, flags, verbose)
+        binding = ex.submit(_compile_binding, flags, verbose) if flags else None
         _check(list(ex.map(_run, jobs)), "nvcc", verbose or ptxas_info)
     objs = [os.path.join(OBJ, s.replace(".cu", ".o")) for s in SOURCES]
     if _older(LIB, objs):
         if os.path.exists(BINDING):                        # it calls the library by the old one's signatures
             os.remove(BINDING)
         _link([cc, *ARCH, "-shared", *objs, "-lcudart"], LIB, "link")
-    bobj = binding.result()
-    if _older(BINDING, [bobj, LIB]):
-        _link(["g++", "-shared", bobj, *flags[1]], BINDING, "link of the binding")
+    if binding:
+        bobj = binding.result()
+        if _older(BINDING, [bobj, LIB]):
+            _link(["g++", "-shared", bobj, *flags[1]], BINDING, "link of the binding")
     return LIB
 
 
 if __name__ == "__main__":
-    print(build(verbose=True, ptxas_info="--ptxas" in sys.argv))
+    print(build(verbose=True, ptxas_info="--ptxas" in sys.argv, library_only="--library" in sys.argv))

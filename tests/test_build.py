@@ -1,5 +1,6 @@
 """The build's own logic, with stand-ins for the compilers in a folder of its own:
 what is made again after a change, a failure, or under another torch."""
+import importlib.util
 import os
 import time
 
@@ -112,3 +113,27 @@ def test_nothing_half_linked(tree):
     tree.change("pkg", "csrc", "a.cu")
     tree.fails("nvcc", "link")
     assert sorted(f.name for f in (tree.root / "pkg").iterdir()) == ["_build", "csrc"]
+
+
+def test_the_library_needs_nvcc_alone(tree, monkeypatch):
+    """Without torch it is made, and no extension stays beside it."""
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    tree.change("include", "ops.h")
+    got = tree.build()
+    assert got and all(c.startswith("nvcc") for c in got) and tree.lib.exists() and not tree.ext.exists()
+
+
+def test_the_library_asked_for_alone(tree):
+    tree.change("pkg", "csrc", "common.cuh")
+    tree.log.write_text("")
+    b.build(library_only=True)
+    assert all(c.startswith("nvcc") for c in tree.log.read_text().splitlines()) and tree.lib.exists() and not tree.ext.exists()
+    assert all(c.startswith("g++") for c in tree.build()) and tree.ext.exists()
+
+
+def test_a_broken_extension_leaves_the_library(tree):
+    tree.lib.unlink(), tree.ext.unlink()
+    tree.change("pkg", "csrc", "binding.cpp")
+    tree.fails("g++", "compile")
+    assert tree.lib.exists() and not tree.ext.exists()
