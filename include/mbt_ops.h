@@ -275,8 +275,11 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
  * k blocks per KV head instead, chosen by a bound on its scores that costs 1/32
  * of the BF16 cache's bytes, and lay out a step's rows on the GPU. In the order
  * of a serving step: op_kv_extend (blocks and rows for the new tokens), the
- * cache write (op_rope_kv_write, op_rope_kv_write_fp4), op_key_bounds (the
- * ranges of the blocks written to), op_block_select, op_block_attention.
+ * cache write, op_key_bounds (the ranges of the blocks written to),
+ * op_block_select, op_block_attention. The write is op_rope_kv_write_fp4 for a
+ * 4-bit cache. op_rope_kv_write has no row_seq: it fits a step in which every
+ * sequence gets one token, so that row i is sequence i; the k and v of any other
+ * step's rows the caller stores in a BF16 or e4m3 cache, at slots[i].
  * All take cache formats, head sizes, groups, scales and table widths as the
  * 4-bit section above says, up to 2^30 rows, 2^16 KV heads and 2^26 chosen
  * blocks per row and head (the last two entry points 2^28 products of rows, KV
@@ -295,7 +298,8 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
  *   held[nseq]          tokens afterwards
  *   cu_seqlens[nseq+1]  first packed row of each sequence's new tokens
  *   positions, row_seq, slots [n]: position, sequence and cache slot (block id *
- *                       16 + position % 16) of each packed row. Rows from
+ *                       16 + position % 16, for writes of the caller's own) of
+ *                       each packed row. Rows from
  *                       cu_seqlens[nseq] on are padding: sequence nseq,
  *                       position 0, slot num_blocks * 16 (the null block; a table
  *                       with one more row that names it makes the other entry
