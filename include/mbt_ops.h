@@ -282,9 +282,10 @@ int op_prompt_attention(int n, const float* q, int nq, int nkv, int d, int nseq,
  * step's rows the caller stores in a BF16 or e4m3 cache, at slots[i].
  * All take cache formats, head sizes, groups, scales and table widths as the
  * 4-bit section above says, up to 2^30 rows, 2^16 KV heads and 2^26 chosen
- * blocks per row and head (the last two entry points 2^28 products of rows, KV
- * heads and groups of eight query heads), and rows of any sequences: row i is at positions[i]
- * of sequence row_seq[i] (NULL: sequence i, nseq >= n) of bt [nseq][bt_stride].
+ * blocks per row and head (the last two entry points fewer than 2^28 products of
+ * rows, KV heads and groups of eight query heads), and rows of any sequences: row
+ * i is at positions[i] of sequence row_seq[i] (NULL: sequence i, nseq >= n) of bt
+ * [nseq][bt_stride].
  * A row whose position or sequence is outside the table sets MBT_DEV_POS_RANGE;
  * an out-of-range block id sets MBT_DEV_BLOCK_RANGE. They keep nothing between
  * calls, and but for op_block_select's long tables use no scratch memory. */
@@ -373,9 +374,12 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
  * is not the rows that attend to it; an infinity or a NaN in V reaches them in its
  * channel. Twice a query's product with a key as the cache holds it (before
  * k_scale) has to stay in fp32's range, and so has the sum of a BF16 cache's
- * values over the row's tokens. Queries and probabilities are exact to 2^-24 over
- * a BF16 cache and to 2^-22 over the others, probabilities below 2^-17 of the
- * row's largest to 2^-39 of that. */
+ * values over the row's tokens. Queries and probabilities enter the products to
+ * 2^-24 over a BF16 cache and to 2^-22 over the others, probabilities below 2^-17
+ * of the row's largest to 2^-39 of that. Scores are sums in fp32, off by about
+ * 2^-22 of sum_i |q_i k_i| / sqrt(d); a probability is off by 2^-22 of itself, for
+ * the exponential, and by 2^-21 for every factor of e between it and the row's
+ * largest, for its argument's roundings. */
 int op_block_attention(int n, const float* q, int nq, int nkv, int d, const void* kpool, const void* vpool, int kv_dtype,
                        float k_scale, float v_scale, const int32_t* positions, const int32_t* row_seq, int nseq,
                        const int32_t* bt, int bt_stride, const int32_t* sel, int k, int num_blocks, float* out,

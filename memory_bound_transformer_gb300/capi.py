@@ -574,7 +574,8 @@ def op_block_select(q, nkv, bounds, scales, positions, bt, num_blocks, keep_firs
                     stream=None, scratch=None) -> None:
     """The blocks with the largest possible scores per row and KV head: q [n][nq][d] fp32, bounds and scales as
     op_key_bounds leaves them, sel [n][nkv][k] int32 (ascending places in the table, then -1). scratch: uint8 device
-    tensor of op_block_select_scratch(n, nkv, width, k) bytes; None takes it from torch's allocator, on the call's stream."""
+    tensor of op_block_select_scratch(n, nkv, width, k) bytes; None takes it from torch's allocator, on the call's stream (in
+    a capture that torch does not make, give it: the graph would go on using memory that torch has taken back)."""
     _check("op_block_select", _binding().op_block_select(q, nkv, bounds, scales, positions, bt, num_blocks, keep_first, keep_last,
                                                          sel, row_seq, scratch, err, _handle(stream)))
 

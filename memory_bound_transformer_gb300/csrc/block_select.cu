@@ -13,9 +13,10 @@
 // for every key of the block; the right side with the 8-bit codes is an exact
 // integer (|.| < 2^29: P - N <= 2^14, codes <= 127, 128 channels), so that no
 // order of summation can move a block over the border of the chosen ones. The
-// roundings only loosen the bound: a code by up to 1/63 of the block's largest key, a
-// query by 2^-11 of the group's largest; 8 bits and 11 keep a range at 1/32 of a BF16
-// block's bytes and the sum inside 32 bits. What is attended to is not rounded.
+// codes only loosen the bound, by up to 1/63 of the block's largest key a channel; u
+// moves it by up to 2^-10 of the group's largest query times the key. 8 bits and 11
+// keep a range at 1/32 of a BF16 block's bytes and the sum inside 32 bits. What is
+// attended to is not rounded.
 // Bound by the gather of the ranges, 2 d bytes each (6.2 TB/s alone for 256): four
 // byte products per instruction, on two bytes of each weight. Measured in a graph,
 // us, 32 + 2 x 8 heads of 128: one row over 2048 blocks 8.1 (five round trips, the
