@@ -753,16 +753,17 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   __syncthreads();
   // an infinity counts whatever its share
   auto share = [](float x, float f) { return x * (fabsf(x) > 3.4e38f ? 1.f : f); };
-  // what a part with maximum m and sum l counts by; one without a token, whose l is
-  // 0, nothing, even where the query makes the factor of its scores NaN
-  auto weight = [](float m, float mu, float l, float fac) { return l == 0.f ? 0.f : ex2((m - mu) * fac); };
+  // What a part with maximum m counts by. fmaxf turns a NaN into nothing: a part without
+  // a token is 0 then, also where the query makes the factor of its scores NaN (one
+  // with tokens is NaN itself).
+  auto weight = [](float m, float mu, float fac) { return ex2(fmaxf((m - mu) * fac, -INFINITY)); };
   for (int i = tid; i < gn * D; i += blockDim.x) {
     const int hr = i / D;
     float M = -INFINITY, Ls = 0.f, acc = 0.f;
     for (int v = 0; v < warps; ++v) M = fmaxf(M, sm_m[v][hr]);
     const float mu = M == -INFINITY ? 0.f : M;
     for (int v = 0; v < warps; ++v) {
-      const float f = weight(sm_m[v][hr], mu, sm_l[v][hr], sm_fac[hr]);
+      const float f = weight(sm_m[v][hr], mu, sm_fac[hr]);
       Ls = fmaf(sm_l[v][hr], f, Ls);
       acc += share(so[v * kBaHeads * D + i], f);
     }
@@ -788,7 +789,7 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
     const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int r = 0; r < kBaCluster; ++r) {
-      const float f = weight(pm[r], mu, pl[r], sm_fac[i / D]);
+      const float f = weight(pm[r], mu, sm_fac[i / D]);
       Ls = fmaf(pl[r], f, Ls);
       acc += share(po[r], f);
     }
