@@ -31,11 +31,12 @@
 // * Few (row, KV head) pairs are shared by clusters, many get CTAs of two warps or
 //   one, so that one wave of up to 12 warps per SM (16 at d = 64) holds them.
 // Measured in a graph, us: 64 rows of 32 + 2 x 8 heads of 128 over 64 BF16 blocks
-// 48.7 (5.6 TB/s; the copies alone 46.8 with three warps a CTA, 52.8 then), 128 rows 88
-// (6.2 TB/s); 64 rows of 64 + 2 x 8 over 128 e4m3 blocks 51.8 (copies 48), over 128 4-bit
-// blocks 54 (copies 32: issue); 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks each
-// 59.5 (issue); one row of 32 + 2 x 8 heads of 128 over 64 BF16
-// blocks 8.0, of which some 7 are the launch, four round trips (position, entry, table,
+// 47 to 48.5 (5.6 to 5.8 TB/s; the copies alone 46.8 with three warps a CTA, 52.8 then),
+// 128 rows 88 (6.2 TB/s); 64 rows of 64 + 2 x 8 heads of 128 over 128 e4m3 blocks 51.3
+// (copies 48), over 128 4-bit blocks 54 (copies 32: conversions and scales; 32 + 2 x 8
+// heads 42); 510 rows of 32 + 2 x 8 heads of 64 over 48 4-bit blocks each 59.7 (issue 67 %
+// while active, in 3.4 waves of CTAs); one row of 32 + 2 x 8 heads of 128 over 64 BF16
+// blocks 8.1, of which some 7 are the launch, four round trips (position, entry, table,
 // block) and the merge.
 #include <algorithm>
 #include <type_traits>
@@ -612,11 +613,12 @@ __global__ void __launch_bounds__(32 * kBaWarps, ba_per_sm(D) / kBaWarps) block_
   unsigned char* mine = ring + warp * L::RING;
   const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(mine);
   // Steps in one body of code, or one for each stage. The former saves fetches of
-  // instructions where a step is long (510 rows over 4-bit blocks of 64 channels 59.5 us
-  // against 64.2; 256 rows of eight heads 58 against 59.5) or BF16 is read for few heads
-  // (one row 8.0 against 8.3, 64 rows the same); the latter registers (64 rows, 128
-  // channels: e4m3 51.6 against 52.2, 4-bit 24.7 against 25.5, BF16 of 8 heads 51.1
-  // against 51.7).
+  // instructions where a step is long or BF16 is read for few heads, the latter
+  // registers. In a graph, us, one body against one per stage: 4-bit blocks of d = 64,
+  // 510 rows of 32 + 2 x 8 heads over 48 59.7 and 63.6, 256 rows of 64 + 2 x 8 over 64 58.0
+  // and 59.0; BF16 blocks of d = 128, 32 + 2 x 8 heads over 64, one row 8.2 and 8.6, 64
+  // rows 48.1 and 47.8. The other way about, d = 128: 64 rows of 64 + 2 x 8 heads over 128
+  // e4m3 blocks 52.8 and 52.1, 128 4-bit blocks 55.8 and 54.7, 64 BF16 blocks 51.8 and 51.5.
   constexpr bool ROLLED = L::TB == 4 || (BF && FEW);
   int blk[L::TB], live[kBaStages][L::TB];                             // of the last step and of those under way
   bool on[kBaStages];
@@ -812,15 +814,26 @@ cudaError_t ba_launch(const BlockAttnArgs& in, long long pairs, int num_sms, cud
   using L = Lay<D, KV>;
   BlockAttnArgs a = in;
   // Four warps a CTA while one wave holds all pairs, then two, then one, and two again for
-  // several waves. 64 rows of 8 KV heads over 64 BF16 blocks (512 pairs; 4 heads a
-  // KV head; us): four warps 61, three 51, two 48, one 53; 40 rows 36, 34, 35, 48; 112
-  // rows 83, 82, 94, 78; 256 rows 170, 170, 165, 180. e4m3, 8 heads: 40 rows 24 (four), 29
-  // (two); 64 rows 44, 32; 128 rows 67, 74, and 57 with one.
+  // several waves. In a graph, us, four, three, two and one warps, 8 KV heads of 128, 64
+  // blocks: BF16, 32 query heads, 40 rows 36, 34, 35, 48; 64 rows 61, 52, 49, 53; 112 rows
+  // 83, 82, 95, 79; 256 rows 168, 169, 165, 181. e4m3, 64 query heads, 40 rows 25, 28, 29,
+  // 41; 64 rows 44, 35, 32, 43; 128 rows 68, 61, 75, 58.
   a.warps = pairs <= ba_places<D, KV, FEW>(4, num_sms) ? 4 : pairs <= ba_places<D, KV, FEW>(2, num_sms) ? 2
           : pairs <= ba_places<D, KV, FEW>(1, num_sms) ? 1 : 2;
-  // Clusters of a power of two (seven CTAs for 64 pairs: 23 us, four 14, one 17) while pairs
-  // are few: up to 4/3 CTAs per SM over BF16 caches, which bound by memory, 8/3 over
-  // the others (64 pairs over 256 4-bit blocks, d = 64: four 13 us, two 18, one 28), no warp with less than a step, or from 32 pairs on than four blocks.
+  // Clusters of a power of two while pairs are few: up to 4/3 CTAs per SM over BF16
+  // caches, which bound by memory, 8/3 over the others, no warp with less than a step, or
+  // from 33 pairs on than four blocks. In a graph, us, one, two, four and eight CTAs a
+  // pair, 32 + 2 x 8 heads of 128 over 64 blocks (* taken; seven CTAs for 64 pairs 23):
+  //   rows  BF16                      e4m3                     4-bit
+  //   1     15.7 12.1  9.2  8.1*      9.6  8.2  6.7  5.6*      10.6  8.8  7.1  6.0*
+  //   4     16.2 12.5 10.1* 11.7     10.6  9.4  7.9  8.6*      11.8 10.1  8.5  8.4*
+  //   8     16.4 13.2* 14.1 23.6     10.8  9.8  9.9* 15.4      12.0 10.3  9.7* 15.9
+  //   16    17.5* 19.4 30.1 36.1     11.5 12.8* 18.3 23.4      12.2 12.4* 18.5 24.1
+  //   24    23.4* 26.7 33.3 48.3     14.6 15.9* 20.7 31.2      15.3 14.8* 20.3 32.0
+  // and of shorter lists: 4 rows over 16 blocks 8.5 8.5 7.7* 9.8, 5.6 6.1* 5.7 7.0, 6.2 6.4*
+  // 6.2 7.4; 6 rows over 16 blocks 8.6* 8.8 10.0 11.6, 6.0* 6.4 7.2 8.1, 6.3* 6.5 7.3 8.3; 8 over
+  // 32 11.3 10.4* 11.7 21.1, 8.0 8.3* 8.5 14.7, 8.8 8.7* 8.4 15.5. d = 64, 8 rows over 256 4-bit
+  // blocks: 20.7 13.4 11.4* 11.7.
   const long long room = (L::BF ? 4LL : 8LL) * num_sms / 3 / pairs, least = std::max(L::TB, pairs > 32 ? 4 : 1);
   const long long most = std::min(room, a.k / (kBaWarps * least));
   a.cluster = 1;

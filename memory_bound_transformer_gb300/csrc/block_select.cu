@@ -3,9 +3,11 @@
 // key_bounds_kernel: per (block, KV head) and channel the smallest and largest
 // key as 8-bit codes, rounded outwards on a power-of-two grid. Reads the keys of
 // the blocks written to once; bound by latency for a step's rows (64 rows of 8
-// heads of 128, BF16: 2.5 us in a graph) and by the instructions per key for a
-// prompt's (4084 rows of 8 x 128, e4m3: 5.0 us; 50021 rows of 8 x 64, 4-bit: 11.6 us,
-// 1.6 TB/s; with every lane encoding eight channels and no keys under way 53).
+// heads of 128, BF16: 2.3 us in a graph) and short prompts (4084 rows of 8 x 128, e4m3:
+// 5.2 us, of which an SM is at work 2600 to 9500 cycles: the look-up of the rows, few
+// blocks a CTA, instructions fetched for the first time), and for long ones by
+// the instructions per key (50021 rows of 8 x 64, 4-bit: 12.1 us, 1.5 TB/s, ALU pipe 64 %
+// while active; with every lane encoding eight channels and no keys under way 53).
 //
 // block_select_kernel: for integers u = rint(q 2^(10 - x)) of the group's
 // queries, P_i and N_i the sums of the positive and negative ones,
@@ -215,7 +217,8 @@ constexpr int kSelPerSm = 4;                 // such CTAs per SM (64 registers a
 constexpr int kSelCluster = 8;               // most CTAs of a cluster
 // Widest table for which one CTA has all keys. One row of 8 KV heads over 2048 blocks
 // 8.4 us (two launches 14.2), 4096 12.4 (14.6), 8192 20.3 (16.0); 64 rows over 4096 87
-// (101), 8192 251 (183).
+// (101), 8192 251 (183). By the table's width, which the host knows, not the contexts:
+// in a wider table 48 rows over 2048 blocks take 54 us, not 39, one row 14.0, not 8.1.
 constexpr int kSelOne = 4096;
 constexpr int kPartWarps = 16;               // warps of a CTA that scores a part of a long context, two per SM
 constexpr int kMergeWarps = 32;              // of one that chooses among the parts' candidates

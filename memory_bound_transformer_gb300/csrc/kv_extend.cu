@@ -10,8 +10,8 @@
 // over, and lays out its share of the rows; the row that begins a block enters it
 // into the table. Where lengths are updated in place the CTAs are one cluster of up
 // to eight, and none writes before all have read. Bound by latency (lengths, sums, a
-// free or table entry per row). In a graph, us: 64 sequences by a token each 2.4;
-// 512 by 65 k rows 4.0 (in place 9.4; one CTA for the sums and tables and a grid
+// free or table entry per row). In a graph, us: 64 sequences by a token each 2.2;
+// 512 by 65 k rows 3.9 (in place 9.4; one CTA for the sums and tables and a grid
 // for the rows 9.1, and 2.5 more of the caller's time).
 #include "common.cuh"
 #include "internal.h"
@@ -21,8 +21,10 @@ namespace mbt {
 namespace {
 
 constexpr int kPlanThreads = 1024;           // most threads of a CTA, a sequence each at a time
-constexpr int kPlanCluster = 8;              // most CTAs in place
-constexpr int kPlanGrid = 128;               // most CTAs otherwise
+// Most CTAs. In a graph, us, with 1, 8, 32, 128 and 256 CTAs: 512 sequences by 32 tokens
+// 14.5, 4.1, 3.8, 3.9, 4.6, by 128 49, 8.8, 4.2, 3.9, 5.7; 16 by 16384 197, 28, 10, 5.1, 8.0.
+constexpr int kPlanGrid = 128;
+constexpr int kPlanCluster = 8;              // in place, portable clusters: 512 by 128 with 1, 2, 4, 8 CTAs 50, 27, 15, 9.4
 constexpr int kPlanRows = 2;                 // rows of a thread at a time (four: 1024 rows 4.9 us against 4.4)
 
 __device__ __forceinline__ int blocks_for(long long tokens) { return (int)((tokens + kBlockTokens - 1) / kBlockTokens); }
@@ -149,7 +151,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvExtendA
 cudaError_t launch_kv_extend(const KvExtendArgs& in, cudaStream_t s) {
   KvExtendArgs a = in;
   void* p[] = {&a};
-  // few sequences and rows: a barrier of few warps
+  // few sequences and rows: a barrier of few warps. In a graph, us, with 128, 512 and 1024
+  // threads: 64 sequences by a token each 2.2, 2.5, 3.2; 512 6.2, 2.9, 3.5; 1000 11.5, 4.7, 4.1.
+  // (1000 rows of one sequence would be quicker with 512: 4.4, 2.7, 3.6.)
   const int most = a.nseq > a.n ? a.nseq : a.n, threads = most <= 128 ? 128 : most <= 512 ? 512 : kPlanThreads;
   a.in_place = a.held == a.ctx_lens || a.free_next == a.free_at;
   int ctas = 1;
