@@ -372,7 +372,7 @@ int op_block_select(int n, const float* q, int nq, int nkv, int d, const int8_t*
  * null block. Cache contents past a row's position never reach it. A query that
  * is not finite makes its row, if that has a token, NaN in that head, a key that
  * is not the rows that attend to it; an infinity or a NaN in V reaches them in its
- * channel. Twice a query's product with a key as the cache holds it (before
+ * channel. Twice sum_i |q_i k_i| over a key as the cache holds it (before
  * k_scale) has to stay in fp32's range, and so has the sum of a BF16 cache's
  * values over the row's tokens. Queries and probabilities enter the products to
  * 2^-24 over a BF16 cache and to 2^-22 over the others, probabilities below 2^-17
